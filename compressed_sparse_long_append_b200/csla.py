@@ -19,12 +19,14 @@ CSLA_GATE_TOKEN, CSLA_GATE_CHANNEL = 0, 1
 CSLA_OP_INDEXER, CSLA_OP_TOPK, CSLA_OP_CSA_ATTEND, CSLA_OP_HCA_ATTEND, CSLA_OP_CSA_DECODE_STEP = 1, 2, 3, 4, 5
 CSLA_OP_INDEXER_TOPK = 6
 CSLA_DEVERR_PAGE, CSLA_DEVERR_INDEX, CSLA_DEVERR_LEN, CSLA_DEVERR_TIMEOUT, CSLA_DEVERR_RANGE = 1, 2, 4, 8, 16
+CSLA_ROPE_ADJACENT, CSLA_ROPE_HALVES = 0, 1
 CSLA_PAGE_TOKENS = 128
 
 EXPORTS = ("csla_compress_append", "csla_indexer_scores", "csla_topk_select", "csla_csa_attend",
            "csla_hca_attend", "csla_workspace_size", "csla_device_error", "csla_strerror", "csla_version",
            "csla_indexer_scores_noalloc", "csla_window_rows", "csla_csa_decode_step", "csla_check_wait_timeout",
-           "csla_cp_record_bytes", "csla_cp_select", "csla_cp_place", "csla_indexer_topk")
+           "csla_cp_record_bytes", "csla_cp_select", "csla_cp_place", "csla_indexer_topk",
+           "csla_kv_append", "csla_kv_attend", "csla_kv_workspace_size")
 CSLA_CP_MAX_RANKS = 64
 CSLA_NOALLOC_INDEXER_SCRATCH_BYTES = 786432
 
@@ -64,6 +66,19 @@ class csla_token_rows(ctypes.Structure):
                 ("offset", ctypes.c_int32)]
 
 
+class csla_kv_cfg(ctypes.Structure):
+    """A dense paged layer's shape (see include/csla.h)."""
+    _fields_ = [("D", ctypes.c_int32), ("HQ", ctypes.c_int32), ("HK", ctypes.c_int32),
+                ("d_rope", ctypes.c_int32), ("rope_pairs", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("rope_theta", ctypes.c_float), ("eps", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
+class csla_kv_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("len", ctypes.c_void_p), ("bt_stride", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("n_slots", ctypes.c_int32)]
+
+
 def queries(q_len, win_rows=None, win_scales=None, win_base=None, n_win_rows=0, one_request=False):
     """csla_queries from tensors (or device addresses); the struct keeps the
     tensors alive for as long as it lives."""
@@ -92,7 +107,7 @@ def _load():
         raise ImportError("libcsla.so not built (%s); run `python "
                           "compressed_sparse_long_append_b200/build.py`" % LIB_PATH)
     L = ctypes.CDLL(LIB_PATH)
-    P, I, Z = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    P, I, Z, L64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_int64
     sig = {
         "csla_compress_append": [P, P, P, P, I, I, P, P, I, P, P, P],
         "csla_window_rows": [P, P, P, I, I, P, P, I, P],
@@ -112,8 +127,11 @@ def _load():
         "csla_indexer_scores_noalloc": [P, P, P, P, I, P, I, P, I, P, I, P, P, I, P],
         "csla_csa_decode_step": [P, P, P, P, I, I, I, P, P, I, P, P, I, P, I, P, P, I, I, P, P, I, P, P, P, I, I,
                                  P, Z, P, Z, P],
+        "csla_kv_append": [P, P, P, I, P, I, P, L64, P, L64, I, P, P],
+        "csla_kv_attend": [P, P, P, I, P, I, I, I, P, I, L64, P, P, P, I, P, Z, P],
+        "csla_kv_workspace_size": [P, I, I, I, I],
     }
-    res = {"csla_workspace_size": ctypes.c_size_t, "csla_strerror": ctypes.c_char_p,
+    res = {"csla_workspace_size": ctypes.c_size_t, "csla_kv_workspace_size": ctypes.c_size_t, "csla_strerror": ctypes.c_char_p,
            "csla_cp_record_bytes": ctypes.c_int32}
     for name, args in sig.items():
         f = getattr(L, name)
@@ -279,3 +297,41 @@ def csla_check_wait_timeout(limit_us, stream=None):
 
 def csla_version():
     return int(_lib.csla_version())
+
+
+_KV_DTYPES = {CSLA_F32: "torch.float32", CSLA_BF16: "torch.bfloat16"}
+
+
+def _kv_tensors(fn, dtype, *tensors):
+    """Tensors of a dense layer's call (addresses pass unchecked): of the given dtype code, on the current device."""
+    import torch
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            continue
+        if str(t.dtype) != _KV_DTYPES.get(dtype):
+            raise ValueError("%s: a %s tensor where dtype code %s was given" % (fn, t.dtype, dtype))
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError("%s: a tensor on %s, not on the current device" % (fn, t.device))
+
+
+def csla_kv_append(cfg, kv, slots, B, q_start, N, k_new, k_stride, v_new, v_stride, dtype, gamma_k=None, stream=None):
+    """Keys (normed with gamma_k, rotated) and values of N new tokens into a dense layer's pages.  q_start: int32
+    [B+1] row offsets, or None when every request has N / B new tokens; strides in elements between tokens."""
+    _kv_tensors("csla_kv_append", dtype, k_new, v_new)
+    return _check("csla_kv_append", _lib.csla_kv_append(
+        _ref(cfg), _ref(kv), _ptr(slots), B, _ptr(q_start), N, _ptr(k_new), k_stride, _ptr(v_new), v_stride, dtype,
+        _ptr(gamma_k), _stream(stream)))
+
+
+def csla_kv_attend(cfg, kv, slots, B, q_start, N, max_new, max_len, q, q_dtype, q_stride, sink, gamma_q, out,
+                   out_dtype, workspace, workspace_bytes, stream=None):
+    """Attention of the N new tokens over a dense layer's pages (their K and V appended before)."""
+    _kv_tensors("csla_kv_attend", q_dtype, q)
+    _kv_tensors("csla_kv_attend", out_dtype, out)
+    return _check("csla_kv_attend", _lib.csla_kv_attend(
+        _ref(cfg), _ref(kv), _ptr(slots), B, _ptr(q_start), N, max_new, max_len, _ptr(q), q_dtype, q_stride,
+        _ptr(sink), _ptr(gamma_q), _ptr(out), out_dtype, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def csla_kv_workspace_size(cfg, B, N, max_new, max_len):
+    return int(_lib.csla_kv_workspace_size(_ref(cfg), B, N, max_new, max_len))

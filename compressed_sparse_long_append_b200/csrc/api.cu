@@ -678,4 +678,84 @@ int csla_cp_place(const csla_cfg *cfg, const csla_state *st, const csla_cache *c
     return cuda_status(launch_cp_move(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// ---- dense paged layers
+
+static int check_kv(const csla_kv_cfg *c, const csla_kv_cache *kv) {
+    if (!c) return CSLA_ERR_ARG;
+    if ((c->D != 64 && c->D != 128) || c->HK < 1 || c->HQ < 1 || c->HQ > 1024 || c->HQ % c->HK ||
+        c->HQ / c->HK > 128 || c->d_rope < 0 || c->d_rope > c->D || c->d_rope % 16 ||
+        (c->rope_pairs != CSLA_ROPE_ADJACENT && c->rope_pairs != CSLA_ROPE_HALVES))
+        return CSLA_ERR_UNSUPPORTED;
+    if (!(c->eps >= 0.f) || !(c->rope_theta > 0.f) || c->window < 0 || !(c->scale >= 0.f) || isinf(c->scale))
+        return CSLA_ERR_ARG;
+    if (!kv) return CSLA_ERR_ARG;
+    if (!kv->k || !kv->v || !kv->block_table || !kv->len || kv->bt_stride < 1 || kv->n_pages < 1 || kv->n_slots < 1 ||
+        !aligned16(kv->k) || !aligned16(kv->v))
+        return CSLA_ERR_ARG;
+    return CSLA_OK;
+}
+
+static int kv_batch(const csla_kv_cache *kv, const int32_t *slots, int32_t B, const int32_t *q_start, int32_t N,
+                    KvBatch *bt) {
+    if (!slots || B < 1 || N < 1 || N > (1 << 30)) return CSLA_ERR_ARG;
+    if (!q_start && N % B) return CSLA_ERR_ARG;
+    bt->slots = slots; bt->q_start = q_start; bt->len = kv->len; bt->block_table = kv->block_table;
+    bt->B = B; bt->N = N; bt->T = q_start ? 0 : N / B;
+    bt->bt_stride = kv->bt_stride; bt->n_pages = kv->n_pages; bt->n_slots = kv->n_slots;
+    return CSLA_OK;
+}
+
+// Rows of `width` elements, `stride` elements apart, 16-byte aligned throughout.
+static bool kv_rows_ok(const void *p, int64_t stride, int64_t width, int32_t dtype) {
+    if (!p || !aligned16(p) || (dtype != CSLA_F32 && dtype != CSLA_BF16)) return false;
+    return stride >= width && stride <= (int64_t(1) << 40) && (stride * (dtype == CSLA_BF16 ? 2 : 4)) % 16 == 0;
+}
+
+int csla_kv_append(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_t *slots, int32_t B,
+                   const int32_t *q_start, int32_t N, const void *k_new, int64_t k_stride, const void *v_new,
+                   int64_t v_stride, int32_t dtype, const float *gamma_k, csla_stream_t stream) {
+    int rc = check_kv(cfg, kv);
+    if (rc) return rc;
+    KvAppendArgs a{};
+    rc = kv_batch(kv, slots, B, q_start, N, &a.bt);
+    if (rc) return rc;
+    const int64_t width = (int64_t)cfg->HK * cfg->D;
+    if (!kv_rows_ok(k_new, k_stride, width, dtype) || !kv_rows_ok(v_new, v_stride, width, dtype)) return CSLA_ERR_ARG;
+    a.D = cfg->D; a.HK = cfg->HK; a.d_rope = cfg->d_rope; a.pairs = cfg->rope_pairs; a.eps = cfg->eps;
+    a.freq = kv_freq(cfg->rope_theta, cfg->d_rope);
+    a.k_new = k_new; a.v_new = v_new; a.k_stride = k_stride; a.v_stride = v_stride; a.gamma_k = gamma_k;
+    a.k = static_cast<uint16_t *>(kv->k); a.v = static_cast<uint16_t *>(kv->v);
+    return cuda_status(launch_kv_append(a, dtype == CSLA_BF16, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t csla_kv_workspace_size(const csla_kv_cfg *cfg, int32_t B, int32_t N, int32_t max_new, int32_t max_len) {
+    if (!cfg || B < 1 || N < 1 || max_new < 1 || max_len < 1) return 0;
+    return 0;
+}
+
+int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_t *slots, int32_t B,
+                   const int32_t *q_start, int32_t N, int32_t max_new, int32_t max_len, const void *q,
+                   int32_t q_dtype, int64_t q_stride, const float *sink, const float *gamma_q, void *out,
+                   int32_t out_dtype, void *workspace, size_t workspace_bytes, csla_stream_t stream) {
+    int rc = check_kv(cfg, kv);
+    if (rc) return rc;
+    KvAttendArgs a{};
+    rc = kv_batch(kv, slots, B, q_start, N, &a.bt);
+    if (rc) return rc;
+    if (!kv_rows_ok(q, q_stride, (int64_t)cfg->HQ * cfg->D, q_dtype)) return CSLA_ERR_ARG;
+    if (!out || !aligned16(out) || (out_dtype != CSLA_F32 && out_dtype != CSLA_BF16)) return CSLA_ERR_ARG;
+    if (max_new < 1 || max_len < 1 || (!q_start && a.bt.T > max_new)) return CSLA_ERR_ARG;
+    if ((long long)kv->n_pages * cfg->HK * CSLA_PAGE_TOKENS >= (1ll << 31)) return CSLA_ERR_UNSUPPORTED;
+    const size_t need = csla_kv_workspace_size(cfg, B, N, max_new, max_len);
+    if (workspace_bytes < need || (need && (!workspace || !aligned16(workspace)))) return CSLA_ERR_ARG;
+    a.D = cfg->D; a.HQ = cfg->HQ; a.HK = cfg->HK; a.d_rope = cfg->d_rope; a.pairs = cfg->rope_pairs;
+    a.window = cfg->window; a.max_new = max_new; a.max_len = max_len; a.eps = cfg->eps;
+    a.scale = cfg->scale > 0.f ? cfg->scale : 1.0f / sqrtf((float)cfg->D);
+    a.freq = kv_freq(cfg->rope_theta, cfg->d_rope);
+    a.q = q; a.q_stride = q_stride; a.sink = sink; a.gamma_q = gamma_q;
+    a.k = static_cast<const uint16_t *>(kv->k); a.v = static_cast<const uint16_t *>(kv->v); a.out = out;
+    return cuda_status(launch_kv_attend(a, q_dtype == CSLA_BF16, out_dtype == CSLA_BF16,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

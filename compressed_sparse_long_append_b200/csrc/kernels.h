@@ -252,4 +252,51 @@ __host__ __device__ inline int attend_max_chunks(long long n) {
     return (int)(c < 1 ? 1 : (c > 32 ? 32 : c));
 }
 
+// ---------------------------------------------------------------- dense paged layers
+// RoPE inverse frequencies of a dense layer (d_rope up to 128).
+struct KvFreq {
+    double inv[64];
+};
+inline KvFreq kv_freq(float theta, int d_rope) {
+    KvFreq f{};
+    for (int i = 0; i < d_rope / 2 && i < 64; ++i) f.inv[i] = pow((double)theta, -(2.0 * i) / (double)d_rope);
+    return f;
+}
+
+// The ragged batch of a dense layer's call and its paged cache.
+struct KvBatch {
+    const int32_t *slots;
+    const int32_t *q_start;   // [B+1] or null: T new tokens each
+    const int32_t *len;
+    const int32_t *block_table;
+    int B, N, T;
+    int bt_stride, n_pages, n_slots;
+};
+
+struct KvAppendArgs {
+    KvBatch bt;
+    int D, HK, d_rope, pairs;
+    float eps;
+    KvFreq freq;
+    const void *k_new, *v_new;
+    long long k_stride, v_stride;   // elements between tokens
+    const float *gamma_k;           // null: no norm
+    uint16_t *k, *v;                // bf16 pages
+};
+cudaError_t launch_kv_append(const KvAppendArgs &a, bool bf16, cudaStream_t stream);
+
+struct KvAttendArgs {
+    KvBatch bt;
+    int D, HQ, HK, d_rope, pairs, window;
+    int max_new, max_len;
+    float eps, scale;
+    KvFreq freq;
+    const void *q;
+    long long q_stride;
+    const float *sink, *gamma_q;    // null: none
+    const uint16_t *k, *v;
+    void *out;
+};
+cudaError_t launch_kv_attend(const KvAttendArgs &a, bool q_bf16, bool out_bf16, cudaStream_t stream);
+
 }  // namespace csla

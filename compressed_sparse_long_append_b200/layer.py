@@ -101,6 +101,59 @@ class LayerBuffers:
         return out
 
 
+@dataclass(frozen=True)
+class DenseShape:
+    """An uncompressed layer: grouped KV heads in bf16 pages, full or sliding-window attention."""
+    D: int = 128           # 64 or 128
+    HQ: int = 64           # query heads
+    HK: int = 8            # KV heads
+    d_rope: int = 64       # rotated dims, the last ones
+    rope_pairs: int = C.CSLA_ROPE_ADJACENT
+    window: int = 0        # 0: every token before
+    theta: float = 10000.0
+    eps: float = 1e-6
+    scale: float = 0.0     # 0: 1/sqrt(D)
+
+    def cfg(self):
+        return C.csla_kv_cfg(self.D, self.HQ, self.HK, self.d_rope, self.rope_pairs, self.window, self.theta,
+                             self.eps, self.scale)
+
+
+class DenseBuffers:
+    """K and V pages of a dense layer for `n_slots` requests.  `block_table`
+    as in LayerBuffers; `length` ([n_slots] int32 on the device) is used as
+    given instead of one of the layer's own (the dense layers of one stack
+    share one; the caller advances it by a step's new tokens before the
+    step's csla_kv_append)."""
+
+    def __init__(self, shape: DenseShape, n_slots: int, n_pages: int, bt_stride: int, device="cuda",
+                 block_table=None, length=None):
+        s = shape
+        self.shape = s
+        self.device = torch.device(device)
+        dev = self.device
+        pool = (n_pages, s.HK, C.CSLA_PAGE_TOKENS, s.D)
+        self.k = torch.zeros(pool, dtype=torch.bfloat16, device=dev)
+        self.v = torch.zeros(pool, dtype=torch.bfloat16, device=dev)
+        if block_table is None:
+            block_table = torch.full((n_slots, bt_stride), -1, dtype=torch.int32, device=dev)
+        if length is None:
+            length = torch.zeros((n_slots,), dtype=torch.int32, device=dev)
+        for t, want, name in ((block_table, (n_slots, bt_stride), "block_table"), (length, (n_slots,), "length")):
+            if t.dtype != torch.int32 or tuple(t.shape) != want or not t.is_contiguous() or t.device.type != dev.type:
+                raise ValueError("%s must be a contiguous %s int32 tensor on %s" % (name, list(want), dev))
+        self.block_table, self.len = block_table, length
+        self.n_slots, self.n_pages, self.bt_stride = n_slots, n_pages, bt_stride
+        self._cfg = s.cfg()
+
+    def cfg(self):
+        return self._cfg
+
+    def cache(self):
+        return C.csla_kv_cache(self.k.data_ptr(), self.v.data_ptr(), self.block_table.data_ptr(), self.len.data_ptr(),
+                               self.bt_stride, self.n_pages, self.n_slots)
+
+
 class LayerStack:
     """The attention layers of one model over one block table.  A page is
     128 raw tokens of a request in every layer (32 CSA entries or 1 HCA
@@ -108,12 +161,17 @@ class LayerStack:
     pool: one allocation covers the whole stack.  Every layer keeps its own
     pools, window ring, tail and length (each layer appends its own
     compressed KV).  `shapes[i]` is layer i's shape, e.g. CSA and HCA
-    layers interleaved."""
+    layers interleaved.  A DenseShape among them makes a dense layer
+    (128 rows of K and V per page and KV head); the stack's dense layers
+    share one length array, `dense_len`."""
 
     def __init__(self, shapes, n_slots: int, n_pages: int, bt_stride: int, device="cuda"):
         self.device = torch.device(device)
         self.block_table = torch.full((n_slots, bt_stride), -1, dtype=torch.int32, device=self.device)
-        self.layers = [LayerBuffers(s, n_slots, n_pages, bt_stride, device, block_table=self.block_table)
+        self.dense_len = torch.zeros((n_slots,), dtype=torch.int32, device=self.device)
+        self.layers = [DenseBuffers(s, n_slots, n_pages, bt_stride, device, self.block_table, self.dense_len)
+                       if isinstance(s, DenseShape) else
+                       LayerBuffers(s, n_slots, n_pages, bt_stride, device, block_table=self.block_table)
                        for s in shapes]
         self.n_slots, self.n_pages, self.bt_stride = n_slots, n_pages, bt_stride
 

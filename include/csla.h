@@ -484,6 +484,114 @@ int csla_cp_place(const csla_cfg *cfg, const csla_state *st, const csla_cache *c
                   const uint8_t *recs, int32_t R, int32_t E_max, const int32_t *b_lo, const int32_t *n,
                   csla_stream_t stream);
 
+/*
+ * Dense paged layers -- the uncompressed layers of a stack (full or
+ * sliding-window attention between CSA and HCA layers), over the same
+ * 128-token pages and block table as the compressed ones.
+ *
+ *   k, v  bf16 [n_pages][HK][CSLA_PAGE_TOKENS][D]: token p of slot s is row
+ *     p % 128 of page block_table[s][p / 128], one row per KV head.
+ *   len  int32 [n_slots]: the context length of each slot, the call's new
+ *     tokens included.  The caller advances it, once per step for every
+ *     dense layer that shares it (csla_state.len after a
+ *     csla_compress_append of the same tokens serves too); neither call
+ *     writes it, so both may be repeated.
+ *
+ * A call covers B requests (slots as above) and N new tokens in one ragged
+ * row block: request b owns rows q_start[b] .. q_start[b+1]-1 (T_b of them,
+ * 0 allowed: its slot is not looked at), its i-th new token at position
+ * p = len[slots[b]] - T_b + i; rows from q_start[B] on belong to nobody and
+ * are left alone (N may be a capacity).
+ * q_start NULL: every request has N / B new tokens (N divisible by B).
+ * Rows are `stride` elements apart (a slice of a fused projection is fine),
+ * heads contiguous inside a row; base addresses 16-byte aligned, strides
+ * multiples of 16 bytes.
+ *
+ * Rotation R(p) of the last d_rope dims: pair i turns by the angle
+ * p * rope_theta^(-2i/d_rope); CSLA_ROPE_ADJACENT pairs dims (2i, 2i+1),
+ * CSLA_ROPE_HALVES dims (i, i + d_rope/2), counted from D - d_rope.
+ *
+ * Device-detected errors: a slot outside [0, n_slots), or q_start not
+ * ascending within [0, N] (CSLA_DEVERR_INDEX), or len outside
+ * [T_b, 128*bt_stride], or (attention) len above max_len or T_b above
+ * max_new (CSLA_DEVERR_LEN): the request is skipped, its outputs untouched.  A page
+ * id outside the pool (CSLA_DEVERR_PAGE): the append skips the tokens in
+ * it, the attention treats them as masked.
+ */
+enum { CSLA_ROPE_ADJACENT = 0, CSLA_ROPE_HALVES = 1 };
+
+/* Supported: D in {64, 128}; HQ a multiple of HK, HQ / HK <= 128, HQ <= 1024;
+ * d_rope a multiple of 16, 0..D. */
+typedef struct csla_kv_cfg {
+    int32_t D;           /* head dim */
+    int32_t HQ;          /* query heads; head h reads KV head h / (HQ / HK) */
+    int32_t HK;          /* KV heads */
+    int32_t d_rope;      /* rotated dims, the last ones; 0: none */
+    int32_t rope_pairs;  /* CSLA_ROPE_ADJACENT or CSLA_ROPE_HALVES */
+    int32_t window;      /* a token sees itself and the window-1 before it; 0: everything before it */
+    float rope_theta;    /* RoPE base */
+    float eps;           /* RMSNorm epsilon */
+    float scale;         /* score scale; 0: 1/sqrt(D) */
+} csla_kv_cfg;
+
+typedef struct csla_kv_cache {
+    void *k;                     /* bf16 [n_pages][HK][128][D], 16-byte aligned */
+    void *v;
+    const int32_t *block_table;  /* [n_slots][bt_stride] */
+    const int32_t *len;          /* [n_slots] */
+    int32_t bt_stride;
+    int32_t n_pages;
+    int32_t n_slots;
+} csla_kv_cache;
+
+/*
+ * csla_kv_append -- keys and values of the new tokens into their pages:
+ *   K row = bf16(R(p) (k / sqrt(mean(k^2) + eps) * gamma_k))  per KV head
+ *           (gamma_k NULL: no norm, bf16(R(p) k)),
+ *   V row = bf16(v).
+ *   k_new, v_new [N][HK][D] dtype (CSLA_F32 or CSLA_BF16), rows k_stride /
+ *   v_stride elements apart; gamma_k f32 [D] or NULL.
+ * Rows are rounded to bf16 once.  Slots must be distinct.  Nothing but the
+ * new tokens' rows is written.  Errors: CSLA_ERR_ARG (null pointers, sizes,
+ * strides, alignment); CSLA_ERR_UNSUPPORTED (shapes); device bits INDEX,
+ * LEN, PAGE.
+ */
+int csla_kv_append(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_t *slots, int32_t B,
+                   const int32_t *q_start, int32_t N, const void *k_new, int64_t k_stride,
+                   const void *v_new, int64_t v_stride, int32_t dtype, const float *gamma_k,
+                   csla_stream_t stream);
+
+/*
+ * csla_kv_attend -- attention of the new tokens over the paged cache (call
+ * csla_kv_append with the same tokens first).  For the token at position p
+ * and query head h (KV head h / (HQ / HK)):
+ *   qh = R(p) (q / sqrt(mean(q^2) + eps) * gamma_q)   (gamma_q NULL: no norm)
+ *   s_j = scale * <qh, K_j>,  j = max(0, p - window + 1) .. p
+ *   o = sum_j e^{s_j} V_j / (e^{sink[h]} + sum_j e^{s_j})   (sink NULL: no sink term)
+ * From one token per request (decode) to whole prompts, mixed in one call.
+ * A row whose tokens all lie in unmapped pages is written as zeros.  Cache
+ * rows that no new token of the request sees (positions >= len, or before
+ * every window) are never used, whatever they hold, and pages of such rows
+ * need not be mapped.  V of a token that some new tokens see and others do
+ * not must be finite for the others too (it enters with weight zero).
+ *   q [N][HQ][D] q_dtype, rows q_stride elements apart; sink f32 [HQ] or
+ *   NULL; gamma_q f32 [D] or NULL; out [N][HQ][D] out_dtype, 16-byte aligned.
+ *   max_new >= every T_b, max_len >= every len (host bounds).
+ * Batch invariant: how a request is split and joined is a function of its
+ * own T_b and len and of the layer's shape.
+ * workspace: csla_kv_workspace_size(cfg, B, N, max_new, max_len) bytes,
+ * 16-byte aligned, not shared with a call that may run at the same time.
+ * Errors: CSLA_ERR_ARG, CSLA_ERR_UNSUPPORTED (shapes; n_pages*HK*128 >=
+ * 2^31); device bits INDEX, LEN, PAGE.
+ */
+int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_t *slots, int32_t B,
+                   const int32_t *q_start, int32_t N, int32_t max_new, int32_t max_len, const void *q,
+                   int32_t q_dtype, int64_t q_stride, const float *sink, const float *gamma_q, void *out,
+                   int32_t out_dtype, void *workspace, size_t workspace_bytes, csla_stream_t stream);
+
+/* Scratch bytes of csla_kv_attend (0 for arguments it would refuse). */
+size_t csla_kv_workspace_size(const csla_kv_cfg *cfg, int32_t B, int32_t N, int32_t max_new, int32_t max_len);
+
 /* Static text for a status code. */
 const char *csla_strerror(int status);
 
@@ -504,7 +612,8 @@ int csla_version(void);
  * storing how many in *count; csla_timeline_clear synchronises and empties
  * the buffer.  Kernel ids: 1 compress, 2 tail update, 3 index-query
  * projection, 4 wide projection, 5 indexer, 6 top-k, (7 unused),
- * 8 attention, 9 chunk combine.
+ * 8 attention, 9 chunk combine, 10 K/V append, 11 paged attention,
+ * 12 paged attention's join.
  */
 #ifdef CSLA_TIMELINE
 int csla_timeline_read(void *records, size_t bytes, uint32_t *count);
