@@ -680,7 +680,7 @@ int csla_cp_place(const csla_cfg *cfg, const csla_state *st, const csla_cache *c
 
 // ---- dense paged layers
 
-static int check_kv(const csla_kv_cfg *c, const csla_kv_cache *kv) {
+static int check_kv_cfg(const csla_kv_cfg *c) {
     if (!c) return CSLA_ERR_ARG;
     if ((c->D != 64 && c->D != 128) || c->HK < 1 || c->HQ < 1 || c->HQ > 1024 || c->HQ % c->HK ||
         c->HQ / c->HK > 128 || c->d_rope < 0 || c->d_rope > c->D || c->d_rope % 16 ||
@@ -688,6 +688,12 @@ static int check_kv(const csla_kv_cfg *c, const csla_kv_cache *kv) {
         return CSLA_ERR_UNSUPPORTED;
     if (!(c->eps >= 0.f) || !(c->rope_theta > 0.f) || c->window < 0 || !(c->scale >= 0.f) || isinf(c->scale))
         return CSLA_ERR_ARG;
+    return CSLA_OK;
+}
+
+static int check_kv(const csla_kv_cfg *c, const csla_kv_cache *kv) {
+    const int rc = check_kv_cfg(c);
+    if (rc) return rc;
     if (!kv) return CSLA_ERR_ARG;
     if (!kv->k || !kv->v || !kv->block_table || !kv->len || kv->bt_stride < 1 || kv->n_pages < 1 || kv->n_slots < 1 ||
         !aligned16(kv->k) || !aligned16(kv->v))
@@ -697,7 +703,7 @@ static int check_kv(const csla_kv_cfg *c, const csla_kv_cache *kv) {
 
 static int kv_batch(const csla_kv_cache *kv, const int32_t *slots, int32_t B, const int32_t *q_start, int32_t N,
                     KvBatch *bt) {
-    if (!slots || B < 1 || N < 1 || N > (1 << 30)) return CSLA_ERR_ARG;
+    if (!slots || B < 1 || B > 65535 || N < 1 || N > (1 << 30)) return CSLA_ERR_ARG;
     if (!q_start && N % B) return CSLA_ERR_ARG;
     bt->slots = slots; bt->q_start = q_start; bt->len = kv->len; bt->block_table = kv->block_table;
     bt->B = B; bt->N = N; bt->T = q_start ? 0 : N / B;
@@ -728,9 +734,53 @@ int csla_kv_append(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
     return cuda_status(launch_kv_append(a, dtype == CSLA_BF16, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// Key tiles that a row tile may have, at most.
+static long long kv_most_tiles(const csla_kv_cfg *c, int max_new, int max_len) {
+    long long nt = ((long long)max_len + CSLA_PAGE_TOKENS - 1) / CSLA_PAGE_TOKENS;
+    if (c->window > 0) {
+        const long long span = max_new < 257 ? max_new : 257;   // new tokens of a row tile
+        const long long w = ((long long)c->window + span) / CSLA_PAGE_TOKENS + 2;
+        nt = w < nt ? w : nt;
+    }
+    return nt;
+}
+
+// Partial rows that a batch within these bounds may need (kv_plan: a chunk
+// is at least kKvMin tiles and at least a 1/kKvUnits share of a request's
+// row tiles and heads).
+static long long kv_most_part_rows(const csla_kv_cfg *c, int B, int N, int max_new, int max_len) {
+    const long long G = c->HQ / c->HK, HK = c->HK, nt = kv_most_tiles(c, max_new, max_len);
+    auto least = [](long long x, long long y) { return x < y ? x : y; };
+    auto parts = [&](long long min_tiles, long long units) {
+        return least((nt + min_tiles - 1) / min_tiles, (units + HK - 1) / HK);
+    };
+    if (nt <= 1) return 0;
+    // requests of one row tile
+    const long long t1 = least(max_new, 128 / G);
+    long long rows = least(N, B * t1) * c->HQ * 2 * parts(kKvMinSingle, kKvUnitsSingle);
+    if (max_new * G > 128 && nt > kKvMinPaired) {
+        // each has chunks * 256 * R * HK rows at most, R * HK < units and chunks <= units / (R * HK) + 1
+        const long long each = 256ll * 2 * kKvUnitsPaired, n = least(B, N * G / 129);
+        rows += least(n * each, (long long)N * c->HQ * parts(kKvMinPaired, kKvUnitsPaired));
+    }
+    return rows;
+}
+
+struct KvWorkspace {
+    size_t ml, o, total;
+};
+static KvWorkspace kv_workspace(const csla_kv_cfg *c, int B, long long rows) {
+    KvWorkspace w{0, 0, 0};
+    if (rows == 0) return w;
+    w.ml = up16((size_t)B * 8);
+    w.o = w.ml + up16((size_t)rows * 8);
+    w.total = w.o + (size_t)rows * c->D * 4;
+    return w;
+}
+
 size_t csla_kv_workspace_size(const csla_kv_cfg *cfg, int32_t B, int32_t N, int32_t max_new, int32_t max_len) {
-    if (!cfg || B < 1 || N < 1 || max_new < 1 || max_len < 1) return 0;
-    return 0;
+    if (check_kv_cfg(cfg) != CSLA_OK || B < 1 || N < 1 || max_new < 1 || max_len < 1) return 0;
+    return kv_workspace(cfg, B, kv_most_part_rows(cfg, B, N, max_new, max_len)).total;
 }
 
 int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_t *slots, int32_t B,
@@ -745,7 +795,8 @@ int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
     if (!kv_rows_ok(q, q_stride, (int64_t)cfg->HQ * cfg->D, q_dtype)) return CSLA_ERR_ARG;
     if (!out || !aligned16(out) || (out_dtype != CSLA_F32 && out_dtype != CSLA_BF16)) return CSLA_ERR_ARG;
     if (max_new < 1 || max_len < 1 || (!q_start && a.bt.T > max_new)) return CSLA_ERR_ARG;
-    if ((long long)kv->n_pages * cfg->HK * CSLA_PAGE_TOKENS >= (1ll << 31)) return CSLA_ERR_UNSUPPORTED;
+    if ((long long)kv->n_pages * cfg->HK * CSLA_PAGE_TOKENS >= (1ll << 31) || (long long)N * cfg->HQ >= (1ll << 31))
+        return CSLA_ERR_UNSUPPORTED;
     const size_t need = csla_kv_workspace_size(cfg, B, N, max_new, max_len);
     if (workspace_bytes < need || (need && (!workspace || !aligned16(workspace)))) return CSLA_ERR_ARG;
     a.D = cfg->D; a.HQ = cfg->HQ; a.HK = cfg->HK; a.d_rope = cfg->d_rope; a.pairs = cfg->rope_pairs;
@@ -753,9 +804,27 @@ int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
     a.scale = cfg->scale > 0.f ? cfg->scale : 1.0f / sqrtf((float)cfg->D);
     a.freq = kv_freq(cfg->rope_theta, cfg->d_rope);
     a.q = q; a.q_stride = q_stride; a.sink = sink; a.gamma_q = gamma_q;
-    a.k = static_cast<const uint16_t *>(kv->k); a.v = static_cast<const uint16_t *>(kv->v); a.out = out;
-    return cuda_status(launch_kv_attend(a, q_dtype == CSLA_BF16, out_dtype == CSLA_BF16,
-                                        reinterpret_cast<cudaStream_t>(stream)));
+    a.out = out;
+    const long long rows = kv_most_part_rows(cfg, B, N, max_new, max_len);
+    const KvWorkspace w = kv_workspace(cfg, B, rows);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    if (rows) {
+        a.part_base = reinterpret_cast<long long *>(ws);
+        a.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
+        a.part_o = reinterpret_cast<float *>(ws + w.o);
+    }
+    // one box = 64 dims of a page's 128 rows
+    CUtensorMap km, vm;
+    const uint64_t cache_rows = (uint64_t)kv->n_pages * cfg->HK * CSLA_PAGE_TOKENS;
+    if (!encode_bf16_2d(&km, kv->k, cfg->D, cache_rows, CSLA_PAGE_TOKENS) ||
+        !encode_bf16_2d(&vm, kv->v, cfg->D, cache_rows, CSLA_PAGE_TOKENS))
+        return CSLA_ERR_CUDA;
+    // items at most: the grid of a small call
+    const int G = cfg->HQ / cfg->HK;
+    const long long nt = kv_most_tiles(cfg, max_new, max_len);
+    const long long items = ((long long)N * G / 256 + B) * cfg->HK * ((nt + kKvMinSingle - 1) / kKvMinSingle);
+    return cuda_status(launch_kv_attend(a, q_dtype == CSLA_BF16, out_dtype == CSLA_BF16, km, vm, num_sms_current(),
+                                        items, rows > 0, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -258,8 +258,13 @@ struct KvFreq {
     double inv[64];
 };
 inline KvFreq kv_freq(float theta, int d_rope) {
+    // powers of one ratio in extended precision (64 products: below 2^-57
+    // relative), a fraction of what 64 calls of pow cost the host
     KvFreq f{};
-    for (int i = 0; i < d_rope / 2 && i < 64; ++i) f.inv[i] = pow((double)theta, -(2.0 * i) / (double)d_rope);
+    if (d_rope <= 0) return f;
+    const long double ratio = expl(-2.0L / d_rope * logl((long double)theta));
+    long double x = 1.0L;
+    for (int i = 0; i < d_rope / 2 && i < 64; ++i, x *= ratio) f.inv[i] = (double)x;
     return f;
 }
 
@@ -294,9 +299,90 @@ struct KvAttendArgs {
     const void *q;
     long long q_stride;
     const float *sink, *gamma_q;    // null: none
-    const uint16_t *k, *v;
     void *out;
+    // workspace: first partial row of each request [B], (m, l) and O of the partial rows
+    long long *part_base;
+    float2 *part_ml;
+    float *part_o;
 };
-cudaError_t launch_kv_attend(const KvAttendArgs &a, bool q_bf16, bool out_bf16, cudaStream_t stream);
+
+// How the attention cuts a request of T new tokens (context L): a function of
+// T, L and the layer alone.  rows = T*G rows per KV head.  At most 128 rows:
+// one row tile (R = 1) whose two streams take key tiles in turn.  More: R row
+// tiles of 256.  Keys are cut into chunks of c tiles, nch at most per row
+// tile, so that a request of few row tiles still fills the SMs.
+struct KvPlan {
+    int rows, R, paired, c, nch, T, G, heads_inside;
+};
+constexpr int kKvUnitsSingle = 296;   // items a long request of one row tile is cut into (all heads)
+constexpr int kKvUnitsPaired = 148;
+constexpr int kKvMinSingle = 4;       // tiles per chunk at least
+constexpr int kKvMinPaired = 8;
+
+// Key tiles of row tile i: [lo, hi); of its two halves: first half [lo, hi0), second [lo1, hi).
+// [k_lo, k_hi): the positions that some row sees.
+struct KvRange {
+    int lo, hi, hi0, lo1, k_lo, k_hi;
+};
+__host__ __device__ inline KvRange kv_range(const KvPlan &p, int pos0, int i, int window) {
+    KvRange g;
+    const int r0 = p.paired ? 256 * i : 0, rows_left = p.rows - r0;
+    const int n = rows_left < 256 ? rows_left : 256;
+    const int first = r0 / p.G, last = (r0 + n - 1) / p.G;
+    g.k_lo = window > 0 && pos0 + first - window + 1 > 0 ? pos0 + first - window + 1 : 0;
+    g.k_hi = pos0 + last + 1;
+    g.lo = g.k_lo / CSLA_PAGE_TOKENS;
+    g.hi = (g.k_hi + CSLA_PAGE_TOKENS - 1) / CSLA_PAGE_TOKENS;
+    g.hi0 = g.hi;
+    g.lo1 = g.lo;
+    if (p.paired) {
+        if (n <= 128) {
+            g.lo1 = g.hi;
+        } else {
+            g.hi0 = (pos0 + (r0 + 127) / p.G) / CSLA_PAGE_TOKENS + 1;
+            const int lo = window > 0 ? pos0 + (r0 + 128) / p.G - window + 1 : 0;
+            g.lo1 = lo > 0 ? lo / CSLA_PAGE_TOKENS : 0;
+        }
+    }
+    return g;
+}
+__host__ __device__ inline KvPlan kv_plan(int T, int L, int G, int HK, int window, int D) {
+    KvPlan p;
+    p.T = T;
+    p.G = G;
+    p.rows = T * G;
+    p.paired = p.rows > 128;
+    p.R = p.paired ? (p.rows + 255) / 256 : 1;
+    // key tiles of the longest row tile (with a window: an upper bound)
+    long long nt = (L + CSLA_PAGE_TOKENS - 1) / CSLA_PAGE_TOKENS;
+    if (window > 0) {
+        const long long w = ((long long)window + (p.paired ? 256 / G + 1 : T) + CSLA_PAGE_TOKENS - 2) / CSLA_PAGE_TOKENS + 1;
+        nt = w < nt ? w : nt;
+    }
+    const long long units = p.paired ? kKvUnitsPaired : kKvUnitsSingle;
+    long long c = (nt * HK * p.R + units - 1) / units;
+    const int least = p.paired ? kKvMinPaired : kKvMinSingle;
+    if (c < least) c = least;
+    if (c > nt) c = nt;
+    p.c = (int)c;
+    p.nch = (int)((nt + c - 1) / c);
+    // K and V of all heads below half of L2: heads in turn, longest row tiles first
+    p.heads_inside = (long long)L * HK * D * 4 <= (64ll << 20);
+    return p;
+}
+// Partials of a row of row tile g: 1 means it is written out at once.
+__host__ __device__ inline int kv_parts(const KvPlan &p, const KvRange &g) {
+    const int nt = g.hi - g.lo;
+    if (p.paired) return (nt + p.c - 1) / p.c;
+    return nt == 1 ? 1 : 2 * ((nt + p.c - 1) / p.c);
+}
+// Partial rows that a request may need.
+__host__ __device__ inline long long kv_part_rows(const KvPlan &p, int T, int HQ) {
+    const long long parts = p.paired ? p.nch : 2ll * p.nch;
+    if (p.paired ? p.nch == 1 : p.c == 1) return 0;
+    return parts * T * HQ;
+}
+cudaError_t launch_kv_attend(const KvAttendArgs &a, bool q_bf16, bool out_bf16, const CUtensorMap &km,
+                             const CUtensorMap &vm, int num_sms, long long items, bool join, cudaStream_t stream);
 
 }  // namespace csla

@@ -3,138 +3,871 @@
 //
 //   s_j = scale <R(p) norm(q), K_j>,  o = sum_j e^{s_j} V_j / (e^{sink} + sum_j e^{s_j})
 //
-// One warp per (token, query head): it walks the visible tokens, four at a
-// time, with a running maximum and sum in fp32.
+// Rows.  The T new tokens of a request and the G query heads of one KV head
+// make T*G rows of one matrix (row = token * G + head): they share every key.
+// A page (128 tokens of one KV head) is one tile of keys and values.
+//
+// Work.  A CTA works on items.  A request of at most 128 rows per KV head
+// (decode, a few tokens) is one row tile, its keys cut into chunks of tiles;
+// one item is a chunk, and the CTA's two streams take its tiles in turn.  A
+// request of more rows is cut into row tiles of 256; one item is such a tile
+// (and a chunk of its keys when there are few row tiles), each stream
+// takes 128 of the rows and both share every key tile.  How a request is cut depends
+// on its own T and len and the layer's shape alone (kv_plan), so its
+// results do not depend on the batch.  Rows whose keys were cut are left as
+// partial (m, l, O) in the workspace and joined, in order, by kv_join_kernel.
+//
+// Roles (one persistent CTA per SM, 16 warps):
+//   warps 0-3, 4-7  softmax of stream 0, 1: a thread per row; a running maximum
+//                   and sum in fp32, P in bf16 back to tensor memory; O is rescaled only when the
+//                   maximum has grown by more than 2^8 (kept exact: the
+//                   reference maximum of a row is whatever its weights were formed with);
+//   warps 8-11      Q: norm and rotation in fp32, rounded to bf16 into the swizzled operand;
+//                   a row tile of few rows keeps the rounding's rest as a second bf16
+//                   operand (its product costs what memory-bound items have to spare);
+//   warp 12         tcgen05.mma: S = Q K^T, O += P V (P from tensor memory);
+//   warp 13         TMA: K and V tiles, in the order the products take them, into one ring;
+//   warp 14         the items: walks the batch 32 requests at a time.
 #include "kv.cuh"
 
 namespace csla {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kWarps = 4;
+constexpr int kThreads = 512;
+constexpr int kTile = CSLA_PAGE_TOKENS;   // keys per tile
+constexpr int kItems = 3;                 // items in flight between the roles
+constexpr int kFlags = 16;                // tiles of page flags
+constexpr float kGrow = 8.0f;             // log2 growth of the maximum that O tolerates
 
-template <int D, bool QBF16, bool OBF16>
-__global__ void __launch_bounds__(32 * kWarps) kv_attend_kernel(const __grid_constant__ KvAttendArgs a) {
-    CSLA_TL_SCOPE(kTlKvAttend);
-    constexpr int kLanes = D / 8, kPer = 32 / kLanes;   // lanes per row, rows per warp step
-    pdl_trigger();
-    pdl_wait();
-    CSLA_TL_WAITED();
-    const int lane = threadIdx.x & 31, c = lane % kLanes, sub = lane / kLanes;
-    const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (unit >= (long long)a.bt.N * a.HQ) return;
-    const int n = (int)(unit / a.HQ), hq = (int)(unit % a.HQ), hk = hq / (a.HQ / a.HK);
-    // the request of row n: the last one that starts at or below it
-    int b = n / max(a.bt.T, 1);
-    if (a.bt.q_start) {
-        int cnt = 0;
-        for (int j = lane + 1; j <= a.bt.B; j += 32) cnt += a.bt.q_start[j] <= n;
-        b = __reduce_add_sync(0xffffffffu, cnt);
+template <int D>
+struct Cfg {
+    static constexpr int kKB = D / 64;                  // 64-dim blocks (128-byte rows)
+    static constexpr int kBlk = 128 * 128;              // bytes of a block: 128 rows x 128 B
+    static constexpr int kTileBytes = kKB * kBlk;
+    static constexpr int kStages = D == 128 ? 5 : 10;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffKV = 2 * kTileBytes;
+    static constexpr int kOffMisc = kOffKV + kStages * kTileBytes;
+    // TMEM columns: S (P over it) of each stream, then O of each stream
+    static constexpr int kColS = 0, kColO = 256;
+};
+
+struct Item {
+    int end;             // no more items
+    int paired;          // two row tiles on the same keys; else one row tile, tiles in turn
+    int n0, T, pos0;     // request: first row of q and out, new tokens, position of the first
+    int slot, hk;
+    int row0, rows;      // first row of the item, rows of the request
+    int lo, hi;          // key tiles [lo, hi)
+    int hi0, lo1;        // paired: stream 0 takes [lo, hi0), stream 1 [lo1, hi)
+    int k_lo, k_hi;      // positions that some row of the row tile sees: [k_lo, k_hi)
+    int part;            // index of the item's (first) partial, -1: rows are written out
+    long long base;      // first partial row of the request
+};
+
+struct Misc {
+    Item item[kItems];
+    uint64_t item_full[kItems], item_empty[kItems];
+    uint64_t kv_full[10], kv_empty[10];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
+    int bad[kFlags];     // tile's page is not mapped
+    uint32_t tmem;
+    int abort;
+};
+
+template <int D>
+constexpr int smem_bytes() {
+    return Cfg<D>::kOffMisc + (int)sizeof(Misc) + 1024;
+}
+
+// ---------------------------------------------------------------- items
+// First item of stream s, and whether it takes tile t.
+__device__ __forceinline__ bool takes(const Item &it, int s, int t) {
+    if (it.paired) return s == 0 ? t < it.hi0 : t >= it.lo1;
+    return ((t - it.lo) & 1) == s;
+}
+
+// Item `local` of a request, in the order: row tiles from the last (the longest
+// under the causal mask) to the first; heads inside, unless the request's
+// keys would not stay in L2 while all heads are in use.
+__device__ __forceinline__ bool make_item(const KvAttendArgs &a, const KvReq &r, const KvPlan &p, int local,
+                                          long long base, Item *it) {
+    int i, hk, j;
+    if (p.heads_inside) {
+        j = local % p.nch;
+        hk = local / p.nch % a.HK;
+        i = p.R - 1 - local / p.nch / a.HK;
+    } else {
+        j = local % p.nch;
+        i = p.R - 1 - local / p.nch % p.R;
+        hk = local / p.nch / p.R;
     }
-    if (b >= a.bt.B) return;
-    const KvReq r = kv_request(a.bt, b, a.max_new, a.max_len);
-    if (!r.ok || n < r.n0 || n >= r.n0 + r.T) {
-        if (r.err) set_dev_err(r.err);
+    const KvRange g = kv_range(p, r.L - r.T, i, a.window);
+    const int lo = g.lo + j * p.c, hi = min(g.hi, lo + p.c);
+    if (lo >= hi) return false;
+    it->end = 0;
+    it->paired = p.paired;
+    it->n0 = r.n0;
+    it->T = r.T;
+    it->pos0 = r.L - r.T;
+    it->slot = r.slot;
+    it->hk = hk;
+    it->row0 = i * 256;
+    it->rows = p.rows;
+    it->lo = lo;
+    it->hi = hi;
+    it->hi0 = min(hi, g.hi0);
+    it->lo1 = max(lo, g.lo1);
+    it->k_lo = g.k_lo;
+    it->k_hi = g.k_hi;
+    const int parts = kv_parts(p, g);
+    it->part = parts > 1 ? (p.paired ? j : 2 * j) : -1;
+    it->base = base;
+    return true;
+}
+
+template <int D>
+__device__ void sched_role(const KvAttendArgs &a, Misc *ms) {
+    const int lane = threadIdx.x & 31;
+    const int G = a.HQ / a.HK, grid = gridDim.x;
+    int first = -32, total = 0;            // requests [first, first + 32) are held, one per lane
+    int before = 0;                        // items before them
+    long long part_before = 0, part_total = 0;
+    KvReq r{};
+    KvPlan p{};
+    int incl = 0;
+    long long part_excl = 0;
+    int n = 0;                             // items published
+    for (int round = 0;; ++round) {
+        const int u = (round & 1) ? (round + 1) * grid - 1 - (int)blockIdx.x : round * grid + (int)blockIdx.x;
+        bool none = false;
+        while (u >= before + total) {
+            before += total;
+            part_before += part_total;
+            first += 32;
+            if (first >= a.bt.B) {
+                none = true;
+                break;
+            }
+            const int b = first + lane;
+            int items = 0;
+            long long parts = 0;
+            if (b < a.bt.B) {
+                r = kv_request(a.bt, b, a.max_new, a.max_len);
+                if (r.err && blockIdx.x == 0) set_dev_err(r.err);
+                if (r.ok) {
+                    p = kv_plan(r.T, r.L, G, a.HK, a.window, D);
+                    items = a.HK * p.R * p.nch;
+                    parts = kv_part_rows(p, r.T, a.HQ);
+                }
+            }
+            incl = items;
+            long long pincl = parts;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                const long long w = __shfl_up_sync(0xffffffffu, pincl, o);
+                if (lane >= o) {
+                    incl += v;
+                    pincl += w;
+                }
+            }
+            part_excl = pincl - parts;
+            total = __shfl_sync(0xffffffffu, incl, 31);
+            part_total = __shfl_sync(0xffffffffu, pincl, 31);
+            if (items && a.part_base && blockIdx.x == 0) a.part_base[b] = part_before + part_excl;
+        }
+        Item it;
+        it.end = 1;
+        bool have = true;
+        if (!none) {
+            const int src = __ffs(__ballot_sync(0xffffffffu, incl > u - before)) - 1;
+            const int prev = __shfl_sync(0xffffffffu, incl, max(src - 1, 0));
+            if (lane == src)
+                have = make_item(a, r, p, u - before - (src ? prev : 0), part_before + part_excl, &it);
+            have = __shfl_sync(0xffffffffu, (int)have, src);
+            if (!have) continue;
+            const int slot = n % kItems;
+            if (n >= kItems && !warp_all(mbar_wait(&ms->item_empty[slot], (n / kItems - 1) & 1, &ms->abort))) return;
+            if (lane == src) ms->item[slot] = it;
+            mbar_arrive_warp(&ms->item_full[slot]);
+            ++n;
+            continue;
+        }
+        const int slot = n % kItems;
+        if (n >= kItems && !warp_all(mbar_wait(&ms->item_empty[slot], (n / kItems - 1) & 1, &ms->abort))) return;
+        if (lane == 0) ms->item[slot].end = 1;
+        mbar_arrive_warp(&ms->item_full[slot]);
         return;
     }
-    const int pos = r.L - r.T + (n - r.n0);
-    const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+}
 
-    float q[8], g[8];
-    widen8<QBF16>(load8<QBF16>(a.q, (long long)n * a.q_stride + (long long)hq * D + 8 * c), q);
-    if (a.gamma_q) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = a.gamma_q[8 * c + i];
-        row_norm<D>(q, g, a.eps);
+// The next item for a role's warp; false when there is none (or on an abort).
+__device__ __forceinline__ bool next_item(Misc *ms, int n, Item *it) {
+    const int slot = n % kItems;
+    if (!warp_all(mbar_wait(&ms->item_full[slot], (n / kItems) & 1, &ms->abort))) return false;
+    *it = ms->item[slot];
+    mbar_arrive_warp(&ms->item_empty[slot]);
+    return !it->end;
+}
+
+// ---------------------------------------------------------------- TMA role
+template <int D>
+struct Loader {
+    const KvAttendArgs &a;
+    const CUtensorMap &km, &vm;
+    uint8_t *smem;
+    Misc *ms;
+    int lane;
+    int st = 0, issued = 0;   // ring stage and tiles issued so far
+    int tiles = 0;            // key tiles so far (flag index)
+    // page ids of 64 tiles from `at` on, two per lane
+    int at = 0, pg0 = -1, pg1 = -1;
+
+    __device__ int fetch(const Item &it, int t) const {
+        return t < it.hi ? a.bt.block_table[(long long)it.slot * a.bt.bt_stride + t] : -1;
     }
-    if (a.d_rope) {
-        const RopeLane rl = rope_lane<D>(c, a.d_rope, a.pairs);
-        float2 cs[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            rope_cos_sin(pos, a.freq.inv[min(rl.first + j, a.d_rope / 2 - 1)], &cs[j].x, &cs[j].y);
-        row_rope(q, rl, c, a.d_rope, a.pairs, cs);
+    __device__ void begin(const Item &it) {
+        at = it.lo;
+        pg0 = fetch(it, at + lane);
+        pg1 = fetch(it, at + 32 + lane);
     }
-    const float sc = a.scale * kLog2e;
-    float m = -INFINITY, l = 0.f, o[8] = {};
-    bool bad = false;
-    for (int j0 = lo; j0 <= pos; j0 += kPer) {
-        const int j = j0 + sub;
-        float s = -INFINITY, v[8] = {};
-        if (j <= pos) {
-            const int page = a.bt.block_table[(long long)r.slot * a.bt.bt_stride + j / CSLA_PAGE_TOKENS];
-            if (page >= 0 && page < a.bt.n_pages) {
-                const long long at = (((long long)page * a.HK + hk) * CSLA_PAGE_TOKENS + j % CSLA_PAGE_TOKENS) * D + 8 * c;
-                float k[8];
-                widen8<true>(load8<true>(a.k, at), k);
-                widen8<true>(load8<true>(a.v, at), v);
-                s = 0.f;
+    __device__ int page(const Item &it, int t) {
+        // tiles are asked for in ascending order, V up to two behind K
+        if (t >= at + 64) {
+            at += 32;
+            pg0 = pg1;
+            pg1 = fetch(it, at + 32 + lane);
+        }
+        const int d = t - at;
+        return d < 32 ? __shfl_sync(0xffffffffu, pg0, d & 31) : __shfl_sync(0xffffffffu, pg1, d & 31);
+    }
+    __device__ bool load(const Item &it, int t, bool is_v) {
+        using C = Cfg<D>;
+        int pg = page(it, t);
+        if (issued >= C::kStages &&
+            !warp_all(mbar_wait(&ms->kv_empty[st], (issued / C::kStages - 1) & 1, &ms->abort)))
+            return false;
+        const bool bad = pg < 0 || pg >= a.bt.n_pages;
+        if (lane == 0) {
+            if (!is_v) {
+                ms->bad[tiles % kFlags] = bad;
+                if (bad) set_dev_err(CSLA_DEVERR_PAGE);
+            }
+            uint64_t *bar = &ms->kv_full[st];
+            mbar_arrive_expect_tx(bar, C::kTileBytes);
+            uint8_t *dst = smem + C::kOffKV + st * C::kTileBytes;
+            // (an unmapped page's tile is page 0's, masked)
+            const int row = ((bad ? 0 : pg) * a.HK + it.hk) * kTile;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s = fmaf(q[i], k[i], s);
-            } else {
-                bad = true;
+            for (int kb = 0; kb < C::kKB; ++kb) tma_load_2d(dst + kb * C::kBlk, is_v ? &vm : &km, 64 * kb, row, bar);
+        }
+        __syncwarp();
+        if (!is_v) ++tiles;
+        ++issued;
+        st = st + 1 == C::kStages ? 0 : st + 1;
+        return true;
+    }
+};
+
+template <int D>
+__device__ void load_role(const KvAttendArgs &a, const CUtensorMap &km, const CUtensorMap &vm, uint8_t *smem, Misc *ms) {
+    using C = Cfg<D>;
+    Loader<D> L{a, km, vm, smem, ms, (int)(threadIdx.x & 31)};
+    bool ok = true;
+    Item it;
+    for (int n = 0; ok && next_item(ms, n, &it); ++n) {
+        L.begin(it);
+        if (it.paired) {
+            for (int t = it.lo; ok && t < it.hi; ++t) ok = L.load(it, t, false) && L.load(it, t, true);
+        } else {
+            ok = L.load(it, it.lo, false);
+            if (ok && it.lo + 1 < it.hi) ok = L.load(it, it.lo + 1, false);
+            for (int t = it.lo; ok && t < it.hi; ++t) {
+                ok = L.load(it, t, true);
+                if (ok && t + 2 < it.hi) ok = L.load(it, t + 2, false);
             }
         }
-#pragma unroll
-        for (int x = kLanes / 2; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= sc;
-        const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.f : mn;
-        const float f = exp2f(m - base), p = exp2f(s - base);
-        l = l * f + p;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = o[i] * f + p * v[i];
-        m = mn;
     }
-    if (bad) set_dev_err(CSLA_DEVERR_PAGE);
-    // join the warp's row groups, in a fixed order, and the sink
-    float mt = m;
+    // copies in flight land before the CTA exits (all have, unless a wait gave up)
+    const int from = max(0, L.issued - C::kStages);
+    for (int i = from; i < L.issued; ++i) mbar_wait(&ms->kv_full[i % C::kStages], (i / C::kStages) & 1, nullptr);
+}
+
+// ---------------------------------------------------------------- Q role
+template <int D, bool QBF16>
+__device__ void q_role(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
+    using C = Cfg<D>;
+    constexpr int kLanes = D / 8, kPer = 32 / kLanes;   // lanes per row, rows per step
+    constexpr int kSteps = 32 / kPer, kFly = 4;
+    const int warp = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31, c = lane % kLanes, sub = lane / kLanes;
+    const int G = a.HQ / a.HK;
+    const RopeLane rl = rope_lane<D>(c, a.d_rope, a.pairs);
+    float g[8];
 #pragma unroll
-    for (int x = kLanes; x < 32; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
-    const float sink = a.sink ? a.sink[hq] * kLog2e : -INFINITY;
-    const bool none = mt == -INFINITY;
-    const float top = fmaxf(mt, sink), base = top == -INFINITY ? 0.f : top;
-    const float f = exp2f(m - base);
-    l *= f;
+    for (int i = 0; i < 8; ++i) g[i] = a.gamma_q ? a.gamma_q[8 * c + i] : 1.f;
+    float2 cs[8];
+    int cs_pos = -1;
+    Item it;
+    for (int n = 0; next_item(ms, n, &it); ++n) {
+        for (int s = 0; s < 2; ++s) {
+            if (s == 1 && !it.paired) break;
+            const int r0 = it.row0 + 128 * s + 32 * warp;
+            if (n > 0) {
+                if (!warp_all(mbar_wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort))) return;
+                if (!it.paired && !warp_all(mbar_wait(&ms->q_empty[1], (n - 1) & 1, &ms->abort))) return;
+            }
+#pragma unroll 1
+            for (int k0 = 0; k0 < kSteps; k0 += kFly) {
+                if (r0 + k0 * kPer >= it.rows) break;
+                Raw8<QBF16> raw[kFly];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] *= f;
+                for (int k = 0; k < kFly; ++k) {
+                    const int r = min(r0 + (k0 + k) * kPer + sub, it.rows - 1);
+                    const long long at = (long long)(it.n0 + r / G) * a.q_stride + (long long)(it.hk * G + r % G) * D + 8 * c;
+                    raw[k] = load8<QBF16>(a.q, at);
+                }
 #pragma unroll
-    for (int x = kLanes; x < 32; x <<= 1) {
-        l += __shfl_xor_sync(0xffffffffu, l, x);
+                for (int k = 0; k < kFly; ++k) {
+                    const int rr = r0 + (k0 + k) * kPer + sub, r = min(rr, it.rows - 1);
+                    float x[8];
+                    widen8<QBF16>(raw[k], x);
+                    if (a.gamma_q) row_norm<D>(x, g, a.eps);
+                    if (a.d_rope) {
+                        const int pos = it.pos0 + r / G;
+                        if (__any_sync(0xffffffffu, pos != cs_pos)) {
+                            cs_pos = pos;
+                            if (rl.role) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] += __shfl_xor_sync(0xffffffffu, o[i], x);
-    }
-    l += a.sink ? exp2f(sink - base) : 0.f;
-    const float inv = none ? 0.f : 1.f / l;
-    if (sub == 0) {
-        const long long at = ((long long)n * a.HQ + hq) * D + 8 * c;
-        if constexpr (OBF16) {
-            uint4 w;
-            w.x = pack_bf16(o[0] * inv, o[1] * inv);
-            w.y = pack_bf16(o[2] * inv, o[3] * inv);
-            w.z = pack_bf16(o[4] * inv, o[5] * inv);
-            w.w = pack_bf16(o[6] * inv, o[7] * inv);
-            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.out) + at) = w;
-        } else {
-            float4 *p = reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + at);
-            p[0] = make_float4(o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
-            p[1] = make_float4(o[4] * inv, o[5] * inv, o[6] * inv, o[7] * inv);
+                                for (int j = 0; j < 8; ++j)
+                                    if (j < 4 || a.pairs == CSLA_ROPE_HALVES)
+                                        rope_cos_sin(pos, a.freq.inv[rl.first + j], &cs[j].x, &cs[j].y);
+                            }
+                        }
+                        row_rope(x, rl, c, a.d_rope, a.pairs, cs);
+                    }
+                    uint4 o;
+                    o.x = pack_bf16(x[0], x[1]);
+                    o.y = pack_bf16(x[2], x[3]);
+                    o.z = pack_bf16(x[4], x[5]);
+                    o.w = pack_bf16(x[6], x[7]);
+                    const int i = 32 * warp + (k0 + k) * kPer + sub;   // row of the operand
+                    const int off = (c >> 3) * C::kBlk + i * 128 + (((c & 7) ^ (i & 7)) << 4);
+                    if (rr < it.rows) {
+                        *reinterpret_cast<uint4 *>(smem + C::kOffQ + s * C::kTileBytes + off) = o;
+                        if (!it.paired) {
+                            uint4 e;   // the rest of the rounding
+                            const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+                            uint32_t d[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                d[j] = pack_bf16(x[2 * j] - __uint_as_float(w[j] << 16),
+                                                 x[2 * j + 1] - __uint_as_float(w[j] & 0xFFFF0000u));
+                            e = make_uint4(d[0], d[1], d[2], d[3]);
+                            *reinterpret_cast<uint4 *>(smem + C::kOffQ + C::kTileBytes + off) = e;
+                        }
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive_warp(&ms->q_full[s]);
+            if (!it.paired) mbar_arrive_warp(&ms->q_full[1]);
         }
     }
 }
 
+// ---------------------------------------------------------------- MMA role
+__device__ __forceinline__ void umma_ts_f16(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 template <int D>
-cudaError_t launch(const KvAttendArgs &a, bool qb, bool ob, cudaStream_t s) {
-    const dim3 grid((unsigned)(((long long)a.bt.N * a.HQ + kWarps - 1) / kWarps)), block(32 * kWarps);
-    if (qb) return ob ? launch_pdl(kv_attend_kernel<D, true, true>, grid, block, 0, s, a)
-                      : launch_pdl(kv_attend_kernel<D, true, false>, grid, block, 0, s, a);
-    return ob ? launch_pdl(kv_attend_kernel<D, false, true>, grid, block, 0, s, a)
-              : launch_pdl(kv_attend_kernel<D, false, false>, grid, block, 0, s, a);
+struct Mma {
+    using C = Cfg<D>;
+    uint8_t *smem;
+    Misc *ms;
+    int lane;
+    uint32_t tmem, q0, kv0;
+    int taken = 0;                 // ring tiles taken
+    int p_count[2] = {0, 0};       // P tiles taken per stream
+
+    // Next tile of the ring; its stage.
+    __device__ bool take(int *stage) {
+        *stage = taken % C::kStages;
+        if (!warp_all(mbar_wait(&ms->kv_full[*stage], (taken / C::kStages) & 1, &ms->abort))) return false;
+        ++taken;
+        tc_fence_after();
+        return true;
+    }
+    // V rows outside [lo, hi) of the tile, which no row sees, to zero (their
+    // weights are zero, but 0 * NaN is not).
+    __device__ void clean_v(int stage, int lo, int hi) {
+        if (lo <= 0 && hi >= kTile) return;
+        uint8_t *v = smem + C::kOffKV + stage * C::kTileBytes;
+        for (int i = lane; i < kTile * 8; i += 32) {
+            const int row = i >> 3;
+            if (row >= lo && row < hi) continue;
+#pragma unroll
+            for (int kb = 0; kb < C::kKB; ++kb)
+                *reinterpret_cast<uint4 *>(v + kb * C::kBlk + i * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+    }
+    // S of stream s = Q K^T (both terms of Q for an unpaired item)
+    __device__ void s_mma(int s, int stage, bool paired) {
+        constexpr uint32_t kId = idesc_bf16(128, kTile, false, false);
+        if (lane == 0) {
+            const uint32_t k0 = kv0 + stage * C::kTileBytes;
+            const int q_lo = paired ? s : 0, q_hi = paired ? s : 1;
+            uint32_t acc = 0;
+            for (int qt = q_lo; qt <= q_hi; ++qt) {
+#pragma unroll
+                for (int kb = 0; kb < C::kKB; ++kb)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        umma_kind_f16(tmem + C::kColS + 128 * s,
+                                      sdesc(q0 + qt * C::kTileBytes + kb * C::kBlk + kk * 32, 16, 1024),
+                                      sdesc(k0 + kb * C::kBlk + kk * 32, 16, 1024), kId, acc);
+                        acc = 1;
+                    }
+            }
+            umma_commit(&ms->s_full[s]);
+        }
+        __syncwarp();
+    }
+    // O of stream s (+)= P V once P is there
+    __device__ bool pv_mma(int s, int stage, bool first) {
+        constexpr uint32_t kId = idesc_bf16(128, D, false, true);
+        if (!warp_all(mbar_wait(&ms->p_full[s], p_count[s] & 1, &ms->abort))) return false;
+        ++p_count[s];
+        tc_fence_after();
+        if (lane == 0) {
+            const uint32_t v0 = kv0 + stage * C::kTileBytes;
+#pragma unroll
+            for (int ks = 0; ks < kTile / 16; ++ks)
+                umma_ts_f16(tmem + C::kColO + D * s, tmem + C::kColS + 128 * s + 8 * ks,
+                            sdesc(v0 + ks * 2048, C::kBlk, 1024), kId, (!first || ks > 0) ? 1u : 0u);
+        }
+        __syncwarp();
+        return true;
+    }
+    __device__ void commit(uint64_t *bar) {
+        if (lane == 0) umma_commit(bar);
+        __syncwarp();
+    }
+
+    __device__ bool item_paired(const Item &it, const int *bad, int tiles) {
+        int kst, vst;
+        if (!take(&kst)) return false;
+        for (int s = 0; s < 2; ++s)
+            if (takes(it, s, it.lo)) s_mma(s, kst, true);
+        commit(&ms->kv_empty[kst]);
+        bool first[2] = {true, true};
+        for (int t = it.lo; t < it.hi; ++t) {
+            if (!take(&vst)) return false;
+            const bool b = bad[(tiles + t - it.lo) % kFlags];
+            clean_v(vst, b ? 0 : it.k_lo - t * kTile, b ? 0 : it.k_hi - t * kTile);
+            const bool more = t + 1 < it.hi;
+            kst = -1;
+            for (int s = 0; s < 2; ++s) {
+                if (takes(it, s, t)) {
+                    if (!pv_mma(s, vst, first[s])) return false;
+                    first[s] = false;
+                    if (!more || !takes(it, s, t + 1)) commit(&ms->o_full[s]);
+                }
+                if (s == 1) commit(&ms->kv_empty[vst]);
+                if (more && takes(it, s, t + 1)) {
+                    if (kst < 0 && !take(&kst)) return false;
+                    s_mma(s, kst, true);
+                }
+            }
+            if (more) {
+                if (kst < 0 && !take(&kst)) return false;   // (no stream takes the tile: not reached)
+                commit(&ms->kv_empty[kst]);
+            }
+        }
+        commit(&ms->q_empty[0]);
+        commit(&ms->q_empty[1]);
+        return true;
+    }
+    __device__ bool item_single(const Item &it, const int *bad, int tiles) {
+        int kst, vst;
+        for (int s = 0; s < 2 && it.lo + s < it.hi; ++s) {
+            if (!take(&kst)) return false;
+            s_mma(s, kst, false);
+            commit(&ms->kv_empty[kst]);
+        }
+        for (int t = it.lo; t < it.hi; ++t) {
+            const int s = (t - it.lo) & 1;
+            if (!take(&vst)) return false;
+            const bool b = bad[(tiles + t - it.lo) % kFlags];
+            clean_v(vst, b ? 0 : it.k_lo - t * kTile, b ? 0 : it.k_hi - t * kTile);
+            if (!pv_mma(s, vst, t - it.lo < 2)) return false;
+            commit(&ms->kv_empty[vst]);
+            if (t + 2 < it.hi) {
+                if (!take(&kst)) return false;
+                s_mma(s, kst, false);
+                commit(&ms->kv_empty[kst]);
+            } else {
+                commit(&ms->o_full[s]);
+            }
+        }
+        commit(&ms->q_empty[0]);
+        commit(&ms->q_empty[1]);
+        return true;
+    }
+};
+
+template <int D>
+__device__ void mma_role(uint8_t *smem, Misc *ms) {
+    using C = Cfg<D>;
+    Mma<D> m{smem, ms, (int)(threadIdx.x & 31), ms->tmem, smem_u32(smem + C::kOffQ), smem_u32(smem + C::kOffKV)};
+    bool ok = true;
+    int tiles = 0;
+    Item it;
+    for (int n = 0; ok && next_item(ms, n, &it); ++n) {
+        for (int s = 0; ok && s < 2; ++s) ok = warp_all(mbar_wait(&ms->q_full[s], n & 1, &ms->abort));
+        if (!ok) break;
+        tc_fence_after();
+        ok = it.paired ? m.item_paired(it, ms->bad, tiles) : m.item_single(it, ms->bad, tiles);
+        tiles += it.hi - it.lo;
+    }
+    // products in flight end before tensor memory is freed (all have, unless a wait gave up)
+    m.commit(&ms->drain);
+    mbar_wait(&ms->drain, 0, nullptr);
+}
+
+// ---------------------------------------------------------------- softmax role
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+template <int D, bool OBF16>
+__device__ void softmax_role(const KvAttendArgs &a, Misc *ms, int s) {
+    using C = Cfg<D>;
+    const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+    const uint32_t tw = ms->tmem + ((uint32_t)(warp * 32) << 16);
+    const uint32_t ts = tw + C::kColS + 128 * s, to = tw + C::kColO + D * s;
+    const int G = a.HQ / a.HK;
+    const float sc = a.scale * kLog2e;
+    int s_count = 0, o_count = 0, tiles = 0;
+    Item it;
+    for (int n = 0; next_item(ms, n, &it); ++n) {
+        const int row = it.row0 + (it.paired ? 128 * s : 0) + 32 * warp + lane;
+        const bool mine = row < it.rows;
+        const bool idle = it.row0 + (it.paired ? 128 * s : 0) + 32 * warp >= it.rows;   // no row of the warp is real
+        const int r = min(row, it.rows - 1);
+        const int pos = it.pos0 + r / G;
+        const int low = a.window > 0 ? pos - a.window + 1 : 0;
+        float m = -INFINITY, l = 0.f;   // m: the maximum the weights are formed with (score * sc)
+        bool any = false;
+        const int t0 = it.paired ? (s == 0 ? it.lo : it.lo1) : it.lo + s;
+        const int t1 = it.paired && s == 0 ? it.hi0 : it.hi;
+        for (int t = t0; t < t1; t += it.paired ? 1 : 2) {
+            if (!warp_all(mbar_wait(&ms->s_full[s], s_count & 1, &ms->abort))) return;
+            ++s_count;
+            tc_fence_after();
+            if (!idle) {
+                const bool bad = ms->bad[(tiles + t - it.lo) % kFlags];
+                const int last = bad ? -1 : pos - t * kTile, from = low - t * kTile;   // visible columns
+                const bool cut = __any_sync(0xffffffffu, last < kTile - 1 || from > 0);
+                float mx = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t v[32];
+                    tmem_ld32x32(ts + 32 * c, v);
+                    tmem_wait_ld();
+                    if (cut) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (32 * c + i > last || 32 * c + i < from) v[i] = 0xFF800000u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(v[i]));
+                }
+                const float mn = fmaxf(m, mx * sc);
+                const bool grow = mn > m + kGrow;   // (also from -inf)
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - mn)) : 1.f;
+                    if (grow) m = mn;
+                    l *= f;
+                    if (any) {
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t v[32];
+                            tmem_ld32x32(to + 32 * c, v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+                            tmem_st32x32(to + 32 * c, v);
+                        }
+                    }
+                }
+                const float sub = m == -INFINITY ? 0.f : m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t v[32], o[16];
+                    tmem_ld32x32(ts + 32 * c, v);
+                    tmem_wait_ld();
+                    if (cut) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (32 * c + i > last || 32 * c + i < from) v[i] = 0xFF800000u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float p0 = ex2(fmaf(__uint_as_float(v[2 * i]), sc, -sub));
+                        const float p1 = ex2(fmaf(__uint_as_float(v[2 * i + 1]), sc, -sub));
+                        sum[i & 3] += p0 + p1;
+                        o[i] = pack_bf16(p0, p1);
+                    }
+                    tmem_st32x16(ts + 16 * c, o);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_wait_st();
+                any = true;
+            }
+            tc_fence_before();
+            mbar_arrive_warp(&ms->p_full[s]);
+        }
+        tiles += it.hi - it.lo;
+        if (t0 < t1) {
+            if (!warp_all(mbar_wait(&ms->o_full[s], o_count & 1, &ms->abort))) return;
+            ++o_count;
+            tc_fence_after();
+        }
+        if (idle) {
+            tc_fence_before();
+            continue;
+        }
+        const bool none = m == -INFINITY;
+        if (it.part >= 0) {
+            // partial: O and (m, l), of part `part` (+ s for a shared row tile)
+            const long long pr = it.base + ((long long)(it.part + (it.paired ? 0 : s)) * a.HK + it.hk) * it.rows + r;
+            if (mine) a.part_ml[pr] = make_float2(m, l);
+            if (t0 < t1) {
+                float *po = a.part_o + pr * D;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t v[32];
+                    tmem_ld32x32(to + 32 * c, v);
+                    tmem_wait_ld();
+                    if (mine) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<uint4 *>(po + 32 * c + 4 * i) =
+                                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    }
+                }
+            }
+        } else if (t0 < t1) {
+            const int hq = it.hk * G + r % G;
+            const float sink = a.sink ? a.sink[hq] * kLog2e : -INFINITY;
+            const float top = fmaxf(m, sink);
+            const float f = none ? 0.f : ex2(m - top);
+            const float den = fmaf(l, f, a.sink && !none ? ex2(sink - top) : 0.f);
+            const float w = none ? 0.f : f / den;
+            const long long at = ((long long)(it.n0 + r / G) * a.HQ + hq) * D;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t v[32];
+                tmem_ld32x32(to + 32 * c, v);
+                tmem_wait_ld();
+                float x[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = none ? 0.f : __uint_as_float(v[i]) * w;
+                if (mine) {
+                    if constexpr (OBF16) {
+                        uint4 *p = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.out) + at + 32 * c);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            p[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
+                                              pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+                    } else {
+                        float4 *p = reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + at + 32 * c);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) p[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                    }
+                }
+            }
+        }
+        tc_fence_before();
+    }
+}
+
+// ---------------------------------------------------------------- kernel
+template <int D, bool QBF16, bool OBF16>
+__global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_constant__ KvAttendArgs a,
+                                                                const __grid_constant__ CUtensorMap km,
+                                                                const __grid_constant__ CUtensorMap vm) {
+    CSLA_TL_SCOPE(kTlKvAttend);
+    using C = Cfg<D>;
+    extern __shared__ uint8_t raw_smem[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
+    Misc *ms = reinterpret_cast<Misc *>(smem + C::kOffMisc);
+    const int warp = threadIdx.x >> 5;
+    if (warp == 12) {
+        tmem_alloc(&ms->tmem, 512);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&ms->item_full[i], 1);
+            mbar_init(&ms->item_empty[i], 14);   // softmax 8, Q 4, MMA, TMA
+        }
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&ms->kv_full[i], 1);
+            mbar_init(&ms->kv_empty[i], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&ms->q_full[s], 4);
+            mbar_init(&ms->q_empty[s], 1);
+            mbar_init(&ms->s_full[s], 1);
+            mbar_init(&ms->p_full[s], 4);
+            mbar_init(&ms->o_full[s], 1);
+        }
+        mbar_init(&ms->drain, 1);
+        ms->abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&km);
+        tma_prefetch_desc(&vm);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_trigger();
+    pdl_wait();
+    CSLA_TL_WAITED();
+    if (warp < 8)
+        softmax_role<D, OBF16>(a, ms, warp >> 2);
+    else if (warp < 12)
+        q_role<D, QBF16>(a, smem, ms);
+    else if (warp == 12)
+        mma_role<D>(smem, ms);
+    else if (warp == 13)
+        load_role<D>(a, km, vm, smem, ms);
+    else if (warp == 14)
+        sched_role<D>(a, ms);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_dealloc(ms->tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- join
+// One warp per (row, KV head) whose keys were cut: o = sum_p w_p O_p /
+// (sum_p w_p l_p + w_sink), w_p = 2^(m_p - M), parts in order.
+constexpr int kJoinWarps = 8;
+template <int D, bool OBF16>
+__global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_constant__ KvAttendArgs a) {
+    CSLA_TL_SCOPE(kTlKvJoin);
+    constexpr int kDims = D / 32;
+    pdl_trigger();
+    pdl_wait();
+    CSLA_TL_WAITED();
+    const int lane = threadIdx.x & 31, b = blockIdx.y, G = a.HQ / a.HK;
+    const KvReq rq = kv_request(a.bt, b, a.max_new, a.max_len);
+    if (!rq.ok) return;
+    const KvPlan p = kv_plan(rq.T, rq.L, G, a.HK, a.window, D);
+    if (kv_part_rows(p, rq.T, a.HQ) == 0) return;
+    const long long base = a.part_base[b];
+    for (int u = blockIdx.x * kJoinWarps + (threadIdx.x >> 5); u < p.rows * a.HK; u += gridDim.x * kJoinWarps) {
+        const int r = u / a.HK, hk = u % a.HK;
+        const KvRange g = kv_range(p, rq.L - rq.T, r / 256, a.window);
+        const int parts = kv_parts(p, g);
+        if (parts <= 1) continue;
+        const long long pr = base + (long long)hk * p.rows + r, step = (long long)a.HK * p.rows;
+        const int hq = hk * G + r % G;
+        const float sink = a.sink ? a.sink[hq] * kLog2e : -INFINITY;
+        float top = -INFINITY;
+        for (int i = lane; i < parts; i += 32) top = fmaxf(top, a.part_ml[pr + i * step].x);
+        top = warp_max(top);
+        const bool none = top == -INFINITY;
+        top = fmaxf(top, sink);
+        float o[kDims] = {}, den = a.sink ? ex2(sink - top) : 0.f;
+        for (int i0 = 0; i0 < parts && !none; i0 += 32) {
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (i0 + lane < parts) ml = a.part_ml[pr + (i0 + lane) * step];
+            const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+            const float wl = ml.x == -INFINITY ? 0.f : w * ml.y;
+            const int cnt = min(32, parts - i0);
+#pragma unroll 8
+            for (int i = 0; i < cnt; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, w, i);
+                den += __shfl_sync(0xffffffffu, wl, i);
+                const bool empty = __shfl_sync(0xffffffffu, ml.x, i) == -INFINITY;   // its O was never written
+                const float *src = a.part_o + (pr + (i0 + i) * step) * D + kDims * lane;
+                float v[kDims];
+                if constexpr (kDims == 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(src);
+                    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2 *>(src);
+                    v[0] = x.x; v[1] = x.y;
+                }
+#pragma unroll
+                for (int d = 0; d < kDims; ++d) o[d] = empty ? o[d] : fmaf(wi, v[d], o[d]);
+            }
+        }
+        const float inv = none ? 0.f : 1.f / den;
+        const long long at = ((long long)(rq.n0 + r / G) * a.HQ + hq) * D + kDims * lane;
+        if constexpr (OBF16) {
+            uint32_t *dst = reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(a.out) + at);
+#pragma unroll
+            for (int d = 0; d < kDims; d += 2) dst[d / 2] = pack_bf16(o[d] * inv, o[d + 1] * inv);
+        } else {
+            float *dst = reinterpret_cast<float *>(a.out) + at;
+#pragma unroll
+            for (int d = 0; d < kDims; ++d) dst[d] = o[d] * inv;
+        }
+    }
+}
+
+template <int D, bool QB, bool OB>
+cudaError_t launch(const KvAttendArgs &a, const CUtensorMap &km, const CUtensorMap &vm, int num_sms, long long items,
+                   bool join, cudaStream_t s) {
+    auto kern = kv_attend_kernel<D, QB, OB>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
+    if (e != cudaSuccess) return e;
+    const unsigned grid = (unsigned)(items < num_sms ? items : num_sms);
+    e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem_bytes<D>(), s, a, km, vm);
+    if (e != cudaSuccess || !join) return e;
+    const long long rows = (long long)min(a.max_new, a.bt.N) * a.HQ;
+    long long x = (rows + kJoinWarps - 1) / kJoinWarps;
+    const long long most = 8ll * num_sms / a.bt.B + 1;
+    if (x > most) x = most;
+    return launch_pdl(kv_join_kernel<D, OB>, dim3((unsigned)x, (unsigned)a.bt.B), dim3(32 * kJoinWarps), 0, s, a);
+}
+
+template <int D>
+cudaError_t launch_types(const KvAttendArgs &a, bool qb, bool ob, const CUtensorMap &km, const CUtensorMap &vm,
+                         int num_sms, long long items, bool join, cudaStream_t s) {
+    if (qb) return ob ? launch<D, true, true>(a, km, vm, num_sms, items, join, s)
+                      : launch<D, true, false>(a, km, vm, num_sms, items, join, s);
+    return ob ? launch<D, false, true>(a, km, vm, num_sms, items, join, s)
+              : launch<D, false, false>(a, km, vm, num_sms, items, join, s);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_attend(const KvAttendArgs &a, bool q_bf16, bool out_bf16, cudaStream_t stream) {
-    return a.D == 64 ? launch<64>(a, q_bf16, out_bf16, stream) : launch<128>(a, q_bf16, out_bf16, stream);
+cudaError_t launch_kv_attend(const KvAttendArgs &a, bool q_bf16, bool out_bf16, const CUtensorMap &km,
+                             const CUtensorMap &vm, int num_sms, long long items, bool join, cudaStream_t stream) {
+    return a.D == 64 ? launch_types<64>(a, q_bf16, out_bf16, km, vm, num_sms, items, join, stream)
+                     : launch_types<128>(a, q_bf16, out_bf16, km, vm, num_sms, items, join, stream);
 }
 
 }  // namespace csla

@@ -47,7 +47,10 @@ def attend_request(q, k, v, first_pos, shape, halves, sink, gamma, q_bits=HALF_B
     The kernel rounds q' to bf16 (half a step per element), so a score is off by at most
     E = scale * sum |q'_d K_jd| (2^-8 + 2^-15) + 2^-20 |s| (fp32 sums of D terms, the norm and rotation, and the argument of
     the exponential); each weight e^s by a factor e^{+-E}, the numerator's weights also by 2^-8 (rounded to bf16) and 2^-12 (the
-    exponential), the sums by 2^-12.  With A = sum p_j |V_j| / sum: |error| <= (e^{2E} (1 + 2^-8)(1 + 2^-12) / (1 - 2^-11) - 1) A."""
+    exponential), the sums by 2^-12.  With A = sum p_j |V_j| / sum: |error| <= (e^{2E} (1 + 2^-8)(1 + 2^-12) / (1 - 2^-11) - 1) A.
+    That is relative, so it says nothing of weights below fp32's smallest normal number 2^-126, which the exponential
+    flushes to zero: a weight counts 2^8 at most before it is normalised, so L flushed ones change o by at most
+    L 2^-118 max|V| (a sink of 100 over scores near 0 gives e^-100 = 2^-144)."""
     t, HQ, D = q.shape
     L, HK = k.shape[:2]
     G = HQ // HK
@@ -77,7 +80,7 @@ def attend_request(q, k, v, first_pos, shape, halves, sink, gamma, q_bits=HALF_B
             total = total + torch.exp(sink[h].double() - m)
         o[:, h] = p @ V / total
         A = p @ V.abs() / total
-        tol[:, h] = (torch.exp(2 * E) * (1 + HALF_BF16) * (1 + 2.0 ** -12) / (1 - 2.0 ** -11) - 1) * A
+        tol[:, h] = (torch.exp(2 * E) * (1 + HALF_BF16) * (1 + 2.0 ** -12) / (1 - 2.0 ** -11) - 1) * A + L * 2.0 ** -118 * V.abs().max()
     return o, tol
 
 
