@@ -8,11 +8,20 @@ compiled in (-DCSLA_TIMELINE, csla_timeline_read/clear exported).
 
 The library has no torch dependency: it is plain CUDA C++ behind the C ABI
 of include/csla.h.  Kernels are compiled for sm_100a only.
+
+The sources share device symbols (-rdc=true), but for those in ALONE: a
+kernel that moves registers between its warps (setmaxnreg) has to be
+compiled as a whole program, the compiler ignores the instruction otherwise.
+Such a unit keeps a device error word of its own, which csla_device_error
+reads too.  (The timeline build compiles them like the others, so it times
+them without that split.)
 """
 import glob
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,11 +31,12 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
-    "-O3", "-lineinfo", "-std=c++17", "-rdc=true",
+    "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
     "--expt-relaxed-constexpr",
     "-I" + os.path.join(ROOT, "include"),
 ]
+ALONE = {"kv_attend.cu"}
 
 
 def sources():
@@ -42,22 +52,32 @@ def _stale():
     return any(os.path.getmtime(p) > t for p in deps)
 
 
-def build(force=False, verbose=False, extra=()):
+def _link(out, extra=(), shared=()):
+    """Compile every source (in parallel) and link them into `out`; sources outside `shared` get a whole program each."""
+    with tempfile.TemporaryDirectory(dir=PKG, prefix="_build") as d:
+        def one(src):
+            name = os.path.basename(src)
+            obj = os.path.join(d, name + ".o")
+            alone = name in ALONE and name not in shared
+            mode = ["-DCSLA_UNIT_ALONE"] if alone else ["-rdc=true"]
+            subprocess.run([NVCC, *FLAGS, *extra, *mode, "-c", "-o", obj, src], check=True)
+            return obj
+        with ThreadPoolExecutor(max_workers=os.cpu_count() or 4) as pool:
+            objs = list(pool.map(one, sources()))
+        tmp = out + ".tmp%d" % os.getpid()
+        subprocess.run([NVCC, *FLAGS, "-rdc=true", "-shared", "-o", tmp, *objs], check=True)
+        os.replace(tmp, out)
+    return out
+
+
+def build(force=False, extra=()):
     if not force and not _stale():
         return LIB
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [NVCC, *FLAGS, *extra, "-shared", "-o", tmp, *sources()]
-    if verbose:
-        print(" ".join(cmd))
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
-    return LIB
+    return _link(LIB, extra)
 
 
 def build_timeline(out):
-    cmd = [NVCC, *FLAGS, "-DCSLA_TIMELINE", "-shared", "-o", out, *sources()]
-    subprocess.run(cmd, check=True)
-    return out
+    return _link(out, ["-DCSLA_TIMELINE"], shared=ALONE)
 
 
 if __name__ == "__main__":
@@ -65,4 +85,4 @@ if __name__ == "__main__":
         print(build_timeline(os.path.abspath(sys.argv[sys.argv.index("--timeline") + 1])))
         sys.exit(0)
     extra = ["-Xptxas", "-v"] if "--ptxas-v" in sys.argv else []
-    print(build(force="--force" in sys.argv or bool(extra), verbose=True, extra=extra))
+    print(build(force="--force" in sys.argv or bool(extra), extra=extra))

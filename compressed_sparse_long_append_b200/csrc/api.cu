@@ -222,6 +222,9 @@ int csla_device_error(csla_stream_t stream, uint32_t *bits) {
     unsigned int v = 0, zero = 0;
     if (cudaMemcpyFromSymbol(&v, csla::g_dev_err, sizeof(v)) != cudaSuccess) return CSLA_ERR_CUDA;
     if (v && cudaMemcpyToSymbol(csla::g_dev_err, &zero, sizeof(zero)) != cudaSuccess) return CSLA_ERR_CUDA;
+    unsigned int own = 0;
+    if (kv_attend_dev_err(&own) != cudaSuccess) return CSLA_ERR_CUDA;
+    v |= own;
     if (bits) *bits = v;
     return v ? CSLA_ERR_DEVICE : CSLA_OK;
 }
@@ -746,21 +749,21 @@ static long long kv_most_tiles(const csla_kv_cfg *c, int max_new, int max_len) {
 }
 
 // Partial rows that a batch within these bounds may need (kv_plan: a chunk
-// is at least kKvMin tiles and at least a 1/kKvUnits share of a request's
-// row tiles and heads).
+// is at least kKvMin tiles, and a request at most kKvUnits items, unless its
+// keys are not cut at all).
 static long long kv_most_part_rows(const csla_kv_cfg *c, int B, int N, int max_new, int max_len) {
     const long long G = c->HQ / c->HK, HK = c->HK, nt = kv_most_tiles(c, max_new, max_len);
     auto least = [](long long x, long long y) { return x < y ? x : y; };
     auto parts = [&](long long min_tiles, long long units) {
-        return least((nt + min_tiles - 1) / min_tiles, (units + HK - 1) / HK);
+        return least((nt + min_tiles - 1) / min_tiles, units / HK > 1 ? units / HK : 1);
     };
     if (nt <= 1) return 0;
     // requests of one row tile
     const long long t1 = least(max_new, 128 / G);
     long long rows = least(N, B * t1) * c->HQ * 2 * parts(kKvMinSingle, kKvUnitsSingle);
     if (max_new * G > 128 && nt > kKvMinPaired) {
-        // each has chunks * 256 * R * HK rows at most, R * HK < units and chunks <= units / (R * HK) + 1
-        const long long each = 256ll * 2 * kKvUnitsPaired, n = least(B, N * G / 129);
+        // each has chunks * 256 * R * HK rows at most, chunks <= units / (R * HK)
+        const long long each = 256ll * kKvUnitsPaired, n = least(B, N * G / 129);
         rows += least(n * each, (long long)N * c->HQ * parts(kKvMinPaired, kKvUnitsPaired));
     }
     return rows;

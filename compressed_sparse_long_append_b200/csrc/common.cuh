@@ -19,8 +19,14 @@
 
 namespace csla {
 
-// Library-wide device error word (CSLA_DEVERR_* bits), one per device.
+// Library-wide device error word (CSLA_DEVERR_* bits), one per device.  A unit
+// that is compiled as a whole program of its own (CSLA_UNIT_ALONE) has a word
+// of its own; csla_device_error reads and clears them all.
+#ifdef CSLA_UNIT_ALONE
+static __device__ unsigned int g_dev_err = 0;
+#else
 extern __device__ unsigned int g_dev_err;
+#endif
 
 __device__ __forceinline__ void set_dev_err(unsigned bits) { atomicOr(&g_dev_err, bits); }
 

@@ -253,9 +253,12 @@ __host__ __device__ inline int attend_max_chunks(long long n) {
 }
 
 // ---------------------------------------------------------------- dense paged layers
-// RoPE inverse frequencies of a dense layer (d_rope up to 128).
+// RoPE frequencies theta^(-2i/d_rope) of a dense layer (d_rope up to 128) as
+// turns per position, in units of 2^-64 turn: position times frequency
+// modulo one turn is then one 64-bit integer product, exact in the product and
+// off by less than pos * 2^-65 turns from the frequency's rounding.
 struct KvFreq {
-    double inv[64];
+    unsigned long long turn[64];
 };
 inline KvFreq kv_freq(float theta, int d_rope) {
     // powers of one ratio in extended precision (64 products: below 2^-57
@@ -263,8 +266,8 @@ inline KvFreq kv_freq(float theta, int d_rope) {
     KvFreq f{};
     if (d_rope <= 0) return f;
     const long double ratio = expl(-2.0L / d_rope * logl((long double)theta));
-    long double x = 1.0L;
-    for (int i = 0; i < d_rope / 2 && i < 64; ++i, x *= ratio) f.inv[i] = (double)x;
+    long double x = 18446744073709551616.0L / 6.283185307179586476925286766559L;   // 2^64 / 2 pi
+    for (int i = 0; i < d_rope / 2 && i < 64; ++i, x *= ratio) f.turn[i] = x < 18446744073709551615.0L ? (unsigned long long)x : 0;
     return f;
 }
 
@@ -354,18 +357,19 @@ __host__ __device__ inline KvPlan kv_plan(int T, int L, int G, int HK, int windo
     p.paired = p.rows > 128;
     p.R = p.paired ? (p.rows + 255) / 256 : 1;
     // key tiles of the longest row tile (with a window: an upper bound)
-    long long nt = (L + CSLA_PAGE_TOKENS - 1) / CSLA_PAGE_TOKENS;
-    if (window > 0) {
-        const long long w = ((long long)window + (p.paired ? 256 / G + 1 : T) + CSLA_PAGE_TOKENS - 2) / CSLA_PAGE_TOKENS + 1;
+    int nt = (L - 1) / CSLA_PAGE_TOKENS + 1;
+    if (window > 0 && window < L) {
+        const int w = (window + (p.paired ? 256 / G + 1 : T) + CSLA_PAGE_TOKENS - 2) / CSLA_PAGE_TOKENS + 1;
         nt = w < nt ? w : nt;
     }
-    const long long units = p.paired ? kKvUnitsPaired : kKvUnitsSingle;
-    long long c = (nt * HK * p.R + units - 1) / units;
+    // (32-bit divisions only: this runs ahead of every item's first load)
+    const unsigned most = (p.paired ? kKvUnitsPaired : kKvUnitsSingle) / (unsigned)(HK * p.R);   // chunks
+    int c = most > 1 ? (int)((nt + most - 1) / most) : nt;
     const int least = p.paired ? kKvMinPaired : kKvMinSingle;
     if (c < least) c = least;
     if (c > nt) c = nt;
-    p.c = (int)c;
-    p.nch = (int)((nt + c - 1) / c);
+    p.c = c;
+    p.nch = (nt + c - 1) / c;
     // K and V of all heads below half of L2: heads in turn, longest row tiles first
     p.heads_inside = (long long)L * HK * D * 4 <= (64ll << 20);
     return p;
@@ -382,6 +386,8 @@ __host__ __device__ inline long long kv_part_rows(const KvPlan &p, int T, int HQ
     if (p.paired ? p.nch == 1 : p.c == 1) return 0;
     return parts * T * HQ;
 }
+// Reads and clears the device error word of kv_attend.cu's unit (0 where it shares the library's).
+cudaError_t kv_attend_dev_err(unsigned int *bits);
 cudaError_t launch_kv_attend(const KvAttendArgs &a, bool q_bf16, bool out_bf16, const CUtensorMap &km,
                              const CUtensorMap &vm, int num_sms, long long items, bool join, cudaStream_t stream);
 

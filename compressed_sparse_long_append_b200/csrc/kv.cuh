@@ -2,6 +2,8 @@
 // ragged batch, and the norm and rotation of a row held 8 dims per lane.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace csla {
@@ -42,35 +44,58 @@ __device__ __forceinline__ KvReq kv_request(const KvBatch &a, int b, int max_new
 }
 
 // ------------------------------------------------------------ rows, 8 dims per lane
-// A row of D dims is held by D/8 consecutive lanes of a warp, lane c of the
-// row holding dims 8c .. 8c+7 in fp32.
+// A row of D dims is held by D/8 consecutive lanes of a warp, 8 dims per lane
+// in two runs of four, d0.. and d1..: lanes of unrotated dims hold eight
+// neighbours, and so do lanes of adjacent pairs (0,1) (2,3) (4,5) (6,7);
+// with pairs of halves a lane holds four dims of the first half and their
+// partners, pairs (0,4) (1,5) (2,6) (3,7).  So every rotation stays in its lane.
+struct RowLane {
+    int d0, d1;   // first dims of the two runs
+    int pair;     // first of the lane's four pairs, -1: not rotated
+};
+template <int D>
+__device__ __forceinline__ RowLane row_lane(int c, int d_rope, int pairs) {
+    RowLane l;
+    const int d = 8 * c - (D - d_rope);   // within the rotated dims (d_rope is a multiple of 16)
+    l.d0 = 8 * c;
+    l.d1 = 8 * c + 4;
+    l.pair = d < 0 ? -1 : d / 2;
+    if (d >= 0 && pairs == CSLA_ROPE_HALVES) {
+        l.d0 = D - d_rope + d / 2;
+        l.d1 = l.d0 + d_rope / 2;
+    }
+    return l;
+}
 
 template <bool BF16>
 struct Raw8 {   // 8 elements as loaded
-    uint4 v[BF16 ? 1 : 2];
+    typename std::conditional<BF16, uint2, uint4>::type v[2];
 };
 template <bool BF16>
-__device__ __forceinline__ Raw8<BF16> load8(const void *base, long long elem) {
+__device__ __forceinline__ Raw8<BF16> load8(const void *base, long long elem, const RowLane &l) {
     Raw8<BF16> r;
-    const uint4 *p = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(base) + elem * (BF16 ? 2 : 4));
-    r.v[0] = __ldg(p);
-    if constexpr (!BF16) r.v[1] = __ldg(p + 1);
+    const char *p = reinterpret_cast<const char *>(base) + elem * (BF16 ? 2 : 4);
+    constexpr int kB = BF16 ? 2 : 4;
+    using V = typename std::conditional<BF16, uint2, uint4>::type;
+    r.v[0] = __ldg(reinterpret_cast<const V *>(p + l.d0 * kB));
+    r.v[1] = __ldg(reinterpret_cast<const V *>(p + l.d1 * kB));
     return r;
 }
 template <bool BF16>
 __device__ __forceinline__ void widen8(const Raw8<BF16> &r, float (&x)[8]) {
-    if constexpr (BF16) {
-        const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    for (int h = 0; h < 2; ++h) {
+        if constexpr (BF16) {
+            x[4 * h] = __uint_as_float(r.v[h].x << 16);
+            x[4 * h + 1] = __uint_as_float(r.v[h].x & 0xFFFF0000u);
+            x[4 * h + 2] = __uint_as_float(r.v[h].y << 16);
+            x[4 * h + 3] = __uint_as_float(r.v[h].y & 0xFFFF0000u);
+        } else {
+            x[4 * h] = __uint_as_float(r.v[h].x);
+            x[4 * h + 1] = __uint_as_float(r.v[h].y);
+            x[4 * h + 2] = __uint_as_float(r.v[h].z);
+            x[4 * h + 3] = __uint_as_float(r.v[h].w);
         }
-    } else {
-        x[0] = __uint_as_float(r.v[0].x); x[1] = __uint_as_float(r.v[0].y);
-        x[2] = __uint_as_float(r.v[0].z); x[3] = __uint_as_float(r.v[0].w);
-        x[4] = __uint_as_float(r.v[1].x); x[5] = __uint_as_float(r.v[1].y);
-        x[6] = __uint_as_float(r.v[1].z); x[7] = __uint_as_float(r.v[1].w);
     }
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -82,42 +107,28 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // RMSNorm over the row (all lanes of the row take part; fixed-order sum).
 template <int D>
 __device__ __forceinline__ void row_norm(float (&x)[8], const float (&g)[8], float eps) {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
+    float s = (x[0] * x[0] + x[1] * x[1]) + (x[2] * x[2] + x[3] * x[3]);
+    s += (x[4] * x[4] + x[5] * x[5]) + (x[6] * x[6] + x[7] * x[7]);
 #pragma unroll
     for (int o = D / 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float f = 1.0f / sqrtf(s * (1.0f / D) + eps);
+    const float f = rsqrtf(s * (1.0f / D) + eps);
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = x[i] * f * g[i];
 }
 
-// Which pairs the 8 dims of a lane belong to: pair of dim i = first + i
-// (halves) or first + i/2 (adjacent); role 0: not rotated, 1: first half of
-// the pairs (or adjacent), 2: second half.
-struct RopeLane {
-    int first, role;
-};
-template <int D>
-__device__ __forceinline__ RopeLane rope_lane(int c, int d_rope, int pairs) {
-    const int d = 8 * c - (D - d_rope);   // 8c within the rotated dims (d_rope is a multiple of 16)
-    RopeLane l{0, 0};
-    if (d < 0) return l;
-    if (pairs == CSLA_ROPE_ADJACENT) {
-        l.first = d / 2;
-        l.role = 1;
-    } else {
-        l.role = d < d_rope / 2 ? 1 : 2;
-        l.first = l.role == 1 ? d : d - d_rope / 2;
-    }
-    return l;
+// cos and sin of position times frequency (turns, see KvFreq): the integer
+// product wraps at whole turns, its upper half is the angle to 2^-32 turn.
+// The angle is then within [-pi, pi], where the fast sine and cosine are good
+// to 2^-20, far below the bf16 step (2^-8) that the rotated row is rounded to.
+__device__ __forceinline__ float2 kv_cos_sin(int pos, unsigned long long turn) {
+    const int t = (int)((unsigned long long)(unsigned)pos * turn >> 32);
+    const float x = (float)t * (6.283185307179586f * 0x1p-32f);
+    return make_float2(__cosf(x), __sinf(x));
 }
-// Rotate the row: cs[j] = (cos, sin) of the lane's j-th pair (4 adjacent
-// pairs, or 8 pairs whose other dims another lane holds).  All 32 lanes call it.
-__device__ __forceinline__ void row_rope(float (&x)[8], const RopeLane &l, int c, int d_rope, int pairs,
-                                         const float2 *cs) {
+
+// Rotate the lane's four pairs by cs[j] = (cos, sin).
+__device__ __forceinline__ void row_rope(float (&x)[8], int pairs, const float2 (&cs)[4]) {
     if (pairs == CSLA_ROPE_ADJACENT) {
-        if (l.role == 0) return;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float u = x[2 * j], w = x[2 * j + 1];
@@ -125,13 +136,11 @@ __device__ __forceinline__ void row_rope(float (&x)[8], const RopeLane &l, int c
             x[2 * j + 1] = u * cs[j].y + w * cs[j].x;
         }
     } else {
-        const int lane = threadIdx.x & 31, hop = d_rope / 16;
-        const int src = l.role == 1 ? lane + hop : (l.role == 2 ? lane - hop : lane);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float o = __shfl_sync(0xffffffffu, x[j], src);
-            if (l.role == 1) x[j] = x[j] * cs[j].x - o * cs[j].y;
-            if (l.role == 2) x[j] = o * cs[j].y + x[j] * cs[j].x;
+        for (int j = 0; j < 4; ++j) {
+            const float u = x[j], w = x[4 + j];
+            x[j] = u * cs[j].x - w * cs[j].y;
+            x[4 + j] = u * cs[j].y + w * cs[j].x;
         }
     }
 }

@@ -28,12 +28,15 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     __shared__ int s_pos[kMaxTok];
     __shared__ long long s_dst[kMaxTok];   // element of the token's row in head 0, -1: skipped
     __shared__ float2 s_cs[kMaxTok][D / 2];
+    __shared__ unsigned long long s_turn[D / 2];
     pdl_trigger();
     const int tid = threadIdx.x, c = tid % kLanes;
     const int n0 = blockIdx.x * tok, nt = min(tok, a.bt.N - n0);
     const int rows = nt * 2 * a.HK;   // (token, K or V, head)
     const int half = a.d_rope / 2;
+    const RowLane rl = row_lane<D>(c, a.d_rope, a.pairs);
     if (tid < kMaxTok) s_cnt[tid] = 0;
+    if (tid < half) s_turn[tid] = a.freq.turn[tid];
     pdl_wait();
     CSLA_TL_WAITED();
 
@@ -45,8 +48,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
             if (r < rows) {
                 const int t = r / (2 * a.HK), w = r % (2 * a.HK);
                 const long long n = n0 + t;
-                raw[j] = w < a.HK ? load8<BF16>(a.k_new, n * a.k_stride + (long long)w * D + 8 * c)
-                                  : load8<BF16>(a.v_new, n * a.v_stride + (long long)(w - a.HK) * D + 8 * c);
+                raw[j] = w < a.HK ? load8<BF16>(a.k_new, n * a.k_stride + (long long)w * D, rl)
+                                  : load8<BF16>(a.v_new, n * a.v_stride + (long long)(w - a.HK) * D, rl);
             }
         }
     };
@@ -90,14 +93,11 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     __syncthreads();
     for (int i = tid; i < nt * half; i += kThreads) {
         const int t = i / half, p = i % half;
-        float2 cs;
-        rope_cos_sin(s_pos[t], a.freq.inv[p], &cs.x, &cs.y);
-        s_cs[t][p] = cs;
+        s_cs[t][p] = kv_cos_sin(s_pos[t], s_turn[p]);
     }
-    const RopeLane rl = rope_lane<D>(c, a.d_rope, a.pairs);
     float g[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = a.gamma_k ? a.gamma_k[8 * c + i] : 1.f;
+    for (int i = 0; i < 8; ++i) g[i] = a.gamma_k ? a.gamma_k[i < 4 ? rl.d0 + i : rl.d1 + i - 4] : 1.f;
     __syncthreads();
 
     for (int r0 = 0; r0 < rows; r0 += kFly * kRows) {
@@ -115,18 +115,24 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] = x[i];
             if (a.gamma_k) row_norm<D>(y, g, a.eps);
-            if (half) row_rope(y, rl, c, a.d_rope, a.pairs, &s_cs[t][rl.first]);
+            if (rl.pair >= 0) {
+                float2 cs[4];
+#pragma unroll
+                for (int p = 0; p < 4; ++p) cs[p] = s_cs[t][rl.pair + p];
+                row_rope(y, a.pairs, cs);
+            }
             const bool is_k = w < a.HK;
-            uint4 o;
-            o.x = is_k ? pack_bf16(y[0], y[1]) : pack_bf16(x[0], x[1]);
-            o.y = is_k ? pack_bf16(y[2], y[3]) : pack_bf16(x[2], x[3]);
-            o.z = is_k ? pack_bf16(y[4], y[5]) : pack_bf16(x[4], x[5]);
-            o.w = is_k ? pack_bf16(y[6], y[7]) : pack_bf16(x[6], x[7]);
+            uint2 o[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                o[i] = is_k ? make_uint2(pack_bf16(y[4 * i], y[4 * i + 1]), pack_bf16(y[4 * i + 2], y[4 * i + 3]))
+                            : make_uint2(pack_bf16(x[4 * i], x[4 * i + 1]), pack_bf16(x[4 * i + 2], x[4 * i + 3]));
             const long long dst = s_dst[t];
             if (r < rows && dst >= 0) {
                 const int h = is_k ? w : w - a.HK;
-                uint16_t *out = (is_k ? a.k : a.v) + dst + (long long)h * CSLA_PAGE_TOKENS * D + 8 * c;
-                *reinterpret_cast<uint4 *>(out) = o;
+                uint16_t *out = (is_k ? a.k : a.v) + dst + (long long)h * CSLA_PAGE_TOKENS * D;
+                *reinterpret_cast<uint2 *>(out + rl.d0) = o[0];
+                *reinterpret_cast<uint2 *>(out + rl.d1) = o[1];
             }
         }
     }

@@ -72,6 +72,7 @@ struct Misc {
     uint64_t kv_full[10], kv_empty[10];
     uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
     int bad[kFlags];     // tile's page is not mapped
+    unsigned long long turn[64];   // rotation frequencies
     uint32_t tmem;
     int abort;
 };
@@ -79,6 +80,25 @@ struct Misc {
 template <int D>
 constexpr int smem_bytes() {
     return Cfg<D>::kOffMisc + (int)sizeof(Misc) + 1024;
+}
+
+// Bounded wait of this kernel's roles: they hand tiles over every few hundred
+// nanoseconds, so they poll (each poll parks the warp for the hardware's own
+// short time) instead of asking to be put to sleep.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (int i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 15) == 0) {
+            if (abort && *abort) return false;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                set_dev_err(CSLA_DEVERR_TIMEOUT);
+                if (abort) *abort = 1;
+                return false;
+            }
+        }
+    }
 }
 
 // ---------------------------------------------------------------- items
@@ -189,14 +209,15 @@ __device__ void sched_role(const KvAttendArgs &a, Misc *ms) {
             have = __shfl_sync(0xffffffffu, (int)have, src);
             if (!have) continue;
             const int slot = n % kItems;
-            if (n >= kItems && !warp_all(mbar_wait(&ms->item_empty[slot], (n / kItems - 1) & 1, &ms->abort))) return;
+            if (n >= kItems && !warp_all(wait(&ms->item_empty[slot], (n / kItems - 1) & 1, &ms->abort))) return;
             if (lane == src) ms->item[slot] = it;
+            if (n == 0 && lane == 0) CSLA_TL_MARK_ANY(0);
             mbar_arrive_warp(&ms->item_full[slot]);
             ++n;
             continue;
         }
         const int slot = n % kItems;
-        if (n >= kItems && !warp_all(mbar_wait(&ms->item_empty[slot], (n / kItems - 1) & 1, &ms->abort))) return;
+        if (n >= kItems && !warp_all(wait(&ms->item_empty[slot], (n / kItems - 1) & 1, &ms->abort))) return;
         if (lane == 0) ms->item[slot].end = 1;
         mbar_arrive_warp(&ms->item_full[slot]);
         return;
@@ -206,7 +227,7 @@ __device__ void sched_role(const KvAttendArgs &a, Misc *ms) {
 // The next item for a role's warp; false when there is none (or on an abort).
 __device__ __forceinline__ bool next_item(Misc *ms, int n, Item *it) {
     const int slot = n % kItems;
-    if (!warp_all(mbar_wait(&ms->item_full[slot], (n / kItems) & 1, &ms->abort))) return false;
+    if (!warp_all(wait(&ms->item_full[slot], (n / kItems) & 1, &ms->abort))) return false;
     *it = ms->item[slot];
     mbar_arrive_warp(&ms->item_empty[slot]);
     return !it->end;
@@ -247,7 +268,7 @@ struct Loader {
         using C = Cfg<D>;
         int pg = page(it, t);
         if (issued >= C::kStages &&
-            !warp_all(mbar_wait(&ms->kv_empty[st], (issued / C::kStages - 1) & 1, &ms->abort)))
+            !warp_all(wait(&ms->kv_empty[st], (issued / C::kStages - 1) & 1, &ms->abort)))
             return false;
         const bool bad = pg < 0 || pg >= a.bt.n_pages;
         if (lane == 0) {
@@ -292,7 +313,7 @@ __device__ void load_role(const KvAttendArgs &a, const CUtensorMap &km, const CU
     }
     // copies in flight land before the CTA exits (all have, unless a wait gave up)
     const int from = max(0, L.issued - C::kStages);
-    for (int i = from; i < L.issued; ++i) mbar_wait(&ms->kv_full[i % C::kStages], (i / C::kStages) & 1, nullptr);
+    for (int i = from; i < L.issued; ++i) wait(&ms->kv_full[i % C::kStages], (i / C::kStages) & 1, nullptr);
 }
 
 // ---------------------------------------------------------------- Q role
@@ -300,75 +321,74 @@ template <int D, bool QBF16>
 __device__ void q_role(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
     using C = Cfg<D>;
     constexpr int kLanes = D / 8, kPer = 32 / kLanes;   // lanes per row, rows per step
-    constexpr int kSteps = 32 / kPer, kFly = 4;
+    constexpr int kSteps = 32 / kPer, kGroup = 4;   // steps of a group: their chains of latencies overlap
     const int warp = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31, c = lane % kLanes, sub = lane / kLanes;
     const int G = a.HQ / a.HK;
-    const RopeLane rl = rope_lane<D>(c, a.d_rope, a.pairs);
+    const RowLane rl = row_lane<D>(c, a.d_rope, a.pairs);
     float g[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = a.gamma_q ? a.gamma_q[8 * c + i] : 1.f;
-    float2 cs[8];
-    int cs_pos = -1;
+    for (int i = 0; i < 8; ++i) g[i] = a.gamma_q ? a.gamma_q[i < 4 ? rl.d0 + i : rl.d1 + i - 4] : 1.f;
+    unsigned long long turn[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) turn[j] = rl.pair >= 0 ? ms->turn[rl.pair + j] : 0;
+    // byte offsets of the lane's runs in a row of the operand (row 0's swizzle)
+    const int b0 = (rl.d0 >> 6) * C::kBlk + (rl.d0 & 63) * 2, b1 = (rl.d1 >> 6) * C::kBlk + (rl.d1 & 63) * 2;
     Item it;
     for (int n = 0; next_item(ms, n, &it); ++n) {
-        for (int s = 0; s < 2; ++s) {
-            if (s == 1 && !it.paired) break;
-            const int r0 = it.row0 + 128 * s + 32 * warp;
-            if (n > 0) {
-                if (!warp_all(mbar_wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort))) return;
-                if (!it.paired && !warp_all(mbar_wait(&ms->q_empty[1], (n - 1) & 1, &ms->abort))) return;
-            }
 #pragma unroll 1
-            for (int k0 = 0; k0 < kSteps; k0 += kFly) {
-                if (r0 + k0 * kPer >= it.rows) break;
-                Raw8<QBF16> raw[kFly];
+        for (int s = 0; s <= it.paired; ++s) {
+            const int r0 = it.row0 + 128 * s + 32 * warp;
+            const int steps = min(kSteps, (it.rows - r0 + kPer - 1) / kPer);
+            int tok = (r0 + sub) / G, head = r0 + sub - tok * G;   // the lane's row; kPer further each step
+            bool waited = n == 0;
+#pragma unroll 1
+            for (int k0 = 0; k0 < steps; k0 += kGroup) {
+                Raw8<QBF16> raw[kGroup];
+                int pos[kGroup];
 #pragma unroll
-                for (int k = 0; k < kFly; ++k) {
-                    const int r = min(r0 + (k0 + k) * kPer + sub, it.rows - 1);
-                    const long long at = (long long)(it.n0 + r / G) * a.q_stride + (long long)(it.hk * G + r % G) * D + 8 * c;
-                    raw[k] = load8<QBF16>(a.q, at);
+                for (int k = 0; k < kGroup; ++k) {
+                    const int t = min(tok, it.T - 1);   // (rows that are not there: any)
+                    pos[k] = it.pos0 + t;
+                    raw[k] = load8<QBF16>(a.q, (long long)(it.n0 + t) * a.q_stride + (it.hk * G + head) * D, rl);
+                    for (head += kPer; head >= G; head -= G) ++tok;
+                }
+                // (the first rows' loads are in flight while the operand is still in use)
+                if (!waited) {
+                    if (!warp_all(wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort))) return;
+                    if (!it.paired && !warp_all(wait(&ms->q_empty[1], (n - 1) & 1, &ms->abort))) return;
+                    waited = true;
                 }
 #pragma unroll
-                for (int k = 0; k < kFly; ++k) {
-                    const int rr = r0 + (k0 + k) * kPer + sub, r = min(rr, it.rows - 1);
+                for (int k = 0; k < kGroup; ++k) {
                     float x[8];
                     widen8<QBF16>(raw[k], x);
                     if (a.gamma_q) row_norm<D>(x, g, a.eps);
                     if (a.d_rope) {
-                        const int pos = it.pos0 + r / G;
-                        if (__any_sync(0xffffffffu, pos != cs_pos)) {
-                            cs_pos = pos;
-                            if (rl.role) {
+                        float2 cs[4];
 #pragma unroll
-                                for (int j = 0; j < 8; ++j)
-                                    if (j < 4 || a.pairs == CSLA_ROPE_HALVES)
-                                        rope_cos_sin(pos, a.freq.inv[rl.first + j], &cs[j].x, &cs[j].y);
-                            }
-                        }
-                        row_rope(x, rl, c, a.d_rope, a.pairs, cs);
+                        for (int j = 0; j < 4; ++j) cs[j] = kv_cos_sin(pos[k], turn[j]);   // (turn 0: unchanged)
+                        row_rope(x, a.pairs, cs);
                     }
-                    uint4 o;
-                    o.x = pack_bf16(x[0], x[1]);
-                    o.y = pack_bf16(x[2], x[3]);
-                    o.z = pack_bf16(x[4], x[5]);
-                    o.w = pack_bf16(x[6], x[7]);
                     const int i = 32 * warp + (k0 + k) * kPer + sub;   // row of the operand
-                    const int off = (c >> 3) * C::kBlk + i * 128 + (((c & 7) ^ (i & 7)) << 4);
-                    if (rr < it.rows) {
-                        *reinterpret_cast<uint4 *>(smem + C::kOffQ + s * C::kTileBytes + off) = o;
-                        if (!it.paired) {
-                            uint4 e;   // the rest of the rounding
-                            const uint32_t w[4] = {o.x, o.y, o.z, o.w};
-                            uint32_t d[4];
+                    uint8_t *dst = smem + C::kOffQ + s * C::kTileBytes + i * 128;
+                    const int sw = (i & 7) << 4;
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                d[j] = pack_bf16(x[2 * j] - __uint_as_float(w[j] << 16),
-                                                 x[2 * j + 1] - __uint_as_float(w[j] & 0xFFFF0000u));
-                            e = make_uint4(d[0], d[1], d[2], d[3]);
-                            *reinterpret_cast<uint4 *>(smem + C::kOffQ + C::kTileBytes + off) = e;
-                        }
+                    for (int h = 0; h < 2; ++h) {
+                        const uint2 o = make_uint2(pack_bf16(x[4 * h], x[4 * h + 1]), pack_bf16(x[4 * h + 2], x[4 * h + 3]));
+                        uint8_t *p = dst + ((h ? b1 : b0) ^ sw);
+                        *reinterpret_cast<uint2 *>(p) = o;
+                        if (!it.paired)   // the rest of the rounding
+                            *reinterpret_cast<uint2 *>(p + C::kTileBytes) =
+                                make_uint2(pack_bf16(x[4 * h] - __uint_as_float(o.x << 16),
+                                                     x[4 * h + 1] - __uint_as_float(o.x & 0xFFFF0000u)),
+                                           pack_bf16(x[4 * h + 2] - __uint_as_float(o.y << 16),
+                                                     x[4 * h + 3] - __uint_as_float(o.y & 0xFFFF0000u)));
                     }
                 }
+            }
+            if (!waited) {   // (no row of this warp: the operand's phases are kept in step all the same)
+                if (!warp_all(wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort))) return;
+                if (!it.paired && !warp_all(wait(&ms->q_empty[1], (n - 1) & 1, &ms->abort))) return;
             }
             fence_proxy_async_smem();
             mbar_arrive_warp(&ms->q_full[s]);
@@ -401,7 +421,7 @@ struct Mma {
     // Next tile of the ring; its stage.
     __device__ bool take(int *stage) {
         *stage = taken % C::kStages;
-        if (!warp_all(mbar_wait(&ms->kv_full[*stage], (taken / C::kStages) & 1, &ms->abort))) return false;
+        if (!warp_all(wait(&ms->kv_full[*stage], (taken / C::kStages) & 1, &ms->abort))) return false;
         ++taken;
         tc_fence_after();
         return true;
@@ -446,7 +466,7 @@ struct Mma {
     // O of stream s (+)= P V once P is there
     __device__ bool pv_mma(int s, int stage, bool first) {
         constexpr uint32_t kId = idesc_bf16(128, D, false, true);
-        if (!warp_all(mbar_wait(&ms->p_full[s], p_count[s] & 1, &ms->abort))) return false;
+        if (!warp_all(wait(&ms->p_full[s], p_count[s] & 1, &ms->abort))) return false;
         ++p_count[s];
         tc_fence_after();
         if (lane == 0) {
@@ -464,11 +484,20 @@ struct Mma {
         __syncwarp();
     }
 
+    __device__ void free_q() {
+        commit(&ms->q_empty[0]);
+        commit(&ms->q_empty[1]);
+    }
+
     __device__ bool item_paired(const Item &it, const int *bad, int tiles) {
         int kst, vst;
         if (!take(&kst)) return false;
-        for (int s = 0; s < 2; ++s)
+        for (int s = 0; s < 2; ++s) {
             if (takes(it, s, it.lo)) s_mma(s, kst, true);
+            // Q is free after the stream's last S (or at once, if it has none)
+            const int from = max(it.lo, it.lo1), to = s == 0 ? it.hi0 : it.hi;
+            if ((s == 0 ? it.lo : from) >= to || (takes(it, s, it.lo) && to == it.lo + 1)) commit(&ms->q_empty[s]);
+        }
         commit(&ms->kv_empty[kst]);
         bool first[2] = {true, true};
         for (int t = it.lo; t < it.hi; ++t) {
@@ -487,6 +516,7 @@ struct Mma {
                 if (more && takes(it, s, t + 1)) {
                     if (kst < 0 && !take(&kst)) return false;
                     s_mma(s, kst, true);
+                    if (t + 2 >= it.hi || !takes(it, s, t + 2)) commit(&ms->q_empty[s]);   // its last S
                 }
             }
             if (more) {
@@ -494,8 +524,6 @@ struct Mma {
                 commit(&ms->kv_empty[kst]);
             }
         }
-        commit(&ms->q_empty[0]);
-        commit(&ms->q_empty[1]);
         return true;
     }
     __device__ bool item_single(const Item &it, const int *bad, int tiles) {
@@ -505,6 +533,7 @@ struct Mma {
             s_mma(s, kst, false);
             commit(&ms->kv_empty[kst]);
         }
+        if (it.lo + 2 >= it.hi) free_q();
         for (int t = it.lo; t < it.hi; ++t) {
             const int s = (t - it.lo) & 1;
             if (!take(&vst)) return false;
@@ -516,12 +545,11 @@ struct Mma {
                 if (!take(&kst)) return false;
                 s_mma(s, kst, false);
                 commit(&ms->kv_empty[kst]);
+                if (t + 3 >= it.hi) free_q();
             } else {
                 commit(&ms->o_full[s]);
             }
         }
-        commit(&ms->q_empty[0]);
-        commit(&ms->q_empty[1]);
         return true;
     }
 };
@@ -534,21 +562,42 @@ __device__ void mma_role(uint8_t *smem, Misc *ms) {
     int tiles = 0;
     Item it;
     for (int n = 0; ok && next_item(ms, n, &it); ++n) {
-        for (int s = 0; ok && s < 2; ++s) ok = warp_all(mbar_wait(&ms->q_full[s], n & 1, &ms->abort));
+        for (int s = 0; ok && s < 2; ++s) ok = warp_all(wait(&ms->q_full[s], n & 1, &ms->abort));
         if (!ok) break;
+        if (n == 0 && m.lane == 0) CSLA_TL_MARK_ANY(1);
         tc_fence_after();
         ok = it.paired ? m.item_paired(it, ms->bad, tiles) : m.item_single(it, ms->bad, tiles);
         tiles += it.hi - it.lo;
     }
     // products in flight end before tensor memory is freed (all have, unless a wait gave up)
     m.commit(&ms->drain);
-    mbar_wait(&ms->drain, 0, nullptr);
+    wait(&ms->drain, 0, nullptr);
 }
 
 // ---------------------------------------------------------------- softmax role
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Two fp32 lanes of one 64-bit register.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float *a, float *b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 
@@ -574,76 +623,81 @@ __device__ void softmax_role(const KvAttendArgs &a, Misc *ms, int s) {
         const int t0 = it.paired ? (s == 0 ? it.lo : it.lo1) : it.lo + s;
         const int t1 = it.paired && s == 0 ? it.hi0 : it.hi;
         for (int t = t0; t < t1; t += it.paired ? 1 : 2) {
-            if (!warp_all(mbar_wait(&ms->s_full[s], s_count & 1, &ms->abort))) return;
+            if (!warp_all(wait(&ms->s_full[s], s_count & 1, &ms->abort))) return;
+            if (s == 0 && s_count == 0 && threadIdx.x == 0) CSLA_TL_MARK_ANY(2);
             ++s_count;
             tc_fence_after();
             if (!idle) {
                 const bool bad = ms->bad[(tiles + t - it.lo) % kFlags];
                 const int last = bad ? -1 : pos - t * kTile, from = low - t * kTile;   // visible columns
                 const bool cut = __any_sync(0xffffffffu, last < kTile - 1 || from > 0);
-                float mx = -INFINITY;
+                uint32_t v[4][32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t v[32];
-                    tmem_ld32x32(ts + 32 * c, v);
-                    tmem_wait_ld();
-                    if (cut) {
+                for (int c = 0; c < 4; ++c) tmem_ld32x32(ts + 32 * c, v[c]);
+                tmem_wait_ld();
+                if (cut) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (32 * c + i > last || 32 * c + i < from) v[i] = 0xFF800000u;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(v[i]));
+                            if (32 * c + i > last || 32 * c + i < from) v[c][i] = 0xFF800000u;
                 }
-                const float mn = fmaxf(m, mx * sc);
+                float mx[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    mx[c] = fmaxf(__uint_as_float(v[c][0]), __uint_as_float(v[c][1]));
+#pragma unroll
+                    for (int i = 2; i < 32; i += 2)
+                        mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(v[c][i])), __uint_as_float(v[c][i + 1]));
+                }
+                const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc);
                 const bool grow = mn > m + kGrow;   // (also from -inf)
                 if (__any_sync(0xffffffffu, grow)) {
                     const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - mn)) : 1.f;
                     if (grow) m = mn;
                     l *= f;
                     if (any) {
-#pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t v[32];
-                            tmem_ld32x32(to + 32 * c, v);
+#pragma unroll 1
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld32x16(to + 16 * c, o);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-                            tmem_st32x32(to + 32 * c, v);
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tmem_st32x16(to + 16 * c, o);
                         }
                     }
                 }
                 const float sub = m == -INFINITY ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t sc2 = pack2(sc, sc), sub2 = pack2(-sub, -sub);
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    uint32_t v[32], o[16];
-                    tmem_ld32x32(ts + 32 * c, v);
-                    tmem_wait_ld();
-                    if (cut) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (32 * c + i > last || 32 * c + i < from) v[i] = 0xFF800000u;
-                    }
+                    uint32_t o[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float p0 = ex2(fmaf(__uint_as_float(v[2 * i]), sc, -sub));
-                        const float p1 = ex2(fmaf(__uint_as_float(v[2 * i + 1]), sc, -sub));
-                        sum[i & 3] += p0 + p1;
+                        float x0, x1;
+                        unpack2(fma2(pack2(__uint_as_float(v[c][2 * i]), __uint_as_float(v[c][2 * i + 1])), sc2, sub2), &x0, &x1);
+                        const float p0 = ex2(x0), p1 = ex2(x1);
+                        sum[i & 1] = add2(sum[i & 1], pack2(p0, p1));
                         o[i] = pack_bf16(p0, p1);
                     }
                     tmem_st32x16(ts + 16 * c, o);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                float l0, l1;
+                unpack2(add2(sum[0], sum[1]), &l0, &l1);
+                l += l0 + l1;
                 tmem_wait_st();
                 any = true;
             }
             tc_fence_before();
+            if (s == 0 && s_count == 1 && threadIdx.x == 0) CSLA_TL_MARK_ANY(3);
             mbar_arrive_warp(&ms->p_full[s]);
         }
         tiles += it.hi - it.lo;
         if (t0 < t1) {
-            if (!warp_all(mbar_wait(&ms->o_full[s], o_count & 1, &ms->abort))) return;
+            if (!warp_all(wait(&ms->o_full[s], o_count & 1, &ms->abort))) return;
+            if (s == 0 && o_count == 0 && threadIdx.x == 0) CSLA_TL_MARK_ANY(4);
             ++o_count;
             tc_fence_after();
         }
@@ -703,6 +757,7 @@ __device__ void softmax_role(const KvAttendArgs &a, Misc *ms, int s) {
             }
         }
         tc_fence_before();
+        if (s == 0 && n == 0 && threadIdx.x == 0) CSLA_TL_MARK_ANY(5);
     }
 }
 
@@ -717,6 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
     Misc *ms = reinterpret_cast<Misc *>(smem + C::kOffMisc);
     const int warp = threadIdx.x >> 5;
+    if (threadIdx.x >= 64 && threadIdx.x < 128) ms->turn[threadIdx.x - 64] = a.freq.turn[threadIdx.x - 64];
     if (warp == 12) {
         tmem_alloc(&ms->tmem, 512);
         tmem_relinquish();
@@ -749,16 +805,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
     pdl_trigger();
     pdl_wait();
     CSLA_TL_WAITED();
-    if (warp < 8)
+    // registers: 2 x 128 x 176 + 128 x 96 + 128 x 64 = 65536, the launch's 512 x 128
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         softmax_role<D, OBF16>(a, ms, warp >> 2);
-    else if (warp < 12)
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         q_role<D, QBF16>(a, smem, ms);
-    else if (warp == 12)
-        mma_role<D>(smem, ms);
-    else if (warp == 13)
-        load_role<D>(a, km, vm, smem, ms);
-    else if (warp == 14)
-        sched_role<D>(a, ms);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == 12)
+            mma_role<D>(smem, ms);
+        else if (warp == 13)
+            load_role<D>(a, km, vm, smem, ms);
+        else if (warp == 14)
+            sched_role<D>(a, ms);
+    }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -863,6 +925,18 @@ cudaError_t launch_types(const KvAttendArgs &a, bool qb, bool ob, const CUtensor
 }
 
 }  // namespace
+
+cudaError_t kv_attend_dev_err(unsigned int *bits) {
+    *bits = 0;
+#ifdef CSLA_UNIT_ALONE
+    cudaError_t e = cudaMemcpyFromSymbol(bits, g_dev_err, sizeof(*bits));
+    const unsigned int zero = 0;
+    if (e == cudaSuccess && *bits) e = cudaMemcpyToSymbol(g_dev_err, &zero, sizeof(zero));
+    return e;
+#else
+    return cudaSuccess;
+#endif
+}
 
 cudaError_t launch_kv_attend(const KvAttendArgs &a, bool q_bf16, bool out_bf16, const CUtensorMap &km,
                              const CUtensorMap &vm, int num_sms, long long items, bool join, cudaStream_t stream) {
