@@ -749,22 +749,27 @@ static long long kv_most_tiles(const csla_kv_cfg *c, int max_new, int max_len) {
 }
 
 // Partial rows that a batch within these bounds may need (kv_plan: a chunk
-// is at least kKvMin tiles, and a request at most kKvUnits items, unless its
-// keys are not cut at all).
+// is at least kv_min_tiles tiles, and a request at most kv_units items, unless
+// its keys are not cut at all).
 static long long kv_most_part_rows(const csla_kv_cfg *c, int B, int N, int max_new, int max_len) {
     const long long G = c->HQ / c->HK, HK = c->HK, nt = kv_most_tiles(c, max_new, max_len);
     auto least = [](long long x, long long y) { return x < y ? x : y; };
-    auto parts = [&](long long min_tiles, long long units) {
-        return least((nt + min_tiles - 1) / min_tiles, units / HK > 1 ? units / HK : 1);
+    auto parts = [&](int kind) {
+        const long long m = kv_min_tiles(kind), most = kv_units(kind) / HK > 1 ? kv_units(kind) / HK : 1;
+        return least((nt + m - 1) / m, most);
     };
     if (nt <= 1) return 0;
-    // requests of one row tile
-    const long long t1 = least(max_new, 128 / G);
-    long long rows = least(N, B * t1) * c->HQ * 2 * parts(kKvMinSingle, kKvUnitsSingle);
-    if (max_new * G > 128 && nt > kKvMinPaired) {
-        // each has chunks * 256 * R * HK rows at most, chunks <= units / (R * HK)
-        const long long each = 256ll * kKvUnitsPaired, n = least(B, N * G / 129);
-        rows += least(n * each, (long long)N * c->HQ * parts(kKvMinPaired, kKvUnitsPaired));
+    // (tokens of all requests of a kind) * (parts of a row)
+    long long tokens = least(N, B * least(max_new, kKvFewRows / G));
+    long long rows = parts(kKvFew) > 1 ? tokens * c->HQ * parts(kKvFew) : 0;
+    if (max_new * G > kKvFewRows) {
+        tokens = least(N, B * least(max_new, 128 / G));
+        rows += tokens * c->HQ * 2 * parts(kKvSingle);
+    }
+    if (max_new * G > 128 && parts(kKvPaired) > 1) {
+        // a request has chunks * 256 * R * HK rows at most, chunks <= units / (R * HK)
+        const long long each = 256ll * kv_units(kKvPaired), n = least(B, N * G / 129);
+        rows += least(n * each, (long long)N * c->HQ * parts(kKvPaired));
     }
     return rows;
 }
@@ -816,18 +821,35 @@ int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
         a.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
         a.part_o = reinterpret_cast<float *>(ws + w.o);
     }
-    // one box = 64 dims of a page's 128 rows
-    CUtensorMap km, vm;
+    // which kinds of requests there may be (KvPlan); a box is 64 dims of a
+    // page's rows
+    const int G = cfg->HQ / cfg->HK, least_rows = q_start ? G : a.bt.T * G;
+    const long long most_rows = q_start ? (long long)max_new * G : least_rows;
+    const bool q16 = q_dtype == CSLA_BF16, o16 = out_dtype == CSLA_BF16;
     const uint64_t cache_rows = (uint64_t)kv->n_pages * cfg->HK * CSLA_PAGE_TOKENS;
-    if (!encode_bf16_2d(&km, kv->k, cfg->D, cache_rows, CSLA_PAGE_TOKENS) ||
-        !encode_bf16_2d(&vm, kv->v, cfg->D, cache_rows, CSLA_PAGE_TOKENS))
-        return CSLA_ERR_CUDA;
-    // items at most: the grid of a small call
-    const int G = cfg->HQ / cfg->HK;
     const long long nt = kv_most_tiles(cfg, max_new, max_len);
-    const long long items = ((long long)N * G / 256 + B) * cfg->HK * ((nt + kKvMinSingle - 1) / kKvMinSingle);
-    return cuda_status(launch_kv_attend(a, q_dtype == CSLA_BF16, out_dtype == CSLA_BF16, km, vm, num_sms_current(),
-                                        items, rows > 0, reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (least_rows <= kKvFewRows) {
+        CUtensorMap km, vm;
+        if (!encode_bf16_2d(&km, kv->k, cfg->D, cache_rows, kv_few_box(cfg->D)) ||
+            !encode_bf16_2d(&vm, kv->v, cfg->D, cache_rows, kv_few_box(cfg->D)))
+            return CSLA_ERR_CUDA;
+        const long long m = kv_min_tiles(kKvFew);
+        e = launch_kv_few(a, q16, o16, (int)(most_rows < kKvFewRows ? most_rows : kKvFewRows), km, vm,
+                          num_sms_current(), (long long)B * cfg->HK * ((nt + m - 1) / m), st);
+    }
+    if (e == cudaSuccess && most_rows > kKvFewRows) {
+        CUtensorMap km, vm;
+        if (!encode_bf16_2d(&km, kv->k, cfg->D, cache_rows, CSLA_PAGE_TOKENS) ||
+            !encode_bf16_2d(&vm, kv->v, cfg->D, cache_rows, CSLA_PAGE_TOKENS))
+            return CSLA_ERR_CUDA;
+        const long long m = kv_min_tiles(kKvSingle);
+        e = launch_kv_attend(a, q16, o16, km, vm, num_sms_current(),
+                             ((long long)N * G / 256 + B) * cfg->HK * ((nt + m - 1) / m), st);
+    }
+    if (e == cudaSuccess && rows) e = launch_kv_join(a, o16, num_sms_current(), st);
+    return cuda_status(e);
 }
 
 }  // extern "C"

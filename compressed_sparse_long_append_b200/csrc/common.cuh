@@ -111,7 +111,7 @@ __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.lau
 // points of interest) into g_timeline, read back with csla_timeline_read().  In normal builds the hooks compile to nothing.
 enum TimelineKernel : uint32_t {
     kTlCompress = 1, kTlTailUpdate, kTlIqProject, kTlIqProjectWide, kTlIndexer, kTlTopk, kTlPrepQ, kTlAttend,
-    kTlCombine, kTlKvAppend, kTlKvAttend, kTlKvJoin
+    kTlCombine, kTlKvAppend, kTlKvAttend, kTlKvJoin, kTlKvFew
 };
 #ifdef CSLA_TIMELINE
 constexpr int kTimelineMarks = 8;

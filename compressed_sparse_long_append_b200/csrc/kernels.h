@@ -310,17 +310,20 @@ struct KvAttendArgs {
 };
 
 // How the attention cuts a request of T new tokens (context L): a function of
-// T, L and the layer alone.  rows = T*G rows per KV head.  At most 128 rows:
-// one row tile (R = 1) whose two streams take key tiles in turn.  More: R row
-// tiles of 256.  Keys are cut into chunks of c tiles, nch at most per row
-// tile, so that a request of few row tiles still fills the SMs.
+// T, L and the layer alone.  rows = T*G rows per KV head.
+//   few     up to 32 rows: kv_few_kernel, R = 1;
+//   single  up to 128 rows: kv_attend_kernel, R = 1, its two streams take key tiles in turn;
+//   paired  more: kv_attend_kernel, R row tiles of 256.
+// Keys are cut into chunks of c tiles, nch at most per row tile, so that a
+// request of few row tiles still fills the SMs.
+enum { kKvFew = 0, kKvSingle = 1, kKvPaired = 2 };
 struct KvPlan {
-    int rows, R, paired, c, nch, T, G, heads_inside;
+    int rows, R, kind, c, nch, T, G, heads_inside;
 };
-constexpr int kKvUnitsSingle = 296;   // items a long request of one row tile is cut into (all heads)
-constexpr int kKvUnitsPaired = 148;
-constexpr int kKvMinSingle = 4;       // tiles per chunk at least
-constexpr int kKvMinPaired = 8;
+constexpr int kKvFewRows = 32;
+// items that a long request is cut into (all heads), and the least tiles of a chunk, by kind
+__host__ __device__ constexpr int kv_units(int kind) { return kind == kKvPaired ? 148 : 296; }
+__host__ __device__ constexpr int kv_min_tiles(int kind) { return kind == kKvPaired ? 8 : (kind == kKvSingle ? 4 : 2); }
 
 // Key tiles of row tile i: [lo, hi); of its two halves: first half [lo, hi0), second [lo1, hi).
 // [k_lo, k_hi): the positions that some row sees.
@@ -329,7 +332,7 @@ struct KvRange {
 };
 __host__ __device__ inline KvRange kv_range(const KvPlan &p, int pos0, int i, int window) {
     KvRange g;
-    const int r0 = p.paired ? 256 * i : 0, rows_left = p.rows - r0;
+    const int r0 = p.kind == kKvPaired ? 256 * i : 0, rows_left = p.rows - r0;
     const int n = rows_left < 256 ? rows_left : 256;
     const int first = r0 / p.G, last = (r0 + n - 1) / p.G;
     g.k_lo = window > 0 && pos0 + first - window + 1 > 0 ? pos0 + first - window + 1 : 0;
@@ -338,7 +341,7 @@ __host__ __device__ inline KvRange kv_range(const KvPlan &p, int pos0, int i, in
     g.hi = (g.k_hi + CSLA_PAGE_TOKENS - 1) / CSLA_PAGE_TOKENS;
     g.hi0 = g.hi;
     g.lo1 = g.lo;
-    if (p.paired) {
+    if (p.kind == kKvPaired) {
         if (n <= 128) {
             g.lo1 = g.hi;
         } else {
@@ -354,18 +357,18 @@ __host__ __device__ inline KvPlan kv_plan(int T, int L, int G, int HK, int windo
     p.T = T;
     p.G = G;
     p.rows = T * G;
-    p.paired = p.rows > 128;
-    p.R = p.paired ? (p.rows + 255) / 256 : 1;
+    p.kind = p.rows <= kKvFewRows ? kKvFew : (p.rows <= 128 ? kKvSingle : kKvPaired);
+    p.R = p.kind == kKvPaired ? (p.rows + 255) / 256 : 1;
     // key tiles of the longest row tile (with a window: an upper bound)
     int nt = (L - 1) / CSLA_PAGE_TOKENS + 1;
     if (window > 0 && window < L) {
-        const int w = (window + (p.paired ? 256 / G + 1 : T) + CSLA_PAGE_TOKENS - 2) / CSLA_PAGE_TOKENS + 1;
+        const int w = (window + (p.kind == kKvPaired ? 256 / G + 1 : T) + CSLA_PAGE_TOKENS - 2) / CSLA_PAGE_TOKENS + 1;
         nt = w < nt ? w : nt;
     }
     // (32-bit divisions only: this runs ahead of every item's first load)
-    const unsigned most = (p.paired ? kKvUnitsPaired : kKvUnitsSingle) / (unsigned)(HK * p.R);   // chunks
+    const unsigned most = kv_units(p.kind) / (unsigned)(HK * p.R);   // chunks
     int c = most > 1 ? (int)((nt + most - 1) / most) : nt;
-    const int least = p.paired ? kKvMinPaired : kKvMinSingle;
+    const int least = kv_min_tiles(p.kind);
     if (c < least) c = least;
     if (c > nt) c = nt;
     p.c = c;
@@ -376,19 +379,22 @@ __host__ __device__ inline KvPlan kv_plan(int T, int L, int G, int HK, int windo
 }
 // Partials of a row of row tile g: 1 means it is written out at once.
 __host__ __device__ inline int kv_parts(const KvPlan &p, const KvRange &g) {
-    const int nt = g.hi - g.lo;
-    if (p.paired) return (nt + p.c - 1) / p.c;
-    return nt == 1 ? 1 : 2 * ((nt + p.c - 1) / p.c);
+    const int nt = g.hi - g.lo, n = (nt + p.c - 1) / p.c;
+    return p.kind == kKvSingle && nt > 1 ? 2 * n : n;
 }
 // Partial rows that a request may need.
 __host__ __device__ inline long long kv_part_rows(const KvPlan &p, int T, int HQ) {
-    const long long parts = p.paired ? p.nch : 2ll * p.nch;
-    if (p.paired ? p.nch == 1 : p.c == 1) return 0;
-    return parts * T * HQ;
+    if (p.kind == kKvSingle ? p.c == 1 : p.nch == 1) return 0;
+    return (p.kind == kKvSingle ? 2ll : 1ll) * p.nch * T * HQ;
 }
+cudaError_t launch_kv_few(const KvAttendArgs &a, bool q_bf16, bool out_bf16, int rows, const CUtensorMap &km,
+                          const CUtensorMap &vm, int num_sms, long long items, cudaStream_t stream);
+// Tokens of a ring stage of kv_few_kernel (the height of its tensor maps' boxes).
+inline int kv_few_box(int D) { return D == 128 ? 64 : 128; }
 // Reads and clears the device error word of kv_attend.cu's unit (0 where it shares the library's).
 cudaError_t kv_attend_dev_err(unsigned int *bits);
 cudaError_t launch_kv_attend(const KvAttendArgs &a, bool q_bf16, bool out_bf16, const CUtensorMap &km,
-                             const CUtensorMap &vm, int num_sms, long long items, bool join, cudaStream_t stream);
+                             const CUtensorMap &vm, int num_sms, long long items, cudaStream_t stream);
+cudaError_t launch_kv_join(const KvAttendArgs &a, bool out_bf16, int num_sms, cudaStream_t stream);
 
 }  // namespace csla

@@ -43,6 +43,90 @@ __device__ __forceinline__ KvReq kv_request(const KvBatch &a, int b, int max_new
     return r;
 }
 
+// ------------------------------------------------------------ items of a persistent CTA
+// A warp's walk over the batch: the items of the requests whose kind is in
+// `kinds`, numbered through the batch; this CTA takes item c, 2*grid-1-c,
+// 2*grid+c, ... (there and back, so that sizes that fall along the
+// numbering even out).  32 requests are held at a time, one per lane.
+struct KvWalk {
+    int first = -32, total = 0, before = 0, round = 0, incl = 0;
+    long long part_before = 0, part_total = 0, part_excl = 0;
+    KvReq r{};
+    KvPlan p{};
+
+    // The next item: true with *src = the lane that holds its request (its r, p
+    // and the request's first partial row part_before + part_excl) and *local
+    // = its number in the request; false when there is none.  All lanes call it.
+    __device__ __forceinline__ bool next(const KvAttendArgs &a, unsigned kinds, int *src, int *local) {
+        const int lane = threadIdx.x & 31, grid = gridDim.x;
+        const int u = (round & 1) ? (round + 1) * grid - 1 - (int)blockIdx.x : round * grid + (int)blockIdx.x;
+        ++round;
+        while (u >= before + total) {
+            before += total;
+            part_before += part_total;
+            first += 32;
+            if (first >= a.bt.B) return false;
+            const int b = first + lane;
+            int items = 0;
+            long long parts = 0;
+            if (b < a.bt.B) {
+                r = kv_request(a.bt, b, a.max_new, a.max_len);
+                if (r.err && blockIdx.x == 0) set_dev_err(r.err);
+                if (r.ok) {
+                    p = kv_plan(r.T, r.L, a.HQ / a.HK, a.HK, a.window, a.D);
+                    items = (kinds >> p.kind) & 1 ? a.HK * p.R * p.nch : 0;
+                    parts = kv_part_rows(p, r.T, a.HQ);
+                }
+            }
+            incl = items;
+            long long pincl = parts;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                const long long w = __shfl_up_sync(0xffffffffu, pincl, o);
+                if (lane >= o) {
+                    incl += v;
+                    pincl += w;
+                }
+            }
+            part_excl = pincl - parts;
+            total = __shfl_sync(0xffffffffu, incl, 31);
+            part_total = __shfl_sync(0xffffffffu, pincl, 31);
+            if (items && parts && blockIdx.x == 0) a.part_base[b] = part_before + part_excl;
+        }
+        *src = __ffs(__ballot_sync(0xffffffffu, incl > u - before)) - 1;
+        const int prev = __shfl_sync(0xffffffffu, incl, max(*src - 1, 0));
+        *local = u - before - (*src ? prev : 0);
+        return true;
+    }
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGrow = 8.0f;   // log2 growth of a row's maximum that its sums tolerate before they are rescaled
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// Bounded wait of the attention kernels' roles: they hand tiles over every few
+// hundred nanoseconds, so they poll (each poll parks the warp for the
+// hardware's own short time) instead of asking to be put to sleep.
+__device__ __forceinline__ bool kv_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (int i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 15) == 0) {
+            if (abort && *abort) return false;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                set_dev_err(CSLA_DEVERR_TIMEOUT);
+                if (abort) *abort = 1;
+                return false;
+            }
+        }
+    }
+}
+
 // ------------------------------------------------------------ rows, 8 dims per lane
 // A row of D dims is held by D/8 consecutive lanes of a warp, 8 dims per lane
 // in two runs of four, d0.. and d1..: lanes of unrotated dims hold eight

@@ -33,12 +33,10 @@
 namespace csla {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kThreads = 512;
 constexpr int kTile = CSLA_PAGE_TOKENS;   // keys per tile
 constexpr int kItems = 3;                 // items in flight between the roles
 constexpr int kFlags = 16;                // tiles of page flags
-constexpr float kGrow = 8.0f;             // log2 growth of the maximum that O tolerates
 
 template <int D>
 struct Cfg {
@@ -82,25 +80,6 @@ constexpr int smem_bytes() {
     return Cfg<D>::kOffMisc + (int)sizeof(Misc) + 1024;
 }
 
-// Bounded wait of this kernel's roles: they hand tiles over every few hundred
-// nanoseconds, so they poll (each poll parks the warp for the hardware's own
-// short time) instead of asking to be put to sleep.
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (int i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 15) == 0) {
-            if (abort && *abort) return false;
-            if (globaltimer_ns() - t0 > kWaitLimitNs) {
-                set_dev_err(CSLA_DEVERR_TIMEOUT);
-                if (abort) *abort = 1;
-                return false;
-            }
-        }
-    }
-}
-
 // ---------------------------------------------------------------- items
 // First item of stream s, and whether it takes tile t.
 __device__ __forceinline__ bool takes(const Item &it, int s, int t) {
@@ -127,7 +106,7 @@ __device__ __forceinline__ bool make_item(const KvAttendArgs &a, const KvReq &r,
     const int lo = g.lo + j * p.c, hi = min(g.hi, lo + p.c);
     if (lo >= hi) return false;
     it->end = 0;
-    it->paired = p.paired;
+    it->paired = p.kind == kKvPaired;
     it->n0 = r.n0;
     it->T = r.T;
     it->pos0 = r.L - r.T;
@@ -142,92 +121,36 @@ __device__ __forceinline__ bool make_item(const KvAttendArgs &a, const KvReq &r,
     it->k_lo = g.k_lo;
     it->k_hi = g.k_hi;
     const int parts = kv_parts(p, g);
-    it->part = parts > 1 ? (p.paired ? j : 2 * j) : -1;
+    it->part = parts > 1 ? (p.kind == kKvPaired ? j : 2 * j) : -1;
     it->base = base;
     return true;
 }
 
-template <int D>
 __device__ void sched_role(const KvAttendArgs &a, Misc *ms) {
     const int lane = threadIdx.x & 31;
-    const int G = a.HQ / a.HK, grid = gridDim.x;
-    int first = -32, total = 0;            // requests [first, first + 32) are held, one per lane
-    int before = 0;                        // items before them
-    long long part_before = 0, part_total = 0;
-    KvReq r{};
-    KvPlan p{};
-    int incl = 0;
-    long long part_excl = 0;
-    int n = 0;                             // items published
-    for (int round = 0;; ++round) {
-        const int u = (round & 1) ? (round + 1) * grid - 1 - (int)blockIdx.x : round * grid + (int)blockIdx.x;
-        bool none = false;
-        while (u >= before + total) {
-            before += total;
-            part_before += part_total;
-            first += 32;
-            if (first >= a.bt.B) {
-                none = true;
-                break;
-            }
-            const int b = first + lane;
-            int items = 0;
-            long long parts = 0;
-            if (b < a.bt.B) {
-                r = kv_request(a.bt, b, a.max_new, a.max_len);
-                if (r.err && blockIdx.x == 0) set_dev_err(r.err);
-                if (r.ok) {
-                    p = kv_plan(r.T, r.L, G, a.HK, a.window, D);
-                    items = a.HK * p.R * p.nch;
-                    parts = kv_part_rows(p, r.T, a.HQ);
-                }
-            }
-            incl = items;
-            long long pincl = parts;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                const long long w = __shfl_up_sync(0xffffffffu, pincl, o);
-                if (lane >= o) {
-                    incl += v;
-                    pincl += w;
-                }
-            }
-            part_excl = pincl - parts;
-            total = __shfl_sync(0xffffffffu, incl, 31);
-            part_total = __shfl_sync(0xffffffffu, pincl, 31);
-            if (items && a.part_base && blockIdx.x == 0) a.part_base[b] = part_before + part_excl;
-        }
+    KvWalk w;
+    for (int n = 0;;) {
+        int src = 0, local = 0;
+        const bool more = w.next(a, 1u << kKvSingle | 1u << kKvPaired, &src, &local);
         Item it;
         it.end = 1;
         bool have = true;
-        if (!none) {
-            const int src = __ffs(__ballot_sync(0xffffffffu, incl > u - before)) - 1;
-            const int prev = __shfl_sync(0xffffffffu, incl, max(src - 1, 0));
-            if (lane == src)
-                have = make_item(a, r, p, u - before - (src ? prev : 0), part_before + part_excl, &it);
-            have = __shfl_sync(0xffffffffu, (int)have, src);
-            if (!have) continue;
-            const int slot = n % kItems;
-            if (n >= kItems && !warp_all(wait(&ms->item_empty[slot], (n / kItems - 1) & 1, &ms->abort))) return;
-            if (lane == src) ms->item[slot] = it;
-            if (n == 0 && lane == 0) CSLA_TL_MARK_ANY(0);
-            mbar_arrive_warp(&ms->item_full[slot]);
-            ++n;
-            continue;
-        }
+        if (more && lane == src) have = make_item(a, w.r, w.p, local, w.part_before + w.part_excl, &it);
+        if (!__shfl_sync(0xffffffffu, (int)have, src)) continue;   // (a chunk behind a short row tile's keys)
         const int slot = n % kItems;
-        if (n >= kItems && !warp_all(wait(&ms->item_empty[slot], (n / kItems - 1) & 1, &ms->abort))) return;
-        if (lane == 0) ms->item[slot].end = 1;
+        if (n >= kItems && !warp_all(kv_wait(&ms->item_empty[slot], (n / kItems - 1) & 1, &ms->abort))) return;
+        if (lane == src) ms->item[slot] = it;
+        if (n == 0 && lane == 0) CSLA_TL_MARK_ANY(0);
         mbar_arrive_warp(&ms->item_full[slot]);
-        return;
+        if (!more) return;
+        ++n;
     }
 }
 
 // The next item for a role's warp; false when there is none (or on an abort).
 __device__ __forceinline__ bool next_item(Misc *ms, int n, Item *it) {
     const int slot = n % kItems;
-    if (!warp_all(wait(&ms->item_full[slot], (n / kItems) & 1, &ms->abort))) return false;
+    if (!warp_all(kv_wait(&ms->item_full[slot], (n / kItems) & 1, &ms->abort))) return false;
     *it = ms->item[slot];
     mbar_arrive_warp(&ms->item_empty[slot]);
     return !it->end;
@@ -268,7 +191,7 @@ struct Loader {
         using C = Cfg<D>;
         int pg = page(it, t);
         if (issued >= C::kStages &&
-            !warp_all(wait(&ms->kv_empty[st], (issued / C::kStages - 1) & 1, &ms->abort)))
+            !warp_all(kv_wait(&ms->kv_empty[st], (issued / C::kStages - 1) & 1, &ms->abort)))
             return false;
         const bool bad = pg < 0 || pg >= a.bt.n_pages;
         if (lane == 0) {
@@ -313,7 +236,7 @@ __device__ void load_role(const KvAttendArgs &a, const CUtensorMap &km, const CU
     }
     // copies in flight land before the CTA exits (all have, unless a wait gave up)
     const int from = max(0, L.issued - C::kStages);
-    for (int i = from; i < L.issued; ++i) wait(&ms->kv_full[i % C::kStages], (i / C::kStages) & 1, nullptr);
+    for (int i = from; i < L.issued; ++i) kv_wait(&ms->kv_full[i % C::kStages], (i / C::kStages) & 1, nullptr);
 }
 
 // ---------------------------------------------------------------- Q role
@@ -354,8 +277,8 @@ __device__ void q_role(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
                 }
                 // (the first rows' loads are in flight while the operand is still in use)
                 if (!waited) {
-                    if (!warp_all(wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort))) return;
-                    if (!it.paired && !warp_all(wait(&ms->q_empty[1], (n - 1) & 1, &ms->abort))) return;
+                    if (!warp_all(kv_wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort))) return;
+                    if (!it.paired && !warp_all(kv_wait(&ms->q_empty[1], (n - 1) & 1, &ms->abort))) return;
                     waited = true;
                 }
 #pragma unroll
@@ -387,8 +310,8 @@ __device__ void q_role(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
                 }
             }
             if (!waited) {   // (no row of this warp: the operand's phases are kept in step all the same)
-                if (!warp_all(wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort))) return;
-                if (!it.paired && !warp_all(wait(&ms->q_empty[1], (n - 1) & 1, &ms->abort))) return;
+                if (!warp_all(kv_wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort))) return;
+                if (!it.paired && !warp_all(kv_wait(&ms->q_empty[1], (n - 1) & 1, &ms->abort))) return;
             }
             fence_proxy_async_smem();
             mbar_arrive_warp(&ms->q_full[s]);
@@ -421,7 +344,7 @@ struct Mma {
     // Next tile of the ring; its stage.
     __device__ bool take(int *stage) {
         *stage = taken % C::kStages;
-        if (!warp_all(wait(&ms->kv_full[*stage], (taken / C::kStages) & 1, &ms->abort))) return false;
+        if (!warp_all(kv_wait(&ms->kv_full[*stage], (taken / C::kStages) & 1, &ms->abort))) return false;
         ++taken;
         tc_fence_after();
         return true;
@@ -466,7 +389,7 @@ struct Mma {
     // O of stream s (+)= P V once P is there
     __device__ bool pv_mma(int s, int stage, bool first) {
         constexpr uint32_t kId = idesc_bf16(128, D, false, true);
-        if (!warp_all(wait(&ms->p_full[s], p_count[s] & 1, &ms->abort))) return false;
+        if (!warp_all(kv_wait(&ms->p_full[s], p_count[s] & 1, &ms->abort))) return false;
         ++p_count[s];
         tc_fence_after();
         if (lane == 0) {
@@ -562,7 +485,7 @@ __device__ void mma_role(uint8_t *smem, Misc *ms) {
     int tiles = 0;
     Item it;
     for (int n = 0; ok && next_item(ms, n, &it); ++n) {
-        for (int s = 0; ok && s < 2; ++s) ok = warp_all(wait(&ms->q_full[s], n & 1, &ms->abort));
+        for (int s = 0; ok && s < 2; ++s) ok = warp_all(kv_wait(&ms->q_full[s], n & 1, &ms->abort));
         if (!ok) break;
         if (n == 0 && m.lane == 0) CSLA_TL_MARK_ANY(1);
         tc_fence_after();
@@ -571,16 +494,10 @@ __device__ void mma_role(uint8_t *smem, Misc *ms) {
     }
     // products in flight end before tensor memory is freed (all have, unless a wait gave up)
     m.commit(&ms->drain);
-    wait(&ms->drain, 0, nullptr);
+    kv_wait(&ms->drain, 0, nullptr);
 }
 
 // ---------------------------------------------------------------- softmax role
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 // Two fp32 lanes of one 64-bit register.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
     uint64_t r;
@@ -623,7 +540,7 @@ __device__ void softmax_role(const KvAttendArgs &a, Misc *ms, int s) {
         const int t0 = it.paired ? (s == 0 ? it.lo : it.lo1) : it.lo + s;
         const int t1 = it.paired && s == 0 ? it.hi0 : it.hi;
         for (int t = t0; t < t1; t += it.paired ? 1 : 2) {
-            if (!warp_all(wait(&ms->s_full[s], s_count & 1, &ms->abort))) return;
+            if (!warp_all(kv_wait(&ms->s_full[s], s_count & 1, &ms->abort))) return;
             if (s == 0 && s_count == 0 && threadIdx.x == 0) CSLA_TL_MARK_ANY(2);
             ++s_count;
             tc_fence_after();
@@ -696,7 +613,7 @@ __device__ void softmax_role(const KvAttendArgs &a, Misc *ms, int s) {
         }
         tiles += it.hi - it.lo;
         if (t0 < t1) {
-            if (!warp_all(wait(&ms->o_full[s], o_count & 1, &ms->abort))) return;
+            if (!warp_all(kv_wait(&ms->o_full[s], o_count & 1, &ms->abort))) return;
             if (s == 0 && o_count == 0 && threadIdx.x == 0) CSLA_TL_MARK_ANY(4);
             ++o_count;
             tc_fence_after();
@@ -819,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
         else if (warp == 13)
             load_role<D>(a, km, vm, smem, ms);
         else if (warp == 14)
-            sched_role<D>(a, ms);
+            sched_role(a, ms);
     }
     __syncwarp();
     tc_fence_before();
@@ -900,28 +817,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_c
 }
 
 template <int D, bool QB, bool OB>
-cudaError_t launch(const KvAttendArgs &a, const CUtensorMap &km, const CUtensorMap &vm, int num_sms, long long items,
-                   bool join, cudaStream_t s) {
+cudaError_t launch(const KvAttendArgs &a, const CUtensorMap &km, const CUtensorMap &vm, unsigned grid, cudaStream_t s) {
     auto kern = kv_attend_kernel<D, QB, OB>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)(items < num_sms ? items : num_sms);
-    e = launch_pdl(kern, dim3(grid), dim3(kThreads), smem_bytes<D>(), s, a, km, vm);
-    if (e != cudaSuccess || !join) return e;
-    const long long rows = (long long)min(a.max_new, a.bt.N) * a.HQ;
-    long long x = (rows + kJoinWarps - 1) / kJoinWarps;
-    const long long most = 8ll * num_sms / a.bt.B + 1;
-    if (x > most) x = most;
-    return launch_pdl(kv_join_kernel<D, OB>, dim3((unsigned)x, (unsigned)a.bt.B), dim3(32 * kJoinWarps), 0, s, a);
+    return launch_pdl(kern, dim3(grid), dim3(kThreads), smem_bytes<D>(), s, a, km, vm);
 }
-
 template <int D>
 cudaError_t launch_types(const KvAttendArgs &a, bool qb, bool ob, const CUtensorMap &km, const CUtensorMap &vm,
-                         int num_sms, long long items, bool join, cudaStream_t s) {
-    if (qb) return ob ? launch<D, true, true>(a, km, vm, num_sms, items, join, s)
-                      : launch<D, true, false>(a, km, vm, num_sms, items, join, s);
-    return ob ? launch<D, false, true>(a, km, vm, num_sms, items, join, s)
-              : launch<D, false, false>(a, km, vm, num_sms, items, join, s);
+                         unsigned grid, cudaStream_t s) {
+    if (qb) return ob ? launch<D, true, true>(a, km, vm, grid, s) : launch<D, true, false>(a, km, vm, grid, s);
+    return ob ? launch<D, false, true>(a, km, vm, grid, s) : launch<D, false, false>(a, km, vm, grid, s);
 }
 
 }  // namespace
@@ -939,9 +845,23 @@ cudaError_t kv_attend_dev_err(unsigned int *bits) {
 }
 
 cudaError_t launch_kv_attend(const KvAttendArgs &a, bool q_bf16, bool out_bf16, const CUtensorMap &km,
-                             const CUtensorMap &vm, int num_sms, long long items, bool join, cudaStream_t stream) {
-    return a.D == 64 ? launch_types<64>(a, q_bf16, out_bf16, km, vm, num_sms, items, join, stream)
-                     : launch_types<128>(a, q_bf16, out_bf16, km, vm, num_sms, items, join, stream);
+                             const CUtensorMap &vm, int num_sms, long long items, cudaStream_t stream) {
+    const unsigned grid = (unsigned)(items < num_sms ? items : num_sms);
+    return a.D == 64 ? launch_types<64>(a, q_bf16, out_bf16, km, vm, grid, stream)
+                     : launch_types<128>(a, q_bf16, out_bf16, km, vm, grid, stream);
+}
+
+cudaError_t launch_kv_join(const KvAttendArgs &a, bool out_bf16, int num_sms, cudaStream_t stream) {
+    const long long rows = (long long)(a.max_new < a.bt.N ? a.max_new : a.bt.N) * a.HQ;
+    long long x = (rows + kJoinWarps - 1) / kJoinWarps;
+    const long long most = 8ll * num_sms / a.bt.B + 1;
+    if (x > most) x = most;
+    const dim3 grid((unsigned)x, (unsigned)a.bt.B), block(32 * kJoinWarps);
+    if (a.D == 64)
+        return out_bf16 ? launch_pdl(kv_join_kernel<64, true>, grid, block, 0, stream, a)
+                        : launch_pdl(kv_join_kernel<64, false>, grid, block, 0, stream, a);
+    return out_bf16 ? launch_pdl(kv_join_kernel<128, true>, grid, block, 0, stream, a)
+                    : launch_pdl(kv_join_kernel<128, false>, grid, block, 0, stream, a);
 }
 
 }  // namespace csla

@@ -1,0 +1,553 @@
+// kv_few.cu -- attention of requests of few rows (up to 32 per KV head:
+// decode, a few drafted tokens) over the dense paged cache: a part of
+// csla_kv_attend.
+//
+//   s_j = scale <R(p) norm(q), K_j>,  o = sum_j e^{s_j} V_j / (e^{sink} + sum_j e^{s_j})
+//
+// Each K and V byte is used by at most 32 rows, so the kernel is bound by
+// HBM and by how much of it is asked for at a time; the products are small.  So
+// they stay in registers: mma.sync on 16-row fragments needs no tensor memory, no handing
+// over between roles and no padding to 128 rows, and its rate is several times what the bytes leave time for.
+//
+// An item is a chunk of pages of one (request, KV head).  Two persistent CTAs
+// per SM; a CTA's producer warp walks the batch and streams K and V stages (16 KB each)
+// by TMA into a ring, across items; four consumer warps each take
+// a quarter of the stage's tokens with a running maximum m, sum l and O of their own:
+//   S = Q K^T (Q as two bf16 terms: the rounding of the rotated query is kept),
+//   P = 2^(S - m) straight from the accumulators into the A operand of O += P V.
+// At the end of an item the four (m, l, O) are joined through shared memory in
+// a fixed order and written out, or left as a partial for kv_join_kernel
+// when the request's keys were cut.
+#include "kv.cuh"
+
+namespace csla {
+namespace {
+
+constexpr int kConsumers = 4;
+constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kItems = 4;
+constexpr int kMaxStages = 6;
+
+template <int D, int MT>
+struct Cfg {
+    static constexpr int kTok = D == 128 ? 64 : 128;      // tokens per stage
+    static constexpr int kKB = D / 64;                    // 128-byte blocks of a row
+    static constexpr int kBlk = kTok * 128;
+    static constexpr int kStage = kKB * kBlk;             // 16 KB
+    static constexpr int kPer = CSLA_PAGE_TOKENS / kTok;  // stages per page
+    static constexpr int kStages = MT == 1 ? 6 : 5;
+    static constexpr int kWT = kTok / kConsumers;         // tokens of a stage per warp
+    static constexpr int kOut = MT * 16 * D * 2;          // half the dims of one warp's O
+    // work area: the Q terms [2][MT*16][D] bf16; at an item's end half of two O, and their (m, l)
+    static constexpr int kOffWork = kStages * kStage;
+    static constexpr int kMl = MT * 32 * 16;              // (m, l) of both row groups, per lane
+    static constexpr int kOffMl = kOffWork + 2 * kOut;
+    static constexpr int kOffMisc = kOffMl + 2 * kMl;
+    static_assert(2 * MT * 16 * D * 2 <= 2 * kOut, "Q fits in the work area");
+};
+
+struct Item {
+    int end, n0, T, pos0, slot, hk, rows;
+    int lo, hi;          // pages
+    int k_lo, k_hi;      // positions that some row sees
+    int part;            // partial's index, -1: written out
+    long long base;
+};
+
+struct Misc {
+    Item item[kItems];
+    uint64_t item_full[kItems], item_empty[kItems], full[kMaxStages], empty[kMaxStages];
+    int bad[kMaxStages];
+    unsigned long long turn[64];
+    int abort;
+};
+
+template <int D, int MT>
+constexpr int smem_bytes() {
+    return Cfg<D, MT>::kOffMisc + (int)sizeof(Misc) + 1024;
+}
+
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void sync_consumers() {
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory");
+}
+// The barrier, and whether `ok` holds in every consumer thread.
+__device__ __forceinline__ bool all_consumers(bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)ok), "n"(32 * kConsumers)
+        : "memory");
+    return r != 0;
+}
+
+// ---------------------------------------------------------------- producer
+template <int D, int MT>
+__device__ void producer(const KvAttendArgs &a, const CUtensorMap &km, const CUtensorMap &vm, uint8_t *smem, Misc *ms) {
+    using C = Cfg<D, MT>;
+    const int lane = threadIdx.x & 31;
+    KvWalk w;
+    int st = 0, issued = 0;
+    bool ok = true;
+    for (int n = 0; ok; ++n) {
+        int src = 0, local = 0;
+        const bool more = w.next(a, 1u << kKvFew, &src, &local);
+        Item it;
+        it.end = !more;
+        if (more && lane == src) {
+            const int j = local % w.p.nch;
+            const KvRange g = kv_range(w.p, w.r.L - w.r.T, 0, a.window);
+            it.n0 = w.r.n0;
+            it.T = w.r.T;
+            it.pos0 = w.r.L - w.r.T;
+            it.slot = w.r.slot;
+            it.hk = local / w.p.nch;
+            it.rows = w.p.rows;
+            it.lo = g.lo + j * w.p.c;
+            it.hi = min(g.hi, it.lo + w.p.c);   // (with a window the last chunk may be empty)
+            it.k_lo = g.k_lo;
+            it.k_hi = g.k_hi;
+            it.part = kv_parts(w.p, g) > 1 ? j : -1;
+            it.base = w.part_before + w.part_excl;
+        }
+        const int lo = __shfl_sync(0xffffffffu, it.lo, src), hi = __shfl_sync(0xffffffffu, it.hi, src);
+        if (more && lo >= hi) {
+            --n;
+            continue;
+        }
+        const int slot = n % kItems;
+        if (n >= kItems && !warp_all(kv_wait(&ms->item_empty[slot], (n / kItems - 1) & 1, &ms->abort))) break;
+        if (lane == src) ms->item[slot] = it;
+        mbar_arrive_warp(&ms->item_full[slot]);
+        if (!more) break;
+        const int req_slot = __shfl_sync(0xffffffffu, it.slot, src), hk = __shfl_sync(0xffffffffu, it.hk, src);
+        const int32_t *table = a.bt.block_table + (long long)req_slot * a.bt.bt_stride;
+        int pages = -1, ahead = lo + lane < hi ? table[lo + lane] : -1;
+        for (int p = lo; ok && p < hi; ++p) {
+            if (((p - lo) & 31) == 0) {
+                pages = ahead;
+                ahead = p + 32 + lane < hi ? table[p + 32 + lane] : -1;
+            }
+            const int pg = __shfl_sync(0xffffffffu, pages, (p - lo) & 31);
+            const bool bad = pg < 0 || pg >= a.bt.n_pages;
+            if (bad && lane == 0) set_dev_err(CSLA_DEVERR_PAGE);
+            // (an unmapped page's tokens are page 0's, masked)
+            const int row = ((bad ? 0 : pg) * a.HK + hk) * CSLA_PAGE_TOKENS;
+            for (int h = 0; ok && h < 2 * C::kPer; ++h) {   // K then V of each part of the page
+                if (issued >= C::kStages) ok = warp_all(kv_wait(&ms->empty[st], (issued / C::kStages - 1) & 1, &ms->abort));
+                if (!ok) break;
+                if (lane == 0) {
+                    ms->bad[st] = bad;
+                    mbar_arrive_expect_tx(&ms->full[st], C::kStage);
+#pragma unroll
+                    for (int kb = 0; kb < C::kKB; ++kb)
+                        tma_load_2d(smem + st * C::kStage + kb * C::kBlk, (h & 1) ? &vm : &km, 64 * kb,
+                                    row + (h >> 1) * C::kTok, &ms->full[st]);
+                }
+                __syncwarp();
+                ++issued;
+                st = st + 1 == C::kStages ? 0 : st + 1;
+            }
+        }
+    }
+    // copies in flight land before the CTA exits (all have, unless a wait gave up)
+    for (int i = max(0, issued - C::kStages); i < issued; ++i)
+        kv_wait(&ms->full[i % C::kStages], (i / C::kStages) & 1, nullptr);
+}
+
+// ---------------------------------------------------------------- consumers
+// Q rows of the item as two bf16 terms, rows of 2D bytes, 16-byte chunk ^ (row & 7).
+template <int D, int MT, bool QBF16>
+__device__ void stage_q(const KvAttendArgs &a, const Item &it, uint8_t *qs, const Misc *ms) {
+    constexpr int kLanes = D / 8, kPer = 32 / kLanes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % kLanes, sub = lane / kLanes;
+    const int G = a.HQ / a.HK;
+    const RowLane rl = row_lane<D>(c, a.d_rope, a.pairs);
+#pragma unroll 1
+    for (int r0 = warp * kPer; r0 < it.rows; r0 += kConsumers * kPer) {
+        const int r = min(r0 + sub, it.rows - 1), t = r / G;
+        const Raw8<QBF16> raw = load8<QBF16>(a.q, (long long)(it.n0 + t) * a.q_stride + (it.hk * G + r - t * G) * D, rl);
+        float2 cs[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) cs[j] = kv_cos_sin(it.pos0 + t, rl.pair >= 0 ? ms->turn[rl.pair + j] : 0);
+        float x[8];
+        widen8<QBF16>(raw, x);
+        if (a.gamma_q) {
+            float g[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = a.gamma_q[i < 4 ? rl.d0 + i : rl.d1 + i - 4];
+            row_norm<D>(x, g, a.eps);
+        }
+        if (a.d_rope) row_rope(x, a.pairs, cs);
+        if (r0 + sub < it.rows) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int byte = 2 * (h ? rl.d1 : rl.d0);
+                uint8_t *p = qs + (r0 + sub) * 2 * D + ((byte & ~15) ^ ((r0 + sub) & 7) << 4) + (byte & 15);
+                const uint2 o = make_uint2(pack_bf16(x[4 * h], x[4 * h + 1]), pack_bf16(x[4 * h + 2], x[4 * h + 3]));
+                *reinterpret_cast<uint2 *>(p) = o;
+                *reinterpret_cast<uint2 *>(p + MT * 16 * 2 * D) =
+                    make_uint2(pack_bf16(x[4 * h] - __uint_as_float(o.x << 16), x[4 * h + 1] - __uint_as_float(o.x & 0xFFFF0000u)),
+                               pack_bf16(x[4 * h + 2] - __uint_as_float(o.y << 16),
+                                         x[4 * h + 3] - __uint_as_float(o.y & 0xFFFF0000u)));
+            }
+        }
+    }
+}
+
+template <int D, int MT, bool QBF16, bool OBF16>
+__device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
+    using C = Cfg<D, MT>;
+    constexpr int kNT = C::kWT / 8;   // 8-token tiles per warp and stage
+    constexpr int kDT = D / 8;        // 8-dim tiles of O
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = a.HQ / a.HK;
+    const float sc = a.scale * kLog2e;
+    const uint32_t ring = smem_u32(smem), work = smem_u32(smem + C::kOffWork);
+    // ldmatrix addresses: K (rows = tokens): matrix i = lane / 8 is (tokens 8 (i>>1), dims 8 (i&1));
+    // V (transposed): (tokens 8 (i&1), dims 8 (i>>1)); Q: (rows 8 (i&1), dims 8 (i>>1))
+    const int mi = lane >> 3, mr = lane & 7;
+    int taken = 0;
+    bool ok = true;
+    for (int n = 0;; ++n) {
+        const int islot = n % kItems;
+        // the warps go on together or not at all: whatever gave up, every
+        // warp passes the same barriers (which also say that the last
+        // item's join is done with the work area)
+        ok = ok && warp_all(kv_wait(&ms->item_full[islot], (n / kItems) & 1, &ms->abort));
+        if (!all_consumers(ok)) return;
+        const Item it = ms->item[islot];
+        mbar_arrive_warp(&ms->item_empty[islot]);
+        if (it.end) return;
+        stage_q<D, MT, QBF16>(a, it, smem + C::kOffWork, ms);
+        sync_consumers();
+
+        float m[MT][2], l[MT][2], o[MT][kDT][4];
+        int pos[MT][2], low[MT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                m[mt][h] = -INFINITY;
+                l[mt][h] = 0.f;
+                pos[mt][h] = it.pos0 + min(16 * mt + 8 * h + (lane >> 2), it.rows - 1) / G;
+                low[mt][h] = a.window > 0 ? pos[mt][h] - a.window + 1 : 0;
+#pragma unroll
+                for (int j = 0; j < kDT; ++j) o[mt][j][2 * h] = o[mt][j][2 * h + 1] = 0.f;
+            }
+        const int parts = (it.hi - it.lo) * C::kPer;
+#pragma unroll 1
+        for (int s = 0; s < parts; ++s) {
+            // ---- S
+            const int ks = taken % C::kStages;
+            ok = warp_all(kv_wait(&ms->full[ks], (taken / C::kStages) & 1, &ms->abort));
+            if (!ok) break;
+            ++taken;
+            const bool bad = ms->bad[ks];
+            const int tok0 = warp * C::kWT;
+            const int t0 = it.lo * CSLA_PAGE_TOKENS + s * C::kTok + tok0;   // position of the warp's first token
+            float acc[MT][kNT][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int j = 0; j < kNT; ++j) acc[mt][j][0] = acc[mt][j][1] = acc[mt][j][2] = acc[mt][j][3] = 0.f;
+            const uint32_t kb = ring + ks * C::kStage;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                uint32_t b[kNT / 2][4];
+#pragma unroll
+                for (int j = 0; j < kNT / 2; ++j) {
+                    const int tok = tok0 + 16 * j + 8 * (mi >> 1) + mr, ch = 2 * k + (mi & 1);
+                    ldsm(b[j], kb + (ch >> 3) * C::kBlk + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
+                }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int term = 0; term < 2; ++term) {
+                        uint32_t q[4];
+                        const int row = 16 * mt + 8 * (mi & 1) + mr, ch = 2 * k + (mi >> 1);
+                        ldsm(q, work + term * (MT * 16 * 2 * D) + row * 2 * D + ((ch ^ (row & 7)) << 4));
+#pragma unroll
+                        for (int j = 0; j < kNT / 2; ++j) {
+                            mma16816(acc[mt][2 * j], q, b[j][0], b[j][1]);
+                            mma16816(acc[mt][2 * j + 1], q, b[j][2], b[j][3]);
+                        }
+                    }
+            }
+            mbar_arrive_warp(&ms->empty[ks]);
+            // ---- mask, maximum, P
+            const int vs = taken % C::kStages;
+            const bool edge = bad || t0 + C::kWT > it.pos0 + 1 || t0 < it.k_lo + it.T;   // some row may not see some token
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                if (edge) {
+#pragma unroll
+                    for (int j = 0; j < kNT; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int t = t0 + 8 * j + 2 * (lane & 3) + (e & 1);
+                            if (bad || t > pos[mt][e >> 1] || t < low[mt][e >> 1]) acc[mt][j][e] = -INFINITY;
+                        }
+                }
+                float mn[2];
+                bool grow = false;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float x = fmaxf(acc[mt][0][2 * h], acc[mt][0][2 * h + 1]);
+#pragma unroll
+                    for (int j = 1; j < kNT; ++j) x = fmaxf(x, fmaxf(acc[mt][j][2 * h], acc[mt][j][2 * h + 1]));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                    mn[h] = fmaxf(m[mt][h], x * sc);
+                    grow |= mn[h] > m[mt][h] + kGrow;
+                }
+                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (mn[h] > m[mt][h] + kGrow) {
+                            const float f = m[mt][h] == -INFINITY ? 0.f : ex2(m[mt][h] - mn[h]);
+                            m[mt][h] = mn[h];
+                            l[mt][h] *= f;
+#pragma unroll
+                            for (int j = 0; j < kDT; ++j) {
+                                o[mt][j][2 * h] *= f;
+                                o[mt][j][2 * h + 1] *= f;
+                            }
+                        }
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float sub = m[mt][h] == -INFINITY ? 0.f : m[mt][h];
+                    float sum = 0.f;
+#pragma unroll
+                    for (int j = 0; j < kNT; ++j) {
+                        acc[mt][j][2 * h] = ex2(fmaf(acc[mt][j][2 * h], sc, -sub));
+                        acc[mt][j][2 * h + 1] = ex2(fmaf(acc[mt][j][2 * h + 1], sc, -sub));
+                        sum += acc[mt][j][2 * h] + acc[mt][j][2 * h + 1];
+                    }
+                    l[mt][h] += sum;
+                }
+            }
+            // ---- O += P V
+            ok = warp_all(kv_wait(&ms->full[vs], (taken / C::kStages) & 1, &ms->abort));
+            if (!ok) break;
+            ++taken;
+            const uint32_t vb = ring + vs * C::kStage;
+#pragma unroll
+            for (int k = 0; k < kNT / 2; ++k) {
+                uint32_t p[MT][4];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    p[mt][0] = pack_bf16(acc[mt][2 * k][0], acc[mt][2 * k][1]);
+                    p[mt][1] = pack_bf16(acc[mt][2 * k][2], acc[mt][2 * k][3]);
+                    p[mt][2] = pack_bf16(acc[mt][2 * k + 1][0], acc[mt][2 * k + 1][1]);
+                    p[mt][3] = pack_bf16(acc[mt][2 * k + 1][2], acc[mt][2 * k + 1][3]);
+                }
+                // tokens that no row sees count nothing, whatever they hold (0 * NaN is not 0)
+                uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+                if (edge) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int t = t0 + 16 * k + 8 * h + 2 * (lane & 3);
+                        keep[h] = bad ? 0u
+                                      : (t >= it.k_lo && t < it.k_hi ? 0xFFFFu : 0u) |
+                                            (t + 1 >= it.k_lo && t + 1 < it.k_hi ? 0xFFFF0000u : 0u);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kDT / 2; ++j) {
+                    uint32_t b[4];
+                    const int tok = tok0 + 16 * k + 8 * (mi & 1) + mr, ch = 2 * j + (mi >> 1);
+                    ldsm_t(b, vb + (ch >> 3) * C::kBlk + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
+                    if (edge) {
+                        b[0] &= keep[0];
+                        b[1] &= keep[1];
+                        b[2] &= keep[0];
+                        b[3] &= keep[1];
+                    }
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        mma16816(o[mt][2 * j], p[mt], b[0], b[1]);
+                        mma16816(o[mt][2 * j + 1], p[mt], b[2], b[3]);
+                    }
+                }
+            }
+            mbar_arrive_warp(&ms->empty[vs]);
+        }
+
+        // ---- join the four warps: 2 into 0 and 3 into 1, then 1 into 0
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                l[mt][h] += __shfl_xor_sync(0xffffffffu, l[mt][h], 1);
+                l[mt][h] += __shfl_xor_sync(0xffffffffu, l[mt][h], 2);
+            }
+        sync_consumers();   // Q is no longer read
+#pragma unroll 1
+        for (int step = 2; step >= 1; --step) {
+            // (step 2: warps 2, 3 write buffers 0, 1; step 1: warp 1 writes buffer 1)
+            const bool gives = warp >= step && warp < 2 * step, takes = warp < step;
+            float4 *buf = reinterpret_cast<float4 *>(smem + C::kOffWork + (gives || step == 2 ? warp & 1 : 1) * C::kOut);
+            float4 *ml = reinterpret_cast<float4 *>(smem + C::kOffMl + (gives || step == 2 ? warp & 1 : 1) * C::kMl);
+            float f[MT][2], g[MT][2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (gives) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                        for (int j = 0; j < kDT / 2; ++j) {
+                            const int i = half * (kDT / 2) + j;
+                            buf[(mt * (kDT / 2) + j) * 32 + lane] = make_float4(o[mt][i][0], o[mt][i][1], o[mt][i][2], o[mt][i][3]);
+                        }
+                        if (half == 0) ml[mt * 32 + lane] = make_float4(m[mt][0], l[mt][0], m[mt][1], l[mt][1]);
+                    }
+                }
+                sync_consumers();
+                if (takes) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        if (half == 0) {
+                            const float4 x = ml[mt * 32 + lane];
+                            const float mo[2] = {x.x, x.z}, lo[2] = {x.y, x.w};
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const float top = fmaxf(m[mt][h], mo[h]), base = top == -INFINITY ? 0.f : top;
+                                f[mt][h] = ex2(m[mt][h] - base);
+                                g[mt][h] = ex2(mo[h] - base);
+                                m[mt][h] = top;
+                                l[mt][h] = l[mt][h] * f[mt][h] + lo[h] * g[mt][h];
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < kDT / 2; ++j) {
+                            const int i = half * (kDT / 2) + j;
+                            const float4 y = buf[(mt * (kDT / 2) + j) * 32 + lane];
+                            o[mt][i][0] = o[mt][i][0] * f[mt][0] + y.x * g[mt][0];
+                            o[mt][i][1] = o[mt][i][1] * f[mt][0] + y.y * g[mt][0];
+                            o[mt][i][2] = o[mt][i][2] * f[mt][1] + y.z * g[mt][1];
+                            o[mt][i][3] = o[mt][i][3] * f[mt][1] + y.w * g[mt][1];
+                        }
+                    }
+                }
+                sync_consumers();
+            }
+        }
+        if (warp == 0 && !ms->abort) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = 16 * mt + 8 * h + (lane >> 2);
+                    if (r >= it.rows) continue;
+                    const int d = 2 * (lane & 3);
+                    if (it.part >= 0) {
+                        const long long pr = it.base + ((long long)it.part * a.HK + it.hk) * it.rows + r;
+                        if (d == 0) a.part_ml[pr] = make_float2(m[mt][h], l[mt][h]);
+#pragma unroll
+                        for (int j = 0; j < kDT; ++j)
+                            *reinterpret_cast<float2 *>(a.part_o + pr * D + 8 * j + d) =
+                                make_float2(o[mt][j][2 * h], o[mt][j][2 * h + 1]);
+                    } else {
+                        const int t = r / G, hq = it.hk * G + r - t * G;
+                        const bool none = m[mt][h] == -INFINITY;
+                        const float sink = a.sink ? a.sink[hq] * kLog2e : -INFINITY;
+                        const float top = fmaxf(m[mt][h], sink);
+                        const float f = none ? 0.f : ex2(m[mt][h] - top);
+                        const float w = none ? 0.f : f / fmaf(l[mt][h], f, a.sink ? ex2(sink - top) : 0.f);
+                        const long long at = ((long long)(it.n0 + t) * a.HQ + hq) * D + d;
+#pragma unroll
+                        for (int j = 0; j < kDT; ++j) {
+                            const float x = none ? 0.f : o[mt][j][2 * h] * w, y = none ? 0.f : o[mt][j][2 * h + 1] * w;
+                            if constexpr (OBF16)
+                                *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(a.out) + at + 8 * j) = pack_bf16(x, y);
+                            else
+                                *reinterpret_cast<float2 *>(reinterpret_cast<float *>(a.out) + at + 8 * j) = make_float2(x, y);
+                        }
+                    }
+                }
+        }
+    }
+}
+
+template <int D, int MT, bool QBF16, bool OBF16>
+__global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1) kv_few_kernel(const __grid_constant__ KvAttendArgs a,
+                                                             const __grid_constant__ CUtensorMap km,
+                                                             const __grid_constant__ CUtensorMap vm) {
+    CSLA_TL_SCOPE(kTlKvFew);
+    using C = Cfg<D, MT>;
+    extern __shared__ uint8_t raw_smem[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
+    Misc *ms = reinterpret_cast<Misc *>(smem + C::kOffMisc);
+    pdl_trigger();
+    if (threadIdx.x < 64) ms->turn[threadIdx.x] = a.freq.turn[threadIdx.x];
+    if (threadIdx.x == 128) {
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&ms->item_full[i], 1);
+            mbar_init(&ms->item_empty[i], kConsumers);
+        }
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&ms->full[i], 1);
+            mbar_init(&ms->empty[i], kConsumers);
+        }
+        ms->abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&km);
+        tma_prefetch_desc(&vm);
+    }
+    __syncthreads();
+    pdl_wait();
+    CSLA_TL_WAITED();
+    if (threadIdx.x >= 32 * kConsumers)
+        producer<D, MT>(a, km, vm, smem, ms);
+    else
+        consumer<D, MT, QBF16, OBF16>(a, smem, ms);
+}
+
+template <int D, int MT, bool QB, bool OB>
+cudaError_t launch(const KvAttendArgs &a, const CUtensorMap &km, const CUtensorMap &vm, unsigned grid, cudaStream_t s) {
+    auto kern = kv_few_kernel<D, MT, QB, OB>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D, MT>());
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(grid), dim3(kThreads), smem_bytes<D, MT>(), s, a, km, vm);
+}
+template <int D, int MT>
+cudaError_t launch_types(const KvAttendArgs &a, bool qb, bool ob, const CUtensorMap &km, const CUtensorMap &vm,
+                         unsigned grid, cudaStream_t s) {
+    if (qb) return ob ? launch<D, MT, true, true>(a, km, vm, grid, s) : launch<D, MT, true, false>(a, km, vm, grid, s);
+    return ob ? launch<D, MT, false, true>(a, km, vm, grid, s) : launch<D, MT, false, false>(a, km, vm, grid, s);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_few(const KvAttendArgs &a, bool q_bf16, bool out_bf16, int rows, const CUtensorMap &km,
+                          const CUtensorMap &vm, int num_sms, long long items, cudaStream_t stream) {
+    const unsigned grid = (unsigned)(items < 2 * num_sms ? items : 2 * num_sms);
+    if (a.D == 64)
+        return rows <= 16 ? launch_types<64, 1>(a, q_bf16, out_bf16, km, vm, grid, stream)
+                          : launch_types<64, 2>(a, q_bf16, out_bf16, km, vm, grid, stream);
+    return rows <= 16 ? launch_types<128, 1>(a, q_bf16, out_bf16, km, vm, grid, stream)
+                      : launch_types<128, 2>(a, q_bf16, out_bf16, km, vm, grid, stream);
+}
+
+}  // namespace csla

@@ -613,7 +613,7 @@ int csla_version(void);
  * the buffer.  Kernel ids: 1 compress, 2 tail update, 3 index-query
  * projection, 4 wide projection, 5 indexer, 6 top-k, (7 unused),
  * 8 attention, 9 chunk combine, 10 K/V append, 11 paged attention,
- * 12 paged attention's join.
+ * 12 its join, 13 its rows of short requests.
  */
 #ifdef CSLA_TIMELINE
 int csla_timeline_read(void *records, size_t bytes, uint32_t *count);
