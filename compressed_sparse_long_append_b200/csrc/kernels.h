@@ -311,7 +311,7 @@ struct KvAttendArgs {
 
 // How the attention cuts a request of T new tokens (context L): a function of
 // T, L and the layer alone.  rows = T*G rows per KV head.
-//   few     up to 32 rows: kv_few_kernel, R = 1;
+//   few     up to 64 rows: kv_few_kernel, R = 1;
 //   single  up to 128 rows: kv_attend_kernel, R = 1, its two streams take key tiles in turn;
 //   paired  more: kv_attend_kernel, R row tiles of 256.
 // Keys are cut into chunks of c tiles, nch at most per row tile, so that a
@@ -320,7 +320,7 @@ enum { kKvFew = 0, kKvSingle = 1, kKvPaired = 2 };
 struct KvPlan {
     int rows, R, kind, c, nch, T, G, heads_inside;
 };
-constexpr int kKvFewRows = 32;
+constexpr int kKvFewRows = 64;
 // items that a long request is cut into (all heads), and the least tiles of a chunk, by kind
 __host__ __device__ constexpr int kv_units(int kind) { return kind == kKvPaired ? 148 : 296; }
 __host__ __device__ constexpr int kv_min_tiles(int kind) { return kind == kKvPaired ? 8 : (kind == kKvSingle ? 4 : 2); }
@@ -368,7 +368,9 @@ __host__ __device__ inline KvPlan kv_plan(int T, int L, int G, int HK, int windo
     // (32-bit divisions only: this runs ahead of every item's first load)
     const unsigned most = kv_units(p.kind) / (unsigned)(HK * p.R);   // chunks
     int c = most > 1 ? (int)((nt + most - 1) / most) : nt;
-    const int least = kv_min_tiles(p.kind);
+    int least = kv_min_tiles(p.kind);
+    // a partial of r rows weighs r / 128 of a tile (written and read): an eighth of a chunk at most
+    if (p.kind == kKvFew && p.rows > 8 * least) least = p.rows / 8;
     if (c < least) c = least;
     if (c > nt) c = nt;
     p.c = c;

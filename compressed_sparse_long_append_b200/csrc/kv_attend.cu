@@ -321,13 +321,42 @@ __device__ void q_role(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
 }
 
 // ---------------------------------------------------------------- MMA role
-__device__ __forceinline__ void umma_ts_f16(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// The products of a tile are 8 to 16 instructions of 64 tensor cycles each,
+// all from one thread: what that thread does per instruction has to stay
+// below that.  So the descriptors' bases are made warp-uniform (a shuffle) and
+// every instruction adds a constant to the low word (address and leading offset, in
+// 16-byte units); the high word is the same for all operands (stride of
+// 8-row groups 1024 bytes, version 1, 128-byte swizzle).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (kLayoutSW128 << 29);
+__device__ constexpr uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) { return (saddr >> 4) | (lbo_bytes >> 4) << 16; }
+
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "mov.b64 a, {%1, %5};\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
         : "memory");
 }
 
@@ -337,7 +366,7 @@ struct Mma {
     uint8_t *smem;
     Misc *ms;
     int lane;
-    uint32_t tmem, q0, kv0;
+    uint32_t tmem, q0, k0, v0;     // TMEM base; low descriptor words of Q, and of ring stage 0 as K and as V
     int taken = 0;                 // ring tiles taken
     int p_count[2] = {0, 0};       // P tiles taken per stream
 
@@ -367,20 +396,20 @@ struct Mma {
     // S of stream s = Q K^T (both terms of Q for an unpaired item)
     __device__ void s_mma(int s, int stage, bool paired) {
         constexpr uint32_t kId = idesc_bf16(128, kTile, false, false);
-        if (lane == 0) {
-            const uint32_t k0 = kv0 + stage * C::kTileBytes;
-            const int q_lo = paired ? s : 0, q_hi = paired ? s : 1;
-            uint32_t acc = 0;
-            for (int qt = q_lo; qt <= q_hi; ++qt) {
+        const uint32_t k = uniform(k0 + (uint32_t)stage * (C::kTileBytes >> 4)), d = uniform(tmem + C::kColS + 128 * s);
+        const uint32_t q = uniform(q0 + (paired && s ? C::kTileBytes >> 4 : 0));
+        if (elect_one()) {
 #pragma unroll
-                for (int kb = 0; kb < C::kKB; ++kb)
+            for (int i = 0; i < 4 * C::kKB; ++i) {
+                const uint32_t off = ((i >> 2) * C::kBlk + (i & 3) * 32) >> 4;
+                umma_ss(d, q + off, k + off, kId, i > 0);
+            }
+            if (!paired) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        umma_kind_f16(tmem + C::kColS + 128 * s,
-                                      sdesc(q0 + qt * C::kTileBytes + kb * C::kBlk + kk * 32, 16, 1024),
-                                      sdesc(k0 + kb * C::kBlk + kk * 32, 16, 1024), kId, acc);
-                        acc = 1;
-                    }
+                for (int i = 0; i < 4 * C::kKB; ++i) {
+                    const uint32_t off = ((i >> 2) * C::kBlk + (i & 3) * 32) >> 4;
+                    umma_ss(d, q + (C::kTileBytes >> 4) + off, k + off, kId, 1);
+                }
             }
             umma_commit(&ms->s_full[s]);
         }
@@ -392,18 +421,17 @@ struct Mma {
         if (!warp_all(kv_wait(&ms->p_full[s], p_count[s] & 1, &ms->abort))) return false;
         ++p_count[s];
         tc_fence_after();
-        if (lane == 0) {
-            const uint32_t v0 = kv0 + stage * C::kTileBytes;
+        const uint32_t v = uniform(v0 + (uint32_t)stage * (C::kTileBytes >> 4)), d = uniform(tmem + C::kColO + D * s);
+        const uint32_t p = uniform(tmem + C::kColS + 128 * s), acc = uniform(first ? 0u : 1u);
+        if (elect_one()) {
 #pragma unroll
-            for (int ks = 0; ks < kTile / 16; ++ks)
-                umma_ts_f16(tmem + C::kColO + D * s, tmem + C::kColS + 128 * s + 8 * ks,
-                            sdesc(v0 + ks * 2048, C::kBlk, 1024), kId, (!first || ks > 0) ? 1u : 0u);
+            for (int i = 0; i < kTile / 16; ++i) umma_ts(d, p + 8 * i, v + (i * 2048 >> 4), kId, i > 0 ? 1u : acc);
         }
         __syncwarp();
         return true;
     }
     __device__ void commit(uint64_t *bar) {
-        if (lane == 0) umma_commit(bar);
+        if (elect_one()) umma_commit(bar);
         __syncwarp();
     }
 
@@ -480,7 +508,9 @@ struct Mma {
 template <int D>
 __device__ void mma_role(uint8_t *smem, Misc *ms) {
     using C = Cfg<D>;
-    Mma<D> m{smem, ms, (int)(threadIdx.x & 31), ms->tmem, smem_u32(smem + C::kOffQ), smem_u32(smem + C::kOffKV)};
+    const uint32_t kv = smem_u32(smem + C::kOffKV);
+    Mma<D> m{smem, ms, (int)(threadIdx.x & 31), ms->tmem, desc_lo(smem_u32(smem + C::kOffQ), 16), desc_lo(kv, 16),
+             desc_lo(kv, C::kBlk)};
     bool ok = true;
     int tiles = 0;
     Item it;

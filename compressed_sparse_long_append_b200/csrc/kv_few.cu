@@ -1,10 +1,10 @@
-// kv_few.cu -- attention of requests of few rows (up to 32 per KV head:
+// kv_few.cu -- attention of requests of few rows (up to 64 per KV head:
 // decode, a few drafted tokens) over the dense paged cache: a part of
 // csla_kv_attend.
 //
 //   s_j = scale <R(p) norm(q), K_j>,  o = sum_j e^{s_j} V_j / (e^{sink} + sum_j e^{s_j})
 //
-// Each K and V byte is used by at most 32 rows, so the kernel is bound by
+// Each K and V byte is used by at most 64 rows, so the kernel is bound by
 // HBM and by how much of it is asked for at a time; the products are small.  So
 // they stay in registers: mma.sync on 16-row fragments needs no tensor memory, no handing
 // over between roles and no padding to 128 rows, and its rate is several times what the bytes leave time for.
@@ -23,10 +23,9 @@
 namespace csla {
 namespace {
 
-constexpr int kConsumers = 4;
-constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kGroups = 4;   // token groups: a quarter of a stage's tokens each
 constexpr int kItems = 4;
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 11;
 
 template <int D, int MT>
 struct Cfg {
@@ -35,8 +34,11 @@ struct Cfg {
     static constexpr int kBlk = kTok * 128;
     static constexpr int kStage = kKB * kBlk;             // 16 KB
     static constexpr int kPer = CSLA_PAGE_TOKENS / kTok;  // stages per page
-    static constexpr int kStages = MT == 1 ? 6 : 5;
-    static constexpr int kWT = kTok / kConsumers;         // tokens of a stage per warp
+    static constexpr int kConsumers = kGroups * MT;       // warp = 4 * (16-row tile) + token group
+    static constexpr int kThreads = 32 * (kConsumers + 1);
+    static constexpr int kCtas = MT == 4 ? 1 : 2;         // per SM
+    static constexpr int kStages = MT == 1 ? 6 : (MT == 2 ? 5 : 11);
+    static constexpr int kWT = kTok / kGroups;            // tokens of a stage per warp
     static constexpr int kOut = MT * 16 * D * 2;          // half the dims of one warp's O
     // work area: the Q terms [2][MT*16][D] bf16; at an item's end half of two O, and their (m, l)
     static constexpr int kOffWork = kStages * kStage;
@@ -83,10 +85,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+template <int N>
 __device__ __forceinline__ void sync_consumers() {
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * N) : "memory");
 }
 // The barrier, and whether `ok` holds in every consumer thread.
+template <int N>
 __device__ __forceinline__ bool all_consumers(bool ok) {
     uint32_t r;
     asm volatile(
@@ -95,7 +99,7 @@ __device__ __forceinline__ bool all_consumers(bool ok) {
         "barrier.cta.red.and.pred q, 1, %2, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)ok), "n"(32 * kConsumers)
+        : "r"((uint32_t)ok), "n"(32 * N)
         : "memory");
     return r != 0;
 }
@@ -183,7 +187,7 @@ __device__ void stage_q(const KvAttendArgs &a, const Item &it, uint8_t *qs, cons
     const int G = a.HQ / a.HK;
     const RowLane rl = row_lane<D>(c, a.d_rope, a.pairs);
 #pragma unroll 1
-    for (int r0 = warp * kPer; r0 < it.rows; r0 += kConsumers * kPer) {
+    for (int r0 = warp * kPer; r0 < it.rows; r0 += kGroups * MT * kPer) {
         const int r = min(r0 + sub, it.rows - 1), t = r / G;
         const Raw8<QBF16> raw = load8<QBF16>(a.q, (long long)(it.n0 + t) * a.q_stride + (it.hk * G + r - t * G) * D, rl);
         float2 cs[4];
@@ -219,13 +223,14 @@ __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
     using C = Cfg<D, MT>;
     constexpr int kNT = C::kWT / 8;   // 8-token tiles per warp and stage
     constexpr int kDT = D / 8;        // 8-dim tiles of O
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = (threadIdx.x >> 5) & (kGroups - 1), mt = threadIdx.x >> 7, lane = threadIdx.x & 31;
     const int G = a.HQ / a.HK;
     const float sc = a.scale * kLog2e;
     const uint32_t ring = smem_u32(smem), work = smem_u32(smem + C::kOffWork);
     // ldmatrix addresses: K (rows = tokens): matrix i = lane / 8 is (tokens 8 (i>>1), dims 8 (i&1));
     // V (transposed): (tokens 8 (i&1), dims 8 (i>>1)); Q: (rows 8 (i&1), dims 8 (i>>1))
     const int mi = lane >> 3, mr = lane & 7;
+    const int tok0 = warp * C::kWT;
     int taken = 0;
     bool ok = true;
     for (int n = 0;; ++n) {
@@ -234,26 +239,25 @@ __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
         // warp passes the same barriers (which also say that the last
         // item's join is done with the work area)
         ok = ok && warp_all(kv_wait(&ms->item_full[islot], (n / kItems) & 1, &ms->abort));
-        if (!all_consumers(ok)) return;
+        if (!all_consumers<C::kConsumers>(ok)) return;
         const Item it = ms->item[islot];
         mbar_arrive_warp(&ms->item_empty[islot]);
         if (it.end) return;
         stage_q<D, MT, QBF16>(a, it, smem + C::kOffWork, ms);
-        sync_consumers();
+        sync_consumers<C::kConsumers>();
 
-        float m[MT][2], l[MT][2], o[MT][kDT][4];
-        int pos[MT][2], low[MT][2];
+        const bool idle = 16 * mt >= it.rows;   // no row of this warp's tile is real
+        float m[2], l[2], o[kDT][4];
+        int pos[2], low[2];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int h = 0; h < 2; ++h) {
+            m[h] = -INFINITY;
+            l[h] = 0.f;
+            pos[h] = it.pos0 + min(16 * mt + 8 * h + (lane >> 2), it.rows - 1) / G;
+            low[h] = a.window > 0 ? pos[h] - a.window + 1 : 0;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                m[mt][h] = -INFINITY;
-                l[mt][h] = 0.f;
-                pos[mt][h] = it.pos0 + min(16 * mt + 8 * h + (lane >> 2), it.rows - 1) / G;
-                low[mt][h] = a.window > 0 ? pos[mt][h] - a.window + 1 : 0;
-#pragma unroll
-                for (int j = 0; j < kDT; ++j) o[mt][j][2 * h] = o[mt][j][2 * h + 1] = 0.f;
-            }
+            for (int j = 0; j < kDT; ++j) o[j][2 * h] = o[j][2 * h + 1] = 0.f;
+        }
         const int parts = (it.hi - it.lo) * C::kPer;
 #pragma unroll 1
         for (int s = 0; s < parts; ++s) {
@@ -263,24 +267,20 @@ __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
             if (!ok) break;
             ++taken;
             const bool bad = ms->bad[ks];
-            const int tok0 = warp * C::kWT;
             const int t0 = it.lo * CSLA_PAGE_TOKENS + s * C::kTok + tok0;   // position of the warp's first token
-            float acc[MT][kNT][4];
+            float acc[kNT][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int j = 0; j < kNT; ++j) acc[mt][j][0] = acc[mt][j][1] = acc[mt][j][2] = acc[mt][j][3] = 0.f;
+            for (int j = 0; j < kNT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
             const uint32_t kb = ring + ks * C::kStage;
+            if (!idle) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                uint32_t b[kNT / 2][4];
+                for (int k = 0; k < D / 16; ++k) {
+                    uint32_t b[kNT / 2][4];
 #pragma unroll
-                for (int j = 0; j < kNT / 2; ++j) {
-                    const int tok = tok0 + 16 * j + 8 * (mi >> 1) + mr, ch = 2 * k + (mi & 1);
-                    ldsm(b[j], kb + (ch >> 3) * C::kBlk + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
-                }
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
+                    for (int j = 0; j < kNT / 2; ++j) {
+                        const int tok = tok0 + 16 * j + 8 * (mi >> 1) + mr, ch = 2 * k + (mi & 1);
+                        ldsm(b[j], kb + (ch >> 3) * C::kBlk + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
+                    }
 #pragma unroll
                     for (int term = 0; term < 2; ++term) {
                         uint32_t q[4];
@@ -288,210 +288,192 @@ __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
                         ldsm(q, work + term * (MT * 16 * 2 * D) + row * 2 * D + ((ch ^ (row & 7)) << 4));
 #pragma unroll
                         for (int j = 0; j < kNT / 2; ++j) {
-                            mma16816(acc[mt][2 * j], q, b[j][0], b[j][1]);
-                            mma16816(acc[mt][2 * j + 1], q, b[j][2], b[j][3]);
+                            mma16816(acc[2 * j], q, b[j][0], b[j][1]);
+                            mma16816(acc[2 * j + 1], q, b[j][2], b[j][3]);
                         }
                     }
+                }
             }
             mbar_arrive_warp(&ms->empty[ks]);
             // ---- mask, maximum, P
             const int vs = taken % C::kStages;
             const bool edge = bad || t0 + C::kWT > it.pos0 + 1 || t0 < it.k_lo + it.T;   // some row may not see some token
+            if (edge) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                if (edge) {
+                for (int j = 0; j < kNT; ++j)
 #pragma unroll
-                    for (int j = 0; j < kNT; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int t = t0 + 8 * j + 2 * (lane & 3) + (e & 1);
-                            if (bad || t > pos[mt][e >> 1] || t < low[mt][e >> 1]) acc[mt][j][e] = -INFINITY;
-                        }
-                }
-                float mn[2];
-                bool grow = false;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float x = fmaxf(acc[mt][0][2 * h], acc[mt][0][2 * h + 1]);
-#pragma unroll
-                    for (int j = 1; j < kNT; ++j) x = fmaxf(x, fmaxf(acc[mt][j][2 * h], acc[mt][j][2 * h + 1]));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                    mn[h] = fmaxf(m[mt][h], x * sc);
-                    grow |= mn[h] > m[mt][h] + kGrow;
-                }
-                if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (mn[h] > m[mt][h] + kGrow) {
-                            const float f = m[mt][h] == -INFINITY ? 0.f : ex2(m[mt][h] - mn[h]);
-                            m[mt][h] = mn[h];
-                            l[mt][h] *= f;
-#pragma unroll
-                            for (int j = 0; j < kDT; ++j) {
-                                o[mt][j][2 * h] *= f;
-                                o[mt][j][2 * h + 1] *= f;
-                            }
-                        }
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float sub = m[mt][h] == -INFINITY ? 0.f : m[mt][h];
-                    float sum = 0.f;
-#pragma unroll
-                    for (int j = 0; j < kNT; ++j) {
-                        acc[mt][j][2 * h] = ex2(fmaf(acc[mt][j][2 * h], sc, -sub));
-                        acc[mt][j][2 * h + 1] = ex2(fmaf(acc[mt][j][2 * h + 1], sc, -sub));
-                        sum += acc[mt][j][2 * h] + acc[mt][j][2 * h + 1];
+                    for (int e = 0; e < 4; ++e) {
+                        const int t = t0 + 8 * j + 2 * (lane & 3) + (e & 1);
+                        if (bad || t > pos[e >> 1] || t < low[e >> 1]) acc[j][e] = -INFINITY;
                     }
-                    l[mt][h] += sum;
+            }
+            float mn[2];
+            bool grow = false;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x = fmaxf(acc[0][2 * h], acc[0][2 * h + 1]);
+#pragma unroll
+                for (int j = 1; j < kNT; ++j) x = fmaxf(x, fmaxf(acc[j][2 * h], acc[j][2 * h + 1]));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                mn[h] = fmaxf(m[h], x * sc);
+                grow |= mn[h] > m[h] + kGrow;
+            }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (mn[h] > m[h] + kGrow) {
+                        const float f = m[h] == -INFINITY ? 0.f : ex2(m[h] - mn[h]);
+                        m[h] = mn[h];
+                        l[h] *= f;
+#pragma unroll
+                        for (int j = 0; j < kDT; ++j) {
+                            o[j][2 * h] *= f;
+                            o[j][2 * h + 1] *= f;
+                        }
+                    }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float sub = m[h] == -INFINITY ? 0.f : m[h];
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < kNT; ++j) {
+                    acc[j][2 * h] = ex2(fmaf(acc[j][2 * h], sc, -sub));
+                    acc[j][2 * h + 1] = ex2(fmaf(acc[j][2 * h + 1], sc, -sub));
+                    sum += acc[j][2 * h] + acc[j][2 * h + 1];
                 }
+                l[h] += sum;
             }
             // ---- O += P V
             ok = warp_all(kv_wait(&ms->full[vs], (taken / C::kStages) & 1, &ms->abort));
             if (!ok) break;
             ++taken;
             const uint32_t vb = ring + vs * C::kStage;
+            if (!idle) {
 #pragma unroll
-            for (int k = 0; k < kNT / 2; ++k) {
-                uint32_t p[MT][4];
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    p[mt][0] = pack_bf16(acc[mt][2 * k][0], acc[mt][2 * k][1]);
-                    p[mt][1] = pack_bf16(acc[mt][2 * k][2], acc[mt][2 * k][3]);
-                    p[mt][2] = pack_bf16(acc[mt][2 * k + 1][0], acc[mt][2 * k + 1][1]);
-                    p[mt][3] = pack_bf16(acc[mt][2 * k + 1][2], acc[mt][2 * k + 1][3]);
-                }
-                // tokens that no row sees count nothing, whatever they hold (0 * NaN is not 0)
-                uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-                if (edge) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int t = t0 + 16 * k + 8 * h + 2 * (lane & 3);
-                        keep[h] = bad ? 0u
-                                      : (t >= it.k_lo && t < it.k_hi ? 0xFFFFu : 0u) |
-                                            (t + 1 >= it.k_lo && t + 1 < it.k_hi ? 0xFFFF0000u : 0u);
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < kDT / 2; ++j) {
-                    uint32_t b[4];
-                    const int tok = tok0 + 16 * k + 8 * (mi & 1) + mr, ch = 2 * j + (mi >> 1);
-                    ldsm_t(b, vb + (ch >> 3) * C::kBlk + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
+                for (int k = 0; k < kNT / 2; ++k) {
+                    const uint32_t p[4] = {pack_bf16(acc[2 * k][0], acc[2 * k][1]), pack_bf16(acc[2 * k][2], acc[2 * k][3]),
+                                           pack_bf16(acc[2 * k + 1][0], acc[2 * k + 1][1]),
+                                           pack_bf16(acc[2 * k + 1][2], acc[2 * k + 1][3])};
+                    // tokens that no row sees count nothing, whatever they hold (0 * NaN is not 0)
+                    uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
                     if (edge) {
-                        b[0] &= keep[0];
-                        b[1] &= keep[1];
-                        b[2] &= keep[0];
-                        b[3] &= keep[1];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int t = t0 + 16 * k + 8 * h + 2 * (lane & 3);
+                            keep[h] = bad ? 0u
+                                          : (t >= it.k_lo && t < it.k_hi ? 0xFFFFu : 0u) |
+                                                (t + 1 >= it.k_lo && t + 1 < it.k_hi ? 0xFFFF0000u : 0u);
+                        }
                     }
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        mma16816(o[mt][2 * j], p[mt], b[0], b[1]);
-                        mma16816(o[mt][2 * j + 1], p[mt], b[2], b[3]);
+                    for (int j = 0; j < kDT / 2; ++j) {
+                        uint32_t b[4];
+                        const int tok = tok0 + 16 * k + 8 * (mi & 1) + mr, ch = 2 * j + (mi >> 1);
+                        ldsm_t(b, vb + (ch >> 3) * C::kBlk + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
+                        if (edge) {
+                            b[0] &= keep[0];
+                            b[1] &= keep[1];
+                            b[2] &= keep[0];
+                            b[3] &= keep[1];
+                        }
+                        mma16816(o[2 * j], p, b[0], b[1]);
+                        mma16816(o[2 * j + 1], p, b[2], b[3]);
                     }
                 }
             }
             mbar_arrive_warp(&ms->empty[vs]);
         }
 
-        // ---- join the four warps: 2 into 0 and 3 into 1, then 1 into 0
+        // ---- join the four token groups: 2 into 0 and 3 into 1, then 1 into 0
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                l[mt][h] += __shfl_xor_sync(0xffffffffu, l[mt][h], 1);
-                l[mt][h] += __shfl_xor_sync(0xffffffffu, l[mt][h], 2);
-            }
-        sync_consumers();   // Q is no longer read
+        for (int h = 0; h < 2; ++h) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        }
+        sync_consumers<C::kConsumers>();   // Q is no longer read
 #pragma unroll 1
         for (int step = 2; step >= 1; --step) {
-            // (step 2: warps 2, 3 write buffers 0, 1; step 1: warp 1 writes buffer 1)
+            // (step 2: groups 2, 3 write buffers 0, 1; step 1: group 1 writes buffer 1)
             const bool gives = warp >= step && warp < 2 * step, takes = warp < step;
-            float4 *buf = reinterpret_cast<float4 *>(smem + C::kOffWork + (gives || step == 2 ? warp & 1 : 1) * C::kOut);
-            float4 *ml = reinterpret_cast<float4 *>(smem + C::kOffMl + (gives || step == 2 ? warp & 1 : 1) * C::kMl);
-            float f[MT][2], g[MT][2];
+            const int side = gives || step == 2 ? warp & 1 : 1;
+            float4 *buf = reinterpret_cast<float4 *>(smem + C::kOffWork + side * C::kOut) + mt * (kDT / 2) * 32;
+            float4 *ml = reinterpret_cast<float4 *>(smem + C::kOffMl + side * C::kMl) + mt * 32;
+            float f[2] = {1.f, 1.f}, g[2] = {0.f, 0.f};
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 if (gives) {
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-                        for (int j = 0; j < kDT / 2; ++j) {
-                            const int i = half * (kDT / 2) + j;
-                            buf[(mt * (kDT / 2) + j) * 32 + lane] = make_float4(o[mt][i][0], o[mt][i][1], o[mt][i][2], o[mt][i][3]);
-                        }
-                        if (half == 0) ml[mt * 32 + lane] = make_float4(m[mt][0], l[mt][0], m[mt][1], l[mt][1]);
+                    for (int j = 0; j < kDT / 2; ++j) {
+                        const int i = half * (kDT / 2) + j;
+                        buf[j * 32 + lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
                     }
+                    if (half == 0) ml[lane] = make_float4(m[0], l[0], m[1], l[1]);
                 }
-                sync_consumers();
+                sync_consumers<C::kConsumers>();
                 if (takes) {
+                    if (half == 0) {
+                        const float4 x = ml[lane];
+                        const float mo[2] = {x.x, x.z}, lo[2] = {x.y, x.w};
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        if (half == 0) {
-                            const float4 x = ml[mt * 32 + lane];
-                            const float mo[2] = {x.x, x.z}, lo[2] = {x.y, x.w};
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const float top = fmaxf(m[mt][h], mo[h]), base = top == -INFINITY ? 0.f : top;
-                                f[mt][h] = ex2(m[mt][h] - base);
-                                g[mt][h] = ex2(mo[h] - base);
-                                m[mt][h] = top;
-                                l[mt][h] = l[mt][h] * f[mt][h] + lo[h] * g[mt][h];
-                            }
-                        }
-#pragma unroll
-                        for (int j = 0; j < kDT / 2; ++j) {
-                            const int i = half * (kDT / 2) + j;
-                            const float4 y = buf[(mt * (kDT / 2) + j) * 32 + lane];
-                            o[mt][i][0] = o[mt][i][0] * f[mt][0] + y.x * g[mt][0];
-                            o[mt][i][1] = o[mt][i][1] * f[mt][0] + y.y * g[mt][0];
-                            o[mt][i][2] = o[mt][i][2] * f[mt][1] + y.z * g[mt][1];
-                            o[mt][i][3] = o[mt][i][3] * f[mt][1] + y.w * g[mt][1];
+                        for (int h = 0; h < 2; ++h) {
+                            const float top = fmaxf(m[h], mo[h]), base = top == -INFINITY ? 0.f : top;
+                            f[h] = ex2(m[h] - base);
+                            g[h] = ex2(mo[h] - base);
+                            m[h] = top;
+                            l[h] = l[h] * f[h] + lo[h] * g[h];
                         }
                     }
+#pragma unroll
+                    for (int j = 0; j < kDT / 2; ++j) {
+                        const int i = half * (kDT / 2) + j;
+                        const float4 y = buf[j * 32 + lane];
+                        o[i][0] = o[i][0] * f[0] + y.x * g[0];
+                        o[i][1] = o[i][1] * f[0] + y.y * g[0];
+                        o[i][2] = o[i][2] * f[1] + y.z * g[1];
+                        o[i][3] = o[i][3] * f[1] + y.w * g[1];
+                    }
                 }
-                sync_consumers();
+                sync_consumers<C::kConsumers>();
             }
         }
-        if (warp == 0 && !ms->abort) {
+        if (warp == 0 && !*(volatile int *)&ms->abort) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int h = 0; h < 2; ++h) {
+                const int r = 16 * mt + 8 * h + (lane >> 2);
+                if (r >= it.rows) continue;
+                const int d = 2 * (lane & 3);
+                if (it.part >= 0) {
+                    const long long pr = it.base + ((long long)it.part * a.HK + it.hk) * it.rows + r;
+                    if (d == 0) a.part_ml[pr] = make_float2(m[h], l[h]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = 16 * mt + 8 * h + (lane >> 2);
-                    if (r >= it.rows) continue;
-                    const int d = 2 * (lane & 3);
-                    if (it.part >= 0) {
-                        const long long pr = it.base + ((long long)it.part * a.HK + it.hk) * it.rows + r;
-                        if (d == 0) a.part_ml[pr] = make_float2(m[mt][h], l[mt][h]);
+                    for (int j = 0; j < kDT; ++j)
+                        *reinterpret_cast<float2 *>(a.part_o + pr * D + 8 * j + d) = make_float2(o[j][2 * h], o[j][2 * h + 1]);
+                } else {
+                    const int t = r / G, hq = it.hk * G + r - t * G;
+                    const bool none = m[h] == -INFINITY;
+                    const float sink = a.sink ? a.sink[hq] * kLog2e : -INFINITY;
+                    const float top = fmaxf(m[h], sink);
+                    const float f = none ? 0.f : ex2(m[h] - top);
+                    const float w = none ? 0.f : f / fmaf(l[h], f, a.sink ? ex2(sink - top) : 0.f);
+                    const long long at = ((long long)(it.n0 + t) * a.HQ + hq) * D + d;
 #pragma unroll
-                        for (int j = 0; j < kDT; ++j)
-                            *reinterpret_cast<float2 *>(a.part_o + pr * D + 8 * j + d) =
-                                make_float2(o[mt][j][2 * h], o[mt][j][2 * h + 1]);
-                    } else {
-                        const int t = r / G, hq = it.hk * G + r - t * G;
-                        const bool none = m[mt][h] == -INFINITY;
-                        const float sink = a.sink ? a.sink[hq] * kLog2e : -INFINITY;
-                        const float top = fmaxf(m[mt][h], sink);
-                        const float f = none ? 0.f : ex2(m[mt][h] - top);
-                        const float w = none ? 0.f : f / fmaf(l[mt][h], f, a.sink ? ex2(sink - top) : 0.f);
-                        const long long at = ((long long)(it.n0 + t) * a.HQ + hq) * D + d;
-#pragma unroll
-                        for (int j = 0; j < kDT; ++j) {
-                            const float x = none ? 0.f : o[mt][j][2 * h] * w, y = none ? 0.f : o[mt][j][2 * h + 1] * w;
-                            if constexpr (OBF16)
-                                *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(a.out) + at + 8 * j) = pack_bf16(x, y);
-                            else
-                                *reinterpret_cast<float2 *>(reinterpret_cast<float *>(a.out) + at + 8 * j) = make_float2(x, y);
-                        }
+                    for (int j = 0; j < kDT; ++j) {
+                        const float x = none ? 0.f : o[j][2 * h] * w, y = none ? 0.f : o[j][2 * h + 1] * w;
+                        if constexpr (OBF16)
+                            *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(a.out) + at + 8 * j) = pack_bf16(x, y);
+                        else
+                            *reinterpret_cast<float2 *>(reinterpret_cast<float *>(a.out) + at + 8 * j) = make_float2(x, y);
                     }
                 }
+            }
         }
     }
 }
 
 template <int D, int MT, bool QBF16, bool OBF16>
-__global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1) kv_few_kernel(const __grid_constant__ KvAttendArgs a,
+__global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtas) kv_few_kernel(const __grid_constant__ KvAttendArgs a,
                                                              const __grid_constant__ CUtensorMap km,
                                                              const __grid_constant__ CUtensorMap vm) {
     CSLA_TL_SCOPE(kTlKvFew);
@@ -501,14 +483,14 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1) kv_few_kernel(const
     Misc *ms = reinterpret_cast<Misc *>(smem + C::kOffMisc);
     pdl_trigger();
     if (threadIdx.x < 64) ms->turn[threadIdx.x] = a.freq.turn[threadIdx.x];
-    if (threadIdx.x == 128) {
+    if (threadIdx.x == 64) {
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&ms->item_full[i], 1);
-            mbar_init(&ms->item_empty[i], kConsumers);
+            mbar_init(&ms->item_empty[i], C::kConsumers);
         }
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&ms->full[i], 1);
-            mbar_init(&ms->empty[i], kConsumers);
+            mbar_init(&ms->empty[i], C::kConsumers);
         }
         ms->abort = 0;
         fence_mbar_init();
@@ -518,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, MT == 1 ? 2 : 1) kv_few_kernel(const
     __syncthreads();
     pdl_wait();
     CSLA_TL_WAITED();
-    if (threadIdx.x >= 32 * kConsumers)
+    if (threadIdx.x >= 32 * C::kConsumers)
         producer<D, MT>(a, km, vm, smem, ms);
     else
         consumer<D, MT, QBF16, OBF16>(a, smem, ms);
@@ -529,7 +511,7 @@ cudaError_t launch(const KvAttendArgs &a, const CUtensorMap &km, const CUtensorM
     auto kern = kv_few_kernel<D, MT, QB, OB>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D, MT>());
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(grid), dim3(kThreads), smem_bytes<D, MT>(), s, a, km, vm);
+    return launch_pdl(kern, dim3(grid), dim3(Cfg<D, MT>::kThreads), smem_bytes<D, MT>(), s, a, km, vm);
 }
 template <int D, int MT>
 cudaError_t launch_types(const KvAttendArgs &a, bool qb, bool ob, const CUtensorMap &km, const CUtensorMap &vm,
@@ -542,12 +524,15 @@ cudaError_t launch_types(const KvAttendArgs &a, bool qb, bool ob, const CUtensor
 
 cudaError_t launch_kv_few(const KvAttendArgs &a, bool q_bf16, bool out_bf16, int rows, const CUtensorMap &km,
                           const CUtensorMap &vm, int num_sms, long long items, cudaStream_t stream) {
-    const unsigned grid = (unsigned)(items < 2 * num_sms ? items : 2 * num_sms);
+    const int ctas = (rows <= 32 ? 2 : 1) * num_sms;
+    const unsigned grid = (unsigned)(items < ctas ? items : ctas);
     if (a.D == 64)
-        return rows <= 16 ? launch_types<64, 1>(a, q_bf16, out_bf16, km, vm, grid, stream)
-                          : launch_types<64, 2>(a, q_bf16, out_bf16, km, vm, grid, stream);
-    return rows <= 16 ? launch_types<128, 1>(a, q_bf16, out_bf16, km, vm, grid, stream)
-                      : launch_types<128, 2>(a, q_bf16, out_bf16, km, vm, grid, stream);
+        return rows <= 16   ? launch_types<64, 1>(a, q_bf16, out_bf16, km, vm, grid, stream)
+               : rows <= 32 ? launch_types<64, 2>(a, q_bf16, out_bf16, km, vm, grid, stream)
+                            : launch_types<64, 4>(a, q_bf16, out_bf16, km, vm, grid, stream);
+    return rows <= 16   ? launch_types<128, 1>(a, q_bf16, out_bf16, km, vm, grid, stream)
+           : rows <= 32 ? launch_types<128, 2>(a, q_bf16, out_bf16, km, vm, grid, stream)
+                        : launch_types<128, 4>(a, q_bf16, out_bf16, km, vm, grid, stream);
 }
 
 }  // namespace csla
