@@ -25,9 +25,14 @@
 //   warps 8-11      Q: norm and rotation in fp32, rounded to bf16 into the swizzled operand;
 //                   a row tile of few rows keeps the rounding's rest as a second bf16
 //                   operand (its product costs what memory-bound items have to spare);
-//   warp 12         tcgen05.mma: S = Q K^T, O += P V (P from tensor memory);
-//   warp 13         TMA: K and V tiles, in the order the products take them, into one ring;
-//   warp 14         the items: walks the batch 32 requests at a time.
+//   warp 12         tcgen05.mma S = Q K^T;
+//   warp 13         TMA: K and V tiles into a ring each;
+//   warp 14         the items: walks the batch 32 requests at a time;
+//   warp 15         tcgen05.mma O += P V (P from tensor memory).
+// Tensor memory (512 columns): O of both streams 256, P of both 128, and one S
+// of 128 that the streams use in turn.  A softmax thread takes its whole row of S
+// into registers at once, so the S columns are free for the other stream's
+// scores while it forms its weights, and a stream's next scores wait for it.
 #include "kv.cuh"
 
 namespace csla {
@@ -43,12 +48,13 @@ struct Cfg {
     static constexpr int kKB = D / 64;                  // 64-dim blocks (128-byte rows)
     static constexpr int kBlk = 128 * 128;              // bytes of a block: 128 rows x 128 B
     static constexpr int kTileBytes = kKB * kBlk;
-    static constexpr int kStages = D == 128 ? 5 : 10;
+    static constexpr int kKStages = D == 128 ? 3 : 5, kVStages = D == 128 ? 2 : 5;
     static constexpr int kOffQ = 0;
-    static constexpr int kOffKV = 2 * kTileBytes;
-    static constexpr int kOffMisc = kOffKV + kStages * kTileBytes;
-    // TMEM columns: S (P over it) of each stream, then O of each stream
-    static constexpr int kColS = 0, kColO = 256;
+    static constexpr int kOffK = 2 * kTileBytes;
+    static constexpr int kOffV = kOffK + kKStages * kTileBytes;
+    static constexpr int kOffMisc = kOffV + kVStages * kTileBytes;
+    // TMEM columns: one S, which the streams use in turn, P of each stream, O of each stream
+    static constexpr int kColS = 0, kColP = 128, kColO = 256;
 };
 
 struct Item {
@@ -67,8 +73,8 @@ struct Item {
 struct Misc {
     Item item[kItems];
     uint64_t item_full[kItems], item_empty[kItems];
-    uint64_t kv_full[10], kv_empty[10];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], drain;
+    uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
+    uint64_t q_full[2], q_empty[2], s_full[2], s_free[2], p_full[2], pv_done[2], drain[2];
     int bad[kFlags];     // tile's page is not mapped
     unsigned long long turn[64];   // rotation frequencies
     uint32_t tmem;
@@ -81,12 +87,6 @@ constexpr int smem_bytes() {
 }
 
 // ---------------------------------------------------------------- items
-// First item of stream s, and whether it takes tile t.
-__device__ __forceinline__ bool takes(const Item &it, int s, int t) {
-    if (it.paired) return s == 0 ? t < it.hi0 : t >= it.lo1;
-    return ((t - it.lo) & 1) == s;
-}
-
 // Item `local` of a request, in the order: row tiles from the last (the longest
 // under the causal mask) to the first; heads inside, unless the request's
 // keys would not stay in L2 while all heads are in use.
@@ -157,28 +157,42 @@ __device__ __forceinline__ bool next_item(Misc *ms, int n, Item *it) {
 }
 
 // ---------------------------------------------------------------- TMA role
+// A ring's next stage and the parity of its phase.
+template <int N>
+struct Ring {
+    int stage = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++stage == N) {
+            stage = 0;
+            phase ^= 1;
+        }
+    }
+};
+
 template <int D>
 struct Loader {
+    using C = Cfg<D>;
     const KvAttendArgs &a;
-    const CUtensorMap &km, &vm;
     uint8_t *smem;
     Misc *ms;
     int lane;
-    int st = 0, issued = 0;   // ring stage and tiles issued so far
-    int tiles = 0;            // key tiles so far (flag index)
+    Ring<C::kKStages> kr;     // (phase of the stage's next filling)
+    Ring<C::kVStages> vr;
+    int ks = 0, vs = 0;       // tiles issued
     // page ids of 64 tiles from `at` on, two per lane
     int at = 0, pg0 = -1, pg1 = -1;
 
-    __device__ int fetch(const Item &it, int t) const {
+    __device__ __forceinline__ int fetch(const Item &it, int t) const {
         return t < it.hi ? a.bt.block_table[(long long)it.slot * a.bt.bt_stride + t] : -1;
     }
-    __device__ void begin(const Item &it) {
+    __device__ __forceinline__ void begin(const Item &it) {
         at = it.lo;
         pg0 = fetch(it, at + lane);
         pg1 = fetch(it, at + 32 + lane);
     }
-    __device__ int page(const Item &it, int t) {
-        // tiles are asked for in ascending order, V up to two behind K
+    __device__ __forceinline__ int page(const Item &it, int t) {
+        // tiles are asked for in ascending order, V two behind K at most
         if (t >= at + 64) {
             at += 32;
             pg0 = pg1;
@@ -187,56 +201,57 @@ struct Loader {
         const int d = t - at;
         return d < 32 ? __shfl_sync(0xffffffffu, pg0, d & 31) : __shfl_sync(0xffffffffu, pg1, d & 31);
     }
-    __device__ bool load(const Item &it, int t, bool is_v) {
-        using C = Cfg<D>;
-        int pg = page(it, t);
-        if (issued >= C::kStages &&
-            !warp_all(kv_wait(&ms->kv_empty[st], (issued / C::kStages - 1) & 1, &ms->abort)))
-            return false;
-        const bool bad = pg < 0 || pg >= a.bt.n_pages;
+    template <int N>
+    __device__ __forceinline__ bool load(const CUtensorMap &map, Ring<N> &r, int issued, uint64_t *full, uint64_t *empty,
+                                         uint8_t *ring, int row) {
+        if (issued >= N && !warp_all(kv_wait(&empty[r.stage], r.phase ^ 1, &ms->abort))) return false;
         if (lane == 0) {
-            if (!is_v) {
-                ms->bad[tiles % kFlags] = bad;
-                if (bad) set_dev_err(CSLA_DEVERR_PAGE);
-            }
-            uint64_t *bar = &ms->kv_full[st];
+            uint64_t *bar = &full[r.stage];
             mbar_arrive_expect_tx(bar, C::kTileBytes);
-            uint8_t *dst = smem + C::kOffKV + st * C::kTileBytes;
-            // (an unmapped page's tile is page 0's, masked)
-            const int row = ((bad ? 0 : pg) * a.HK + it.hk) * kTile;
+            uint8_t *dst = ring + r.stage * C::kTileBytes;
 #pragma unroll
-            for (int kb = 0; kb < C::kKB; ++kb) tma_load_2d(dst + kb * C::kBlk, is_v ? &vm : &km, 64 * kb, row, bar);
+            for (int kb = 0; kb < C::kKB; ++kb) tma_load_2d(dst + kb * C::kBlk, &map, 64 * kb, row, bar);
         }
         __syncwarp();
-        if (!is_v) ++tiles;
-        ++issued;
-        st = st + 1 == C::kStages ? 0 : st + 1;
+        r.next();
         return true;
+    }
+    __device__ __forceinline__ bool load_k(const Item &it, int t, const CUtensorMap &map) {
+        const int pg = page(it, t);
+        const bool bad = pg < 0 || pg >= a.bt.n_pages;
+        if (lane == 0) {
+            ms->bad[ks % kFlags] = bad;
+            if (bad) set_dev_err(CSLA_DEVERR_PAGE);
+        }
+        // (an unmapped page's tile is page 0's, masked)
+        return load(map, kr, ks++, ms->k_full, ms->k_empty, smem + C::kOffK, ((bad ? 0 : pg) * a.HK + it.hk) * kTile);
+    }
+    __device__ __forceinline__ bool load_v(const Item &it, int t, const CUtensorMap &map) {
+        const int pg = page(it, t);
+        const bool bad = pg < 0 || pg >= a.bt.n_pages;
+        return load(map, vr, vs++, ms->v_full, ms->v_empty, smem + C::kOffV, ((bad ? 0 : pg) * a.HK + it.hk) * kTile);
     }
 };
 
 template <int D>
 __device__ void load_role(const KvAttendArgs &a, const CUtensorMap &km, const CUtensorMap &vm, uint8_t *smem, Misc *ms) {
     using C = Cfg<D>;
-    Loader<D> L{a, km, vm, smem, ms, (int)(threadIdx.x & 31)};
+    Loader<D> L{a, smem, ms, (int)(threadIdx.x & 31)};
     bool ok = true;
     Item it;
     for (int n = 0; ok && next_item(ms, n, &it); ++n) {
         L.begin(it);
-        if (it.paired) {
-            for (int t = it.lo; ok && t < it.hi; ++t) ok = L.load(it, t, false) && L.load(it, t, true);
-        } else {
-            ok = L.load(it, it.lo, false);
-            if (ok && it.lo + 1 < it.hi) ok = L.load(it, it.lo + 1, false);
-            for (int t = it.lo; ok && t < it.hi; ++t) {
-                ok = L.load(it, t, true);
-                if (ok && t + 2 < it.hi) ok = L.load(it, t + 2, false);
-            }
+        const int d = it.paired ? 1 : 2;   // V follows its K by d tiles: the order in which they are used
+        for (int t = it.lo; ok && t < it.hi + d; ++t) {
+            if (t < it.hi) ok = L.load_k(it, t, km);
+            if (ok && t - d >= it.lo) ok = L.load_v(it, t - d, vm);
         }
     }
     // copies in flight land before the CTA exits (all have, unless a wait gave up)
-    const int from = max(0, L.issued - C::kStages);
-    for (int i = from; i < L.issued; ++i) kv_wait(&ms->kv_full[i % C::kStages], (i / C::kStages) & 1, nullptr);
+    for (int i = max(0, L.ks - C::kKStages); i < L.ks; ++i)
+        kv_wait(&ms->k_full[i % C::kKStages], (i / C::kKStages) & 1, nullptr);
+    for (int i = max(0, L.vs - C::kVStages); i < L.vs; ++i)
+        kv_wait(&ms->v_full[i % C::kVStages], (i / C::kVStages) & 1, nullptr);
 }
 
 // ---------------------------------------------------------------- Q role
@@ -320,13 +335,14 @@ __device__ void q_role(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
     }
 }
 
-// ---------------------------------------------------------------- MMA role
-// The products of a tile are 8 to 16 instructions of 64 tensor cycles each,
-// all from one thread: what that thread does per instruction has to stay
-// below that.  So the descriptors' bases are made warp-uniform (a shuffle) and
-// every instruction adds a constant to the low word (address and leading offset, in
-// 16-byte units); the high word is the same for all operands (stride of
-// 8-row groups 1024 bytes, version 1, 128-byte swizzle).
+// ---------------------------------------------------------------- MMA roles
+// The products of a step are 8 to 16 instructions of 64 tensor cycles each,
+// and the tensor cores queue little: what the issuing thread does between two
+// steps is time they stand still.  So S and PV have a warp each, their only
+// order is what the barriers say, and a step's descriptors are a warp-uniform base
+// plus constants in the low word (address and leading offset, in 16-byte
+// units); the high word is the same for all operands (stride of 8-row groups
+// 1024 bytes, version 1, 128-byte swizzle).
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (kLayoutSW128 << 29);
 __device__ constexpr uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) { return (saddr >> 4) | (lbo_bytes >> 4) << 16; }
 
@@ -361,42 +377,25 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32
 }
 
 template <int D>
-struct Mma {
+__device__ void s_role(uint8_t *smem, Misc *ms) {
     using C = Cfg<D>;
-    uint8_t *smem;
-    Misc *ms;
-    int lane;
-    uint32_t tmem, q0, k0, v0;     // TMEM base; low descriptor words of Q, and of ring stage 0 as K and as V
-    int taken = 0;                 // ring tiles taken
-    int p_count[2] = {0, 0};       // P tiles taken per stream
-
-    // Next tile of the ring; its stage.
-    __device__ bool take(int *stage) {
-        *stage = taken % C::kStages;
-        if (!warp_all(kv_wait(&ms->kv_full[*stage], (taken / C::kStages) & 1, &ms->abort))) return false;
-        ++taken;
-        tc_fence_after();
-        return true;
-    }
-    // V rows outside [lo, hi) of the tile, which no row sees, to zero (their
-    // weights are zero, but 0 * NaN is not).
-    __device__ void clean_v(int stage, int lo, int hi) {
-        if (lo <= 0 && hi >= kTile) return;
-        uint8_t *v = smem + C::kOffKV + stage * C::kTileBytes;
-        for (int i = lane; i < kTile * 8; i += 32) {
-            const int row = i >> 3;
-            if (row >= lo && row < hi) continue;
-#pragma unroll
-            for (int kb = 0; kb < C::kKB; ++kb)
-                *reinterpret_cast<uint4 *>(v + kb * C::kBlk + i * 16) = make_uint4(0, 0, 0, 0);
+    constexpr uint32_t kId = idesc_bf16(128, kTile, false, false);
+    const uint32_t d = uniform(ms->tmem) + C::kColS;
+    const uint32_t q0 = uniform(desc_lo(smem_u32(smem + C::kOffQ), 16)), k0 = uniform(desc_lo(smem_u32(smem + C::kOffK), 16));
+    Ring<C::kKStages> kr;
+    uint32_t free0 = 0, free1 = 0;   // phases of s_free
+    int pending = -1;                // stream of the last S, not yet waited for
+    Item it;
+    // S of stream s = Q K^T (both terms of Q for an unpaired item) from K's stage, once the scores before it have been read
+    auto step = [&](int s, bool paired, bool last) {
+        if (pending >= 0) {
+            if (!warp_all(kv_wait(&ms->s_free[pending], pending ? free1 : free0, &ms->abort))) return false;
+            if (pending) free1 ^= 1;
+            else free0 ^= 1;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-    }
-    // S of stream s = Q K^T (both terms of Q for an unpaired item)
-    __device__ void s_mma(int s, int stage, bool paired) {
-        constexpr uint32_t kId = idesc_bf16(128, kTile, false, false);
-        const uint32_t k = uniform(k0 + (uint32_t)stage * (C::kTileBytes >> 4)), d = uniform(tmem + C::kColS + 128 * s);
+        pending = s;
+        tc_fence_after();
+        const uint32_t k = uniform(k0 + (uint32_t)kr.stage * (C::kTileBytes >> 4));
         const uint32_t q = uniform(q0 + (paired && s ? C::kTileBytes >> 4 : 0));
         if (elect_one()) {
 #pragma unroll
@@ -412,119 +411,110 @@ struct Mma {
                 }
             }
             umma_commit(&ms->s_full[s]);
-        }
-        __syncwarp();
-    }
-    // O of stream s (+)= P V once P is there
-    __device__ bool pv_mma(int s, int stage, bool first) {
-        constexpr uint32_t kId = idesc_bf16(128, D, false, true);
-        if (!warp_all(kv_wait(&ms->p_full[s], p_count[s] & 1, &ms->abort))) return false;
-        ++p_count[s];
-        tc_fence_after();
-        const uint32_t v = uniform(v0 + (uint32_t)stage * (C::kTileBytes >> 4)), d = uniform(tmem + C::kColO + D * s);
-        const uint32_t p = uniform(tmem + C::kColS + 128 * s), acc = uniform(first ? 0u : 1u);
-        if (elect_one()) {
-#pragma unroll
-            for (int i = 0; i < kTile / 16; ++i) umma_ts(d, p + 8 * i, v + (i * 2048 >> 4), kId, i > 0 ? 1u : acc);
+            if (last) {   // Q is free
+                umma_commit(&ms->q_empty[s]);
+                if (!paired) umma_commit(&ms->q_empty[s ^ 1]);
+            }
         }
         __syncwarp();
         return true;
-    }
-    __device__ void commit(uint64_t *bar) {
-        if (elect_one()) umma_commit(bar);
-        __syncwarp();
-    }
-
-    __device__ void free_q() {
-        commit(&ms->q_empty[0]);
-        commit(&ms->q_empty[1]);
-    }
-
-    __device__ bool item_paired(const Item &it, const int *bad, int tiles) {
-        int kst, vst;
-        if (!take(&kst)) return false;
-        for (int s = 0; s < 2; ++s) {
-            if (takes(it, s, it.lo)) s_mma(s, kst, true);
-            // Q is free after the stream's last S (or at once, if it has none)
-            const int from = max(it.lo, it.lo1), to = s == 0 ? it.hi0 : it.hi;
-            if ((s == 0 ? it.lo : from) >= to || (takes(it, s, it.lo) && to == it.lo + 1)) commit(&ms->q_empty[s]);
-        }
-        commit(&ms->kv_empty[kst]);
-        bool first[2] = {true, true};
-        for (int t = it.lo; t < it.hi; ++t) {
-            if (!take(&vst)) return false;
-            const bool b = bad[(tiles + t - it.lo) % kFlags];
-            clean_v(vst, b ? 0 : it.k_lo - t * kTile, b ? 0 : it.k_hi - t * kTile);
-            const bool more = t + 1 < it.hi;
-            kst = -1;
-            for (int s = 0; s < 2; ++s) {
-                if (takes(it, s, t)) {
-                    if (!pv_mma(s, vst, first[s])) return false;
-                    first[s] = false;
-                    if (!more || !takes(it, s, t + 1)) commit(&ms->o_full[s]);
-                }
-                if (s == 1) commit(&ms->kv_empty[vst]);
-                if (more && takes(it, s, t + 1)) {
-                    if (kst < 0 && !take(&kst)) return false;
-                    s_mma(s, kst, true);
-                    if (t + 2 >= it.hi || !takes(it, s, t + 2)) commit(&ms->q_empty[s]);   // its last S
-                }
-            }
-            if (more) {
-                if (kst < 0 && !take(&kst)) return false;   // (no stream takes the tile: not reached)
-                commit(&ms->kv_empty[kst]);
-            }
-        }
-        return true;
-    }
-    __device__ bool item_single(const Item &it, const int *bad, int tiles) {
-        int kst, vst;
-        for (int s = 0; s < 2 && it.lo + s < it.hi; ++s) {
-            if (!take(&kst)) return false;
-            s_mma(s, kst, false);
-            commit(&ms->kv_empty[kst]);
-        }
-        if (it.lo + 2 >= it.hi) free_q();
-        for (int t = it.lo; t < it.hi; ++t) {
-            const int s = (t - it.lo) & 1;
-            if (!take(&vst)) return false;
-            const bool b = bad[(tiles + t - it.lo) % kFlags];
-            clean_v(vst, b ? 0 : it.k_lo - t * kTile, b ? 0 : it.k_hi - t * kTile);
-            if (!pv_mma(s, vst, t - it.lo < 2)) return false;
-            commit(&ms->kv_empty[vst]);
-            if (t + 2 < it.hi) {
-                if (!take(&kst)) return false;
-                s_mma(s, kst, false);
-                commit(&ms->kv_empty[kst]);
-                if (t + 3 >= it.hi) free_q();
-            } else {
-                commit(&ms->o_full[s]);
-            }
-        }
-        return true;
-    }
-};
-
-template <int D>
-__device__ void mma_role(uint8_t *smem, Misc *ms) {
-    using C = Cfg<D>;
-    const uint32_t kv = smem_u32(smem + C::kOffKV);
-    Mma<D> m{smem, ms, (int)(threadIdx.x & 31), ms->tmem, desc_lo(smem_u32(smem + C::kOffQ), 16), desc_lo(kv, 16),
-             desc_lo(kv, C::kBlk)};
+    };
     bool ok = true;
-    int tiles = 0;
-    Item it;
     for (int n = 0; ok && next_item(ms, n, &it); ++n) {
-        for (int s = 0; ok && s < 2; ++s) ok = warp_all(kv_wait(&ms->q_full[s], n & 1, &ms->abort));
-        if (!ok) break;
-        if (n == 0 && m.lane == 0) CSLA_TL_MARK_ANY(1);
-        tc_fence_after();
-        ok = it.paired ? m.item_paired(it, ms->bad, tiles) : m.item_single(it, ms->bad, tiles);
-        tiles += it.hi - it.lo;
+        ok = warp_all(kv_wait(&ms->q_full[0], n & 1, &ms->abort) && kv_wait(&ms->q_full[1], n & 1, &ms->abort));
+        if (n == 0 && (threadIdx.x & 31) == 0) CSLA_TL_MARK_ANY(1);
+        const bool paired = it.paired;
+#pragma unroll 1
+        for (int t = it.lo; ok && t < it.hi; ++t) {
+            ok = warp_all(kv_wait(&ms->k_full[kr.stage], kr.phase, &ms->abort));
+            if (!ok) break;
+            if (paired) {
+                if (t < it.hi0) ok = step(0, true, t + 1 == it.hi0);
+                if (ok && t >= it.lo1) ok = step(1, true, t + 1 == it.hi);
+            } else {
+                ok = step((t - it.lo) & 1, false, t + 1 == it.hi);
+            }
+            if (elect_one()) umma_commit(&ms->k_empty[kr.stage]);
+            __syncwarp();
+            kr.next();
+        }
+        // a stream without a key tile has not used its Q
+        if (ok && paired && elect_one()) {
+            if (it.hi0 <= it.lo) umma_commit(&ms->q_empty[0]);
+            if (it.lo1 >= it.hi) umma_commit(&ms->q_empty[1]);
+        }
+        __syncwarp();
     }
     // products in flight end before tensor memory is freed (all have, unless a wait gave up)
-    m.commit(&ms->drain);
-    kv_wait(&ms->drain, 0, nullptr);
+    if (elect_one()) umma_commit(&ms->drain[0]);
+    __syncwarp();
+    kv_wait(&ms->drain[0], 0, nullptr);
+}
+
+template <int D>
+__device__ void pv_role(uint8_t *smem, Misc *ms) {
+    using C = Cfg<D>;
+    constexpr uint32_t kId = idesc_bf16(128, D, false, true);
+    const int lane = threadIdx.x & 31;
+    const uint32_t tmem = uniform(ms->tmem), v0 = uniform(desc_lo(smem_u32(smem + C::kOffV), C::kBlk));
+    Ring<C::kVStages> vr;
+    uint32_t p0 = 0, p1 = 0;   // phases of p_full
+    int tiles = 0;
+    Item it;
+    // O of stream s (+)= P V once P is there
+    auto step = [&](int s, bool first) {
+        if (!warp_all(kv_wait(&ms->p_full[s], s ? p1 : p0, &ms->abort))) return false;
+        if (s) p1 ^= 1;
+        else p0 ^= 1;
+        tc_fence_after();
+        const uint32_t v = uniform(v0 + (uint32_t)vr.stage * (C::kTileBytes >> 4)), acc = uniform(first ? 0u : 1u);
+        const uint32_t o = uniform(tmem + C::kColO + D * s), p = uniform(tmem + C::kColP + 64 * s);
+        if (elect_one()) {
+#pragma unroll
+            for (int i = 0; i < kTile / 16; ++i) umma_ts(o, p + 8 * i, v + (i * 2048 >> 4), kId, i > 0 ? 1u : acc);
+            umma_commit(&ms->pv_done[s]);
+        }
+        __syncwarp();
+        return true;
+    };
+    bool ok = true;
+    for (int n = 0; ok && next_item(ms, n, &it); ++n) {
+        const bool paired = it.paired;
+#pragma unroll 1
+        for (int t = it.lo; ok && t < it.hi; ++t) {
+            ok = warp_all(kv_wait(&ms->v_full[vr.stage], vr.phase, &ms->abort));
+            if (!ok) break;
+            // V rows that no row of the item sees are set to zero: their
+            // weights are zero, but 0 * NaN is not
+            const bool bad = ms->bad[(tiles + t - it.lo) % kFlags];
+            const int lo = it.k_lo - t * kTile, hi = bad ? 0 : it.k_hi - t * kTile;
+            if (lo > 0 || hi < kTile) {
+                uint8_t *v = smem + C::kOffV + vr.stage * C::kTileBytes;
+                for (int i = lane; i < kTile * 8; i += 32) {
+                    const int row = i >> 3;
+                    if (row >= lo && row < hi) continue;
+#pragma unroll
+                    for (int kb = 0; kb < C::kKB; ++kb)
+                        *reinterpret_cast<uint4 *>(v + kb * C::kBlk + i * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            if (paired) {
+                if (t < it.hi0) ok = step(0, t == it.lo);
+                if (ok && t >= it.lo1) ok = step(1, t == it.lo1);
+            } else {
+                ok = step((t - it.lo) & 1, t < it.lo + 2);
+            }
+            if (elect_one()) umma_commit(&ms->v_empty[vr.stage]);
+            __syncwarp();
+            vr.next();
+        }
+        tiles += it.hi - it.lo;
+    }
+    if (elect_one()) umma_commit(&ms->drain[1]);
+    __syncwarp();
+    kv_wait(&ms->drain[1], 0, nullptr);
 }
 
 // ---------------------------------------------------------------- softmax role
@@ -553,10 +543,10 @@ __device__ void softmax_role(const KvAttendArgs &a, Misc *ms, int s) {
     using C = Cfg<D>;
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const uint32_t tw = ms->tmem + ((uint32_t)(warp * 32) << 16);
-    const uint32_t ts = tw + C::kColS + 128 * s, to = tw + C::kColO + D * s;
+    const uint32_t ts = tw + C::kColS, tp = tw + C::kColP + 64 * s, to = tw + C::kColO + D * s;
     const int G = a.HQ / a.HK;
     const float sc = a.scale * kLog2e;
-    int s_count = 0, o_count = 0, tiles = 0;
+    int s_count = 0, tiles = 0;   // S tiles taken; the PV of tile s_count - 1 frees P and leaves O
     Item it;
     for (int n = 0; next_item(ms, n, &it); ++n) {
         const int row = it.row0 + (it.paired ? 128 * s : 0) + 32 * warp + lane;
@@ -582,6 +572,8 @@ __device__ void softmax_role(const KvAttendArgs &a, Misc *ms, int s) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32x32(ts + 32 * c, v[c]);
                 tmem_wait_ld();
+                tc_fence_before();
+                mbar_arrive_warp(&ms->s_free[s]);
                 if (cut) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
@@ -599,6 +591,10 @@ __device__ void softmax_role(const KvAttendArgs &a, Misc *ms, int s) {
                 }
                 const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc);
                 const bool grow = mn > m + kGrow;   // (also from -inf)
+                if (any) {   // P and O of the tile before
+                    if (!warp_all(kv_wait(&ms->pv_done[s], s_count & 1, &ms->abort))) return;
+                    tc_fence_after();
+                }
                 if (__any_sync(0xffffffffu, grow)) {
                     const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - mn)) : 1.f;
                     if (grow) m = mn;
@@ -629,12 +625,17 @@ __device__ void softmax_role(const KvAttendArgs &a, Misc *ms, int s) {
                         sum[i & 1] = add2(sum[i & 1], pack2(p0, p1));
                         o[i] = pack_bf16(p0, p1);
                     }
-                    tmem_st32x16(ts + 16 * c, o);
+                    tmem_st32x16(tp + 16 * c, o);
                 }
                 float l0, l1;
                 unpack2(add2(sum[0], sum[1]), &l0, &l1);
                 l += l0 + l1;
                 tmem_wait_st();
+                any = true;
+            } else {
+                mbar_arrive_warp(&ms->s_free[s]);
+                // (this warp's arrival for P must not come a tile early)
+                if (any && !warp_all(kv_wait(&ms->pv_done[s], s_count & 1, &ms->abort))) return;
                 any = true;
             }
             tc_fence_before();
@@ -643,9 +644,7 @@ __device__ void softmax_role(const KvAttendArgs &a, Misc *ms, int s) {
         }
         tiles += it.hi - it.lo;
         if (t0 < t1) {
-            if (!warp_all(kv_wait(&ms->o_full[s], o_count & 1, &ms->abort))) return;
-            if (s == 0 && o_count == 0 && threadIdx.x == 0) CSLA_TL_MARK_ANY(4);
-            ++o_count;
+            if (!warp_all(kv_wait(&ms->pv_done[s], (s_count - 1) & 1, &ms->abort))) return;
             tc_fence_after();
         }
         if (idle) {
@@ -727,20 +726,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
     if (threadIdx.x == 0) {
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&ms->item_full[i], 1);
-            mbar_init(&ms->item_empty[i], 14);   // softmax 8, Q 4, MMA, TMA
+            mbar_init(&ms->item_empty[i], 15);   // softmax 8, Q 4, S, PV, TMA
         }
-        for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&ms->kv_full[i], 1);
-            mbar_init(&ms->kv_empty[i], 1);
+        for (int i = 0; i < 5; ++i) {
+            mbar_init(&ms->k_full[i], 1);
+            mbar_init(&ms->k_empty[i], 1);
+            mbar_init(&ms->v_full[i], 1);
+            mbar_init(&ms->v_empty[i], 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&ms->q_full[s], 4);
             mbar_init(&ms->q_empty[s], 1);
             mbar_init(&ms->s_full[s], 1);
             mbar_init(&ms->p_full[s], 4);
-            mbar_init(&ms->o_full[s], 1);
+            mbar_init(&ms->s_free[s], 4);
+            mbar_init(&ms->pv_done[s], 1);
         }
-        mbar_init(&ms->drain, 1);
+        mbar_init(&ms->drain[0], 1);
+        mbar_init(&ms->drain[1], 1);
         ms->abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&km);
@@ -762,11 +765,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == 12)
-            mma_role<D>(smem, ms);
+            s_role<D>(smem, ms);
         else if (warp == 13)
             load_role<D>(a, km, vm, smem, ms);
         else if (warp == 14)
             sched_role(a, ms);
+        else
+            pv_role<D>(smem, ms);
     }
     __syncwarp();
     tc_fence_before();
