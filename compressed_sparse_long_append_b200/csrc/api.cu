@@ -766,10 +766,13 @@ static long long kv_most_part_rows(const csla_kv_cfg *c, int B, int N, int max_n
         tokens = least(N, B * least(max_new, 128 / G));
         rows += tokens * c->HQ * 2 * parts(kKvSingle);
     }
-    if (max_new * G > 128 && parts(kKvPaired) > 1) {
+    if (max_new * G > 128 && nt > kv_min_tiles(kKvPaired)) {
         // a request has chunks * 256 * R * HK rows at most, chunks <= units / (R * HK)
         const long long each = 256ll * kv_units(kKvPaired), n = least(B, N * G / 129);
         rows += least(n * each, (long long)N * c->HQ * parts(kKvPaired));
+        // or the row tiles left over from full rounds, fewer than half of units of them, are cut in up to 4
+        if (nt >= 32 && (max_new * G + 255) / 256 * HK > kv_units(kKvPaired))
+            rows += n * (kv_units(kKvPaired) + 4 * HK) * 256;
     }
     return rows;
 }
@@ -780,7 +783,7 @@ struct KvWorkspace {
 static KvWorkspace kv_workspace(const csla_kv_cfg *c, int B, long long rows) {
     KvWorkspace w{0, 0, 0};
     if (rows == 0) return w;
-    w.ml = up16((size_t)B * 8);
+    w.ml = up16((size_t)B * sizeof(KvJoin));
     w.o = w.ml + up16((size_t)rows * 8);
     w.total = w.o + (size_t)rows * c->D * 4;
     return w;
@@ -817,7 +820,7 @@ int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
     const KvWorkspace w = kv_workspace(cfg, B, rows);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     if (rows) {
-        a.part_base = reinterpret_cast<long long *>(ws);
+        a.part_req = reinterpret_cast<KvJoin *>(ws);
         a.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
         a.part_o = reinterpret_cast<float *>(ws + w.o);
     }
@@ -836,8 +839,8 @@ int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
             !encode_bf16_2d(&vm, kv->v, cfg->D, cache_rows, kv_few_box(cfg->D)))
             return CSLA_ERR_CUDA;
         const long long m = kv_min_tiles(kKvFew);
-        e = launch_kv_few(a, q16, o16, (int)(most_rows < kKvFewRows ? most_rows : kKvFewRows), km, vm,
-                          num_sms_current(), (long long)B * cfg->HK * ((nt + m - 1) / m), st);
+        e = launch_kv_few(a, q16, o16, km, vm, num_sms_current(),
+                          (long long)B * cfg->HK * ((nt + m - 1) / m), st);
     }
     if (e == cudaSuccess && most_rows > kKvFewRows) {
         CUtensorMap km, vm;

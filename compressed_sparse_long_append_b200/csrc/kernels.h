@@ -293,6 +293,10 @@ struct KvAppendArgs {
 };
 cudaError_t launch_kv_append(const KvAppendArgs &a, bool bf16, cudaStream_t stream);
 
+struct KvJoin {
+    int n0, T, L, pad;   // T = 0: nothing to join
+    long long base;      // first partial row
+};
 struct KvAttendArgs {
     KvBatch bt;
     int D, HQ, HK, d_rope, pairs, window;
@@ -304,26 +308,28 @@ struct KvAttendArgs {
     const float *sink, *gamma_q;    // null: none
     void *out;
     // workspace: first partial row of each request [B], (m, l) and O of the partial rows
-    long long *part_base;
+    KvJoin *part_req;   // [B], what the join needs of a request
     float2 *part_ml;
     float *part_o;
 };
 
 // How the attention cuts a request of T new tokens (context L): a function of
 // T, L and the layer alone.  rows = T*G rows per KV head.
-//   few     up to 64 rows: kv_few_kernel, R = 1;
+//   few     up to 16 rows: kv_few_kernel, R = 1;
 //   single  up to 128 rows: kv_attend_kernel, R = 1, its two streams take key tiles in turn;
 //   paired  more: kv_attend_kernel, R row tiles of 256.
-// Keys are cut into chunks of c tiles, nch at most per row tile, so that a
-// request of few row tiles still fills the SMs.
+// The keys of row tiles i < Rs are cut into chunks of c tiles, nch at most per
+// row tile: all of them when the request has few row tiles for the SMs, else those
+// left over from full rounds over the SMs (512 row tiles of all heads on 148
+// SMs are 3 rounds and 68 left: cut in two they take half a round, not a whole one).
 enum { kKvFew = 0, kKvSingle = 1, kKvPaired = 2 };
 struct KvPlan {
-    int rows, R, kind, c, nch, T, G, heads_inside;
+    int rows, R, Rs, rows_s, kind, c, nch, T, G, heads_inside;   // rows_s: rows of the cut row tiles
 };
-constexpr int kKvFewRows = 64;
+constexpr int kKvFewRows = 16;
 // items that a long request is cut into (all heads), and the least tiles of a chunk, by kind
 __host__ __device__ constexpr int kv_units(int kind) { return kind == kKvPaired ? 148 : 296; }
-__host__ __device__ constexpr int kv_min_tiles(int kind) { return kind == kKvPaired ? 8 : (kind == kKvSingle ? 4 : 2); }
+__host__ __device__ constexpr int kv_min_tiles(int kind) { return kind == kKvPaired ? 8 : (kind == kKvSingle ? 8 : 2); }
 
 // Key tiles of row tile i: [lo, hi); of its two halves: first half [lo, hi0), second [lo1, hi).
 // [k_lo, k_hi): the positions that some row sees.
@@ -368,28 +374,39 @@ __host__ __device__ inline KvPlan kv_plan(int T, int L, int G, int HK, int windo
     // (32-bit divisions only: this runs ahead of every item's first load)
     const unsigned most = kv_units(p.kind) / (unsigned)(HK * p.R);   // chunks
     int c = most > 1 ? (int)((nt + most - 1) / most) : nt;
-    int least = kv_min_tiles(p.kind);
-    // a partial of r rows weighs r / 128 of a tile (written and read): an eighth of a chunk at most
-    if (p.kind == kKvFew && p.rows > 8 * least) least = p.rows / 8;
+    const int least = kv_min_tiles(p.kind);
     if (c < least) c = least;
     if (c > nt) c = nt;
+    p.Rs = p.kind == kKvSingle || c < nt ? p.R : 0;
+    if (p.kind == kKvPaired && most <= 1 && window == 0 && L - T >= T) {
+        // more row tiles than SMs, all of about nt tiles
+        const int sms = kv_units(kKvPaired), left = HK * p.R % sms, cuts = left ? sms / left : 1;
+        if (cuts > 1 && nt >= 32 && HK * p.R < 16 * sms) {
+            p.Rs = (left + HK - 1) / HK;
+            c = (nt + (cuts < 4 ? cuts : 4) - 1) / (cuts < 4 ? cuts : 4);
+        }
+    }
     p.c = c;
-    p.nch = (nt + c - 1) / c;
+    p.nch = p.Rs ? (nt + c - 1) / c : 1;
+    p.rows_s = p.Rs == p.R ? p.rows : 256 * p.Rs;
     // K and V of all heads below half of L2: heads in turn, longest row tiles first
     p.heads_inside = (long long)L * HK * D * 4 <= (64ll << 20);
     return p;
 }
-// Partials of a row of row tile g: 1 means it is written out at once.
-__host__ __device__ inline int kv_parts(const KvPlan &p, const KvRange &g) {
+// Items of a request: row tiles Rs .. R-1 once per head, the cut ones nch times.
+__host__ __device__ inline int kv_items(const KvPlan &p, int HK) { return HK * (p.R - p.Rs + p.Rs * p.nch); }
+// Partials of a row of row tile i (keys g): 1 means it is written out at once.
+__host__ __device__ inline int kv_parts(const KvPlan &p, const KvRange &g, int i) {
+    if (i >= p.Rs) return 1;
     const int nt = g.hi - g.lo, n = (nt + p.c - 1) / p.c;
     return p.kind == kKvSingle && nt > 1 ? 2 * n : n;
 }
-// Partial rows that a request may need.
-__host__ __device__ inline long long kv_part_rows(const KvPlan &p, int T, int HQ) {
-    if (p.kind == kKvSingle ? p.c == 1 : p.nch == 1) return 0;
-    return (p.kind == kKvSingle ? 2ll : 1ll) * p.nch * T * HQ;
+// Partial rows that a request may need (rows_s of each part and head).
+__host__ __device__ inline long long kv_part_rows(const KvPlan &p, int HK) {
+    if (p.Rs == 0 || (p.kind == kKvSingle ? p.c == 1 : p.nch == 1)) return 0;
+    return (p.kind == kKvSingle ? 2ll : 1ll) * p.nch * p.rows_s * HK;
 }
-cudaError_t launch_kv_few(const KvAttendArgs &a, bool q_bf16, bool out_bf16, int rows, const CUtensorMap &km,
+cudaError_t launch_kv_few(const KvAttendArgs &a, bool q_bf16, bool out_bf16, const CUtensorMap &km,
                           const CUtensorMap &vm, int num_sms, long long items, cudaStream_t stream);
 // Tokens of a ring stage of kv_few_kernel (the height of its tensor maps' boxes).
 inline int kv_few_box(int D) { return D == 128 ? 64 : 128; }

@@ -74,8 +74,8 @@ struct KvWalk {
                 if (r.err && blockIdx.x == 0) set_dev_err(r.err);
                 if (r.ok) {
                     p = kv_plan(r.T, r.L, a.HQ / a.HK, a.HK, a.window, a.D);
-                    items = (kinds >> p.kind) & 1 ? a.HK * p.R * p.nch : 0;
-                    parts = kv_part_rows(p, r.T, a.HQ);
+                    items = (kinds >> p.kind) & 1 ? kv_items(p, a.HK) : 0;
+                    parts = kv_part_rows(p, a.HK);
                 }
             }
             incl = items;
@@ -92,7 +92,9 @@ struct KvWalk {
             part_excl = pincl - parts;
             total = __shfl_sync(0xffffffffu, incl, 31);
             part_total = __shfl_sync(0xffffffffu, pincl, 31);
-            if (items && parts && blockIdx.x == 0) a.part_base[b] = part_before + part_excl;
+            // (every attention kernel of the call writes the same)
+            if (a.part_req && blockIdx.x == 0 && b < a.bt.B)
+                a.part_req[b] = KvJoin{r.n0, parts ? r.T : 0, r.L, 0, part_before + part_excl};
         }
         *src = __ffs(__ballot_sync(0xffffffffu, incl > u - before)) - 1;
         const int prev = __shfl_sync(0xffffffffu, incl, max(*src - 1, 0));

@@ -63,6 +63,7 @@ struct Item {
     int n0, T, pos0;     // request: first row of q and out, new tokens, position of the first
     int slot, hk;
     int row0, rows;      // first row of the item, rows of the request
+    int rows_s;          // rows whose keys are cut
     int lo, hi;          // key tiles [lo, hi)
     int hi0, lo1;        // paired: stream 0 takes [lo, hi0), stream 1 [lo1, hi)
     int k_lo, k_hi;      // positions that some row of the row tile sees: [k_lo, k_hi)
@@ -92,18 +93,24 @@ constexpr int smem_bytes() {
 // keys would not stay in L2 while all heads are in use.
 __device__ __forceinline__ bool make_item(const KvAttendArgs &a, const KvReq &r, const KvPlan &p, int local,
                                           long long base, Item *it) {
-    int i, hk, j;
+    int i, hk, j = 0, n = a.HK * (p.R - p.Rs), top = p.R - 1, tiles = p.R - p.Rs;   // whole row tiles first
+    if (local >= n) {
+        local -= n;
+        j = local % p.nch;
+        local /= p.nch;
+        top = p.Rs - 1;
+        tiles = p.Rs;
+    }
+    const bool cut = top < p.Rs;
     if (p.heads_inside) {
-        j = local % p.nch;
-        hk = local / p.nch % a.HK;
-        i = p.R - 1 - local / p.nch / a.HK;
+        hk = local % a.HK;
+        i = top - local / a.HK;
     } else {
-        j = local % p.nch;
-        i = p.R - 1 - local / p.nch % p.R;
-        hk = local / p.nch / p.R;
+        i = top - local % tiles;
+        hk = local / tiles;
     }
     const KvRange g = kv_range(p, r.L - r.T, i, a.window);
-    const int lo = g.lo + j * p.c, hi = min(g.hi, lo + p.c);
+    const int lo = g.lo + j * p.c, hi = cut ? min(g.hi, lo + p.c) : g.hi;
     if (lo >= hi) return false;
     it->end = 0;
     it->paired = p.kind == kKvPaired;
@@ -114,13 +121,14 @@ __device__ __forceinline__ bool make_item(const KvAttendArgs &a, const KvReq &r,
     it->hk = hk;
     it->row0 = i * 256;
     it->rows = p.rows;
+    it->rows_s = p.rows_s;
     it->lo = lo;
     it->hi = hi;
     it->hi0 = min(hi, g.hi0);
     it->lo1 = max(lo, g.lo1);
     it->k_lo = g.k_lo;
     it->k_hi = g.k_hi;
-    const int parts = kv_parts(p, g);
+    const int parts = kv_parts(p, g, i);
     it->part = parts > 1 ? (p.kind == kKvPaired ? j : 2 * j) : -1;
     it->base = base;
     return true;
@@ -259,7 +267,7 @@ template <int D, bool QBF16>
 __device__ void q_role(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
     using C = Cfg<D>;
     constexpr int kLanes = D / 8, kPer = 32 / kLanes;   // lanes per row, rows per step
-    constexpr int kSteps = 32 / kPer, kGroup = 4;   // steps of a group: their chains of latencies overlap
+    constexpr int kGroup = 4;   // steps of a group: their chains of latencies overlap; a step is 4 * kPer rows
     const int warp = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31, c = lane % kLanes, sub = lane / kLanes;
     const int G = a.HQ / a.HK;
     const RowLane rl = row_lane<D>(c, a.d_rope, a.pairs);
@@ -275,21 +283,36 @@ __device__ void q_role(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
     for (int n = 0; next_item(ms, n, &it); ++n) {
 #pragma unroll 1
         for (int s = 0; s <= it.paired; ++s) {
-            const int r0 = it.row0 + 128 * s + 32 * warp;
-            const int steps = min(kSteps, (it.rows - r0 + kPer - 1) / kPer);
-            int tok = (r0 + sub) / G, head = r0 + sub - tok * G;   // the lane's row; kPer further each step
+            // row of step k: 4 kPer k + first (within the 128 of the operand)
+            const int first = warp * kPer + sub, r0 = it.row0 + 128 * s;
+            const int steps = min(32 / kPer, (it.rows - r0 - warp * kPer + 4 * kPer - 1) / (4 * kPer));
+            int tok = (r0 + first) / G, head = r0 + first - tok * G;   // the lane's row, 4 kPer further each step
+            Raw8<QBF16> next[kGroup];
+            int npos[kGroup];
+            auto fetch = [&]() {
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k) {
+                    const int t = min(tok, it.T - 1);   // (rows that are not there: any)
+                    npos[k] = it.pos0 + t;
+                    next[k] = load8<QBF16>(a.q, (long long)(it.n0 + t) * a.q_stride + (it.hk * G + head) * D, rl);
+                    head += 4 * kPer;
+                    const int up = head / G;
+                    tok += up;
+                    head -= up * G;
+                }
+            };
             bool waited = n == 0;
+            if (steps > 0) fetch();
 #pragma unroll 1
             for (int k0 = 0; k0 < steps; k0 += kGroup) {
                 Raw8<QBF16> raw[kGroup];
                 int pos[kGroup];
 #pragma unroll
                 for (int k = 0; k < kGroup; ++k) {
-                    const int t = min(tok, it.T - 1);   // (rows that are not there: any)
-                    pos[k] = it.pos0 + t;
-                    raw[k] = load8<QBF16>(a.q, (long long)(it.n0 + t) * a.q_stride + (it.hk * G + head) * D, rl);
-                    for (head += kPer; head >= G; head -= G) ++tok;
+                    raw[k] = next[k];
+                    pos[k] = npos[k];
                 }
+                if (k0 + kGroup < steps) fetch();   // a group ahead
                 // (the first rows' loads are in flight while the operand is still in use)
                 if (!waited) {
                     if (!warp_all(kv_wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort))) return;
@@ -307,15 +330,15 @@ __device__ void q_role(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
                         for (int j = 0; j < 4; ++j) cs[j] = kv_cos_sin(pos[k], turn[j]);   // (turn 0: unchanged)
                         row_rope(x, a.pairs, cs);
                     }
-                    const int i = 32 * warp + (k0 + k) * kPer + sub;   // row of the operand
+                    const int i = (k0 + k) * 4 * kPer + first;   // row of the operand
                     uint8_t *dst = smem + C::kOffQ + s * C::kTileBytes + i * 128;
                     const int sw = (i & 7) << 4;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint2 o = make_uint2(pack_bf16(x[4 * h], x[4 * h + 1]), pack_bf16(x[4 * h + 2], x[4 * h + 3]));
                         uint8_t *p = dst + ((h ? b1 : b0) ^ sw);
-                        *reinterpret_cast<uint2 *>(p) = o;
-                        if (!it.paired)   // the rest of the rounding
+                        if (i < 128) *reinterpret_cast<uint2 *>(p) = o;
+                        if (!it.paired && i < 128)   // the rest of the rounding
                             *reinterpret_cast<uint2 *>(p + C::kTileBytes) =
                                 make_uint2(pack_bf16(x[4 * h] - __uint_as_float(o.x << 16),
                                                      x[4 * h + 1] - __uint_as_float(o.x & 0xFFFF0000u)),
@@ -547,8 +570,17 @@ __device__ void softmax_role(const KvAttendArgs &a, Misc *ms, int s) {
     const int G = a.HQ / a.HK;
     const float sc = a.scale * kLog2e;
     int s_count = 0, tiles = 0;   // S tiles taken; the PV of tile s_count - 1 frees P and leaves O
-    Item it;
-    for (int n = 0; next_item(ms, n, &it); ++n) {
+    for (int n = 0;; ++n) {
+        // the item stays in its slot to the end: what the key loop does not
+        // need is read there again, its registers hold scores
+        const int slot = n % kItems;
+        if (!warp_all(kv_wait(&ms->item_full[slot], (n / kItems) & 1, &ms->abort))) return;
+        const Item &it = ms->item[slot];
+        if (it.end) {
+            mbar_arrive_warp(&ms->item_empty[slot]);
+            return;
+        }
+        const bool paired = it.paired;
         const int row = it.row0 + (it.paired ? 128 * s : 0) + 32 * warp + lane;
         const bool mine = row < it.rows;
         const bool idle = it.row0 + (it.paired ? 128 * s : 0) + 32 * warp >= it.rows;   // no row of the warp is real
@@ -557,15 +589,14 @@ __device__ void softmax_role(const KvAttendArgs &a, Misc *ms, int s) {
         const int low = a.window > 0 ? pos - a.window + 1 : 0;
         float m = -INFINITY, l = 0.f;   // m: the maximum the weights are formed with (score * sc)
         bool any = false;
-        const int t0 = it.paired ? (s == 0 ? it.lo : it.lo1) : it.lo + s;
-        const int t1 = it.paired && s == 0 ? it.hi0 : it.hi;
-        for (int t = t0; t < t1; t += it.paired ? 1 : 2) {
+        const int lo = it.lo, t0 = paired ? (s == 0 ? lo : it.lo1) : lo + s, t1 = paired && s == 0 ? it.hi0 : it.hi;
+        for (int t = t0; t < t1; t += paired ? 1 : 2) {
             if (!warp_all(kv_wait(&ms->s_full[s], s_count & 1, &ms->abort))) return;
             if (s == 0 && s_count == 0 && threadIdx.x == 0) CSLA_TL_MARK_ANY(2);
             ++s_count;
             tc_fence_after();
             if (!idle) {
-                const bool bad = ms->bad[(tiles + t - it.lo) % kFlags];
+                const bool bad = ms->bad[(tiles + t - lo) % kFlags];
                 const int last = bad ? -1 : pos - t * kTile, from = low - t * kTile;   // visible columns
                 const bool cut = __any_sync(0xffffffffu, last < kTile - 1 || from > 0);
                 uint32_t v[4][32];
@@ -649,12 +680,13 @@ __device__ void softmax_role(const KvAttendArgs &a, Misc *ms, int s) {
         }
         if (idle) {
             tc_fence_before();
+            mbar_arrive_warp(&ms->item_empty[slot]);
             continue;
         }
         const bool none = m == -INFINITY;
         if (it.part >= 0) {
             // partial: O and (m, l), of part `part` (+ s for a shared row tile)
-            const long long pr = it.base + ((long long)(it.part + (it.paired ? 0 : s)) * a.HK + it.hk) * it.rows + r;
+            const long long pr = it.base + ((long long)(it.part + (it.paired ? 0 : s)) * a.HK + it.hk) * it.rows_s + r;
             if (mine) a.part_ml[pr] = make_float2(m, l);
             if (t0 < t1) {
                 float *po = a.part_o + pr * D;
@@ -703,6 +735,7 @@ __device__ void softmax_role(const KvAttendArgs &a, Misc *ms, int s) {
             }
         }
         tc_fence_before();
+        mbar_arrive_warp(&ms->item_empty[slot]);
         if (s == 0 && n == 0 && threadIdx.x == 0) CSLA_TL_MARK_ANY(5);
     }
 }
@@ -783,61 +816,97 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
 }
 
 // ---------------------------------------------------------------- join
-// One warp per (row, KV head) whose keys were cut: o = sum_p w_p O_p /
-// (sum_p w_p l_p + w_sink), w_p = 2^(m_p - M), parts in order.
-constexpr int kJoinWarps = 8;
+// Rows whose keys were cut: o = sum_p w_p O_p / (sum_p w_p l_p + w_sink),
+// w_p = 2^(m_p - M), parts in a fixed order.  A row of few parts is a warp's;
+// one of many is a block's, a range of parts per warp, the warps' sums added
+// in order (a long context of one KV head leaves hundreds of parts on a few
+// rows: 4 rows x 64 heads x 256 parts took 75 us with a warp per row).
+constexpr int kJoinWarps = 8, kJoinFew = 16;
+
+// Weighted sum of O over parts [i0, i1) of the row at pr; w of lane i & 31 holds part i's weight (0: nothing written).
+template <int D>
+__device__ __forceinline__ void join_parts(const KvAttendArgs &a, long long pr, long long step, int i0, int i1, float top,
+                                           float (&o)[D / 32]) {
+    constexpr int kDims = D / 32;
+    const int lane = threadIdx.x & 31;
+    for (int j0 = i0; j0 < i1; j0 += 32) {
+        float w = 0.f;
+        if (j0 + lane < i1) w = ex2(a.part_ml[pr + (j0 + lane) * step].x - top);   // (-inf: 0)
+        const int cnt = min(32, i1 - j0);
+#pragma unroll 8
+        for (int i = 0; i < cnt; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            const float *src = a.part_o + (pr + (j0 + i) * step) * D + kDims * lane;
+            float v[kDims];
+            if constexpr (kDims == 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(src);
+                v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+            } else {
+                const float2 x = *reinterpret_cast<const float2 *>(src);
+                v[0] = x.x; v[1] = x.y;
+            }
+            // (a part of weight zero may never have been written)
+#pragma unroll
+            for (int d = 0; d < kDims; ++d) o[d] = wi == 0.f ? o[d] : fmaf(wi, v[d], o[d]);
+        }
+    }
+}
+
 template <int D, bool OBF16>
 __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_constant__ KvAttendArgs a) {
     CSLA_TL_SCOPE(kTlKvJoin);
     constexpr int kDims = D / 32;
+    __shared__ float sum[kJoinWarps][D];
     pdl_trigger();
     pdl_wait();
     CSLA_TL_WAITED();
-    const int lane = threadIdx.x & 31, b = blockIdx.y, G = a.HQ / a.HK;
-    const KvReq rq = kv_request(a.bt, b, a.max_new, a.max_len);
-    if (!rq.ok) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.y, G = a.HQ / a.HK;
+    const KvJoin rq = a.part_req[b];
+    if (rq.T == 0) return;
     const KvPlan p = kv_plan(rq.T, rq.L, G, a.HK, a.window, D);
-    if (kv_part_rows(p, rq.T, a.HQ) == 0) return;
-    const long long base = a.part_base[b];
-    for (int u = blockIdx.x * kJoinWarps + (threadIdx.x >> 5); u < p.rows * a.HK; u += gridDim.x * kJoinWarps) {
+    const long long base = rq.base, step = (long long)a.HK * p.rows_s;
+    // (the request's most parts decide, so that a block's warps agree)
+    const bool block = (p.kind == kKvSingle ? 2 : 1) * p.nch > kJoinFew;
+    const int per = block ? 1 : kJoinWarps;
+    for (int u0 = blockIdx.x * per; u0 < p.rows_s * a.HK; u0 += gridDim.x * per) {
+        const int u = block ? u0 : u0 + warp;
+        if (u >= p.rows_s * a.HK) break;
         const int r = u / a.HK, hk = u % a.HK;
-        const KvRange g = kv_range(p, rq.L - rq.T, r / 256, a.window);
-        const int parts = kv_parts(p, g);
-        if (parts <= 1) continue;
-        const long long pr = base + (long long)hk * p.rows + r, step = (long long)a.HK * p.rows;
+        const int parts = kv_parts(p, kv_range(p, rq.L - rq.T, r / 256, a.window), r / 256);
+        if (parts <= 1) continue;   // (all warps of a block that shares the row)
+        const long long pr = base + (long long)hk * p.rows_s + r;
         const int hq = hk * G + r % G;
         const float sink = a.sink ? a.sink[hq] * kLog2e : -INFINITY;
         float top = -INFINITY;
         for (int i = lane; i < parts; i += 32) top = fmaxf(top, a.part_ml[pr + i * step].x);
         top = warp_max(top);
         const bool none = top == -INFINITY;
-        top = fmaxf(top, sink);
-        float o[kDims] = {}, den = a.sink ? ex2(sink - top) : 0.f;
-        for (int i0 = 0; i0 < parts && !none; i0 += 32) {
-            float2 ml = make_float2(-INFINITY, 0.f);
-            if (i0 + lane < parts) ml = a.part_ml[pr + (i0 + lane) * step];
-            const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-            const float wl = ml.x == -INFINITY ? 0.f : w * ml.y;
-            const int cnt = min(32, parts - i0);
-#pragma unroll 8
-            for (int i = 0; i < cnt; ++i) {
-                const float wi = __shfl_sync(0xffffffffu, w, i);
-                den += __shfl_sync(0xffffffffu, wl, i);
-                const bool empty = __shfl_sync(0xffffffffu, ml.x, i) == -INFINITY;   // its O was never written
-                const float *src = a.part_o + (pr + (i0 + i) * step) * D + kDims * lane;
-                float v[kDims];
-                if constexpr (kDims == 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(src);
-                    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-                } else {
-                    const float2 x = *reinterpret_cast<const float2 *>(src);
-                    v[0] = x.x; v[1] = x.y;
-                }
-#pragma unroll
-                for (int d = 0; d < kDims; ++d) o[d] = empty ? o[d] : fmaf(wi, v[d], o[d]);
-            }
+        top = none ? 0.f : fmaxf(top, sink);
+        float den = 0.f;
+        for (int i = lane; i < parts; i += 32) {
+            const float2 ml = a.part_ml[pr + i * step];
+            den += ml.x == -INFINITY ? 0.f : ex2(ml.x - top) * ml.y;
         }
+        den = warp_sum(den) + (a.sink ? ex2(sink - top) : 0.f);
         const float inv = none ? 0.f : 1.f / den;
+        float o[kDims] = {};
+        if (!block) {
+            join_parts<D>(a, pr, step, 0, parts, top, o);
+        } else {
+            const int n = (parts + kJoinWarps - 1) / kJoinWarps;
+            join_parts<D>(a, pr, step, min(parts, warp * n), min(parts, (warp + 1) * n), top, o);
+#pragma unroll
+            for (int d = 0; d < kDims; ++d) sum[warp][kDims * lane + d] = o[d];
+            __syncthreads();
+            if (warp == 0) {
+#pragma unroll
+                for (int w = 1; w < kJoinWarps; ++w)
+#pragma unroll
+                    for (int d = 0; d < kDims; ++d) o[d] += sum[w][kDims * lane + d];
+            }
+            __syncthreads();
+            if (warp != 0) continue;
+        }
         const long long at = ((long long)(rq.n0 + r / G) * a.HQ + hq) * D + kDims * lane;
         if constexpr (OBF16) {
             uint32_t *dst = reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(a.out) + at);
@@ -888,9 +957,8 @@ cudaError_t launch_kv_attend(const KvAttendArgs &a, bool q_bf16, bool out_bf16, 
 
 cudaError_t launch_kv_join(const KvAttendArgs &a, bool out_bf16, int num_sms, cudaStream_t stream) {
     const long long rows = (long long)(a.max_new < a.bt.N ? a.max_new : a.bt.N) * a.HQ;
-    long long x = (rows + kJoinWarps - 1) / kJoinWarps;
     const long long most = 8ll * num_sms / a.bt.B + 1;
-    if (x > most) x = most;
+    const long long x = rows < most ? rows : most;
     const dim3 grid((unsigned)x, (unsigned)a.bt.B), block(32 * kJoinWarps);
     if (a.D == 64)
         return out_bf16 ? launch_pdl(kv_join_kernel<64, true>, grid, block, 0, stream, a)

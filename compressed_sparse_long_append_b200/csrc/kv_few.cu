@@ -1,10 +1,10 @@
-// kv_few.cu -- attention of requests of few rows (up to 64 per KV head:
-// decode, a few drafted tokens) over the dense paged cache: a part of
+// kv_few.cu -- attention of requests of few rows (up to 16 per KV head:
+// decode) over the dense paged cache: a part of
 // csla_kv_attend.
 //
 //   s_j = scale <R(p) norm(q), K_j>,  o = sum_j e^{s_j} V_j / (e^{sink} + sum_j e^{s_j})
 //
-// Each K and V byte is used by at most 64 rows, so the kernel is bound by
+// Each K and V byte is used by at most 16 rows, so the kernel is bound by
 // HBM and by how much of it is asked for at a time; the products are small.  So
 // they stay in registers: mma.sync on 16-row fragments needs no tensor memory, no handing
 // over between roles and no padding to 128 rows, and its rate is several times what the bytes leave time for.
@@ -23,29 +23,27 @@
 namespace csla {
 namespace {
 
-constexpr int kGroups = 4;   // token groups: a quarter of a stage's tokens each
+constexpr int kConsumers = 4;   // warps, a quarter of a stage's tokens each
+constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kRows = 16;       // of an item
 constexpr int kItems = 4;
-constexpr int kMaxStages = 11;
+constexpr int kMaxStages = 6;
 
-template <int D, int MT>
+template <int D>
 struct Cfg {
     static constexpr int kTok = D == 128 ? 64 : 128;      // tokens per stage
     static constexpr int kKB = D / 64;                    // 128-byte blocks of a row
     static constexpr int kBlk = kTok * 128;
     static constexpr int kStage = kKB * kBlk;             // 16 KB
     static constexpr int kPer = CSLA_PAGE_TOKENS / kTok;  // stages per page
-    static constexpr int kConsumers = kGroups * MT;       // warp = 4 * (16-row tile) + token group
-    static constexpr int kThreads = 32 * (kConsumers + 1);
-    static constexpr int kCtas = MT == 4 ? 1 : 2;         // per SM
-    static constexpr int kStages = MT == 1 ? 6 : (MT == 2 ? 5 : 11);
-    static constexpr int kWT = kTok / kGroups;            // tokens of a stage per warp
-    static constexpr int kOut = MT * 16 * D * 2;          // half the dims of one warp's O
-    // work area: the Q terms [2][MT*16][D] bf16; at an item's end half of two O, and their (m, l)
+    static constexpr int kStages = 6;
+    static constexpr int kWT = kTok / kConsumers;         // tokens of a stage per warp
+    static constexpr int kOut = kRows * D * 2;           // half the dims of one warp's O
+    // work area: the Q terms [2][16][D] bf16; at an item's end half of two O, and their (m, l)
     static constexpr int kOffWork = kStages * kStage;
-    static constexpr int kMl = MT * 32 * 16;              // (m, l) of both row groups, per lane
+    static constexpr int kMl = 32 * 16;                  // (m, l) of both row groups, per lane
     static constexpr int kOffMl = kOffWork + 2 * kOut;
     static constexpr int kOffMisc = kOffMl + 2 * kMl;
-    static_assert(2 * MT * 16 * D * 2 <= 2 * kOut, "Q fits in the work area");
 };
 
 struct Item {
@@ -64,9 +62,9 @@ struct Misc {
     int abort;
 };
 
-template <int D, int MT>
+template <int D>
 constexpr int smem_bytes() {
-    return Cfg<D, MT>::kOffMisc + (int)sizeof(Misc) + 1024;
+    return Cfg<D>::kOffMisc + (int)sizeof(Misc) + 1024;
 }
 
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
@@ -105,9 +103,9 @@ __device__ __forceinline__ bool all_consumers(bool ok) {
 }
 
 // ---------------------------------------------------------------- producer
-template <int D, int MT>
+template <int D>
 __device__ void producer(const KvAttendArgs &a, const CUtensorMap &km, const CUtensorMap &vm, uint8_t *smem, Misc *ms) {
-    using C = Cfg<D, MT>;
+    using C = Cfg<D>;
     const int lane = threadIdx.x & 31;
     KvWalk w;
     int st = 0, issued = 0;
@@ -130,7 +128,7 @@ __device__ void producer(const KvAttendArgs &a, const CUtensorMap &km, const CUt
             it.hi = min(g.hi, it.lo + w.p.c);   // (with a window the last chunk may be empty)
             it.k_lo = g.k_lo;
             it.k_hi = g.k_hi;
-            it.part = kv_parts(w.p, g) > 1 ? j : -1;
+            it.part = kv_parts(w.p, g, 0) > 1 ? j : -1;
             it.base = w.part_before + w.part_excl;
         }
         const int lo = __shfl_sync(0xffffffffu, it.lo, src), hi = __shfl_sync(0xffffffffu, it.hi, src);
@@ -180,14 +178,14 @@ __device__ void producer(const KvAttendArgs &a, const CUtensorMap &km, const CUt
 
 // ---------------------------------------------------------------- consumers
 // Q rows of the item as two bf16 terms, rows of 2D bytes, 16-byte chunk ^ (row & 7).
-template <int D, int MT, bool QBF16>
+template <int D, bool QBF16>
 __device__ void stage_q(const KvAttendArgs &a, const Item &it, uint8_t *qs, const Misc *ms) {
     constexpr int kLanes = D / 8, kPer = 32 / kLanes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % kLanes, sub = lane / kLanes;
     const int G = a.HQ / a.HK;
     const RowLane rl = row_lane<D>(c, a.d_rope, a.pairs);
 #pragma unroll 1
-    for (int r0 = warp * kPer; r0 < it.rows; r0 += kGroups * MT * kPer) {
+    for (int r0 = warp * kPer; r0 < it.rows; r0 += kConsumers * kPer) {
         const int r = min(r0 + sub, it.rows - 1), t = r / G;
         const Raw8<QBF16> raw = load8<QBF16>(a.q, (long long)(it.n0 + t) * a.q_stride + (it.hk * G + r - t * G) * D, rl);
         float2 cs[4];
@@ -209,7 +207,7 @@ __device__ void stage_q(const KvAttendArgs &a, const Item &it, uint8_t *qs, cons
                 uint8_t *p = qs + (r0 + sub) * 2 * D + ((byte & ~15) ^ ((r0 + sub) & 7) << 4) + (byte & 15);
                 const uint2 o = make_uint2(pack_bf16(x[4 * h], x[4 * h + 1]), pack_bf16(x[4 * h + 2], x[4 * h + 3]));
                 *reinterpret_cast<uint2 *>(p) = o;
-                *reinterpret_cast<uint2 *>(p + MT * 16 * 2 * D) =
+                *reinterpret_cast<uint2 *>(p + kRows * 2 * D) =
                     make_uint2(pack_bf16(x[4 * h] - __uint_as_float(o.x << 16), x[4 * h + 1] - __uint_as_float(o.x & 0xFFFF0000u)),
                                pack_bf16(x[4 * h + 2] - __uint_as_float(o.y << 16),
                                          x[4 * h + 3] - __uint_as_float(o.y & 0xFFFF0000u)));
@@ -218,12 +216,12 @@ __device__ void stage_q(const KvAttendArgs &a, const Item &it, uint8_t *qs, cons
     }
 }
 
-template <int D, int MT, bool QBF16, bool OBF16>
+template <int D, bool QBF16, bool OBF16>
 __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
-    using C = Cfg<D, MT>;
+    using C = Cfg<D>;
     constexpr int kNT = C::kWT / 8;   // 8-token tiles per warp and stage
     constexpr int kDT = D / 8;        // 8-dim tiles of O
-    const int warp = (threadIdx.x >> 5) & (kGroups - 1), mt = threadIdx.x >> 7, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = a.HQ / a.HK;
     const float sc = a.scale * kLog2e;
     const uint32_t ring = smem_u32(smem), work = smem_u32(smem + C::kOffWork);
@@ -239,21 +237,20 @@ __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
         // warp passes the same barriers (which also say that the last
         // item's join is done with the work area)
         ok = ok && warp_all(kv_wait(&ms->item_full[islot], (n / kItems) & 1, &ms->abort));
-        if (!all_consumers<C::kConsumers>(ok)) return;
+        if (!all_consumers<kConsumers>(ok)) return;
         const Item it = ms->item[islot];
         mbar_arrive_warp(&ms->item_empty[islot]);
         if (it.end) return;
-        stage_q<D, MT, QBF16>(a, it, smem + C::kOffWork, ms);
-        sync_consumers<C::kConsumers>();
+        stage_q<D, QBF16>(a, it, smem + C::kOffWork, ms);
+        sync_consumers<kConsumers>();
 
-        const bool idle = 16 * mt >= it.rows;   // no row of this warp's tile is real
         float m[2], l[2], o[kDT][4];
         int pos[2], low[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             m[h] = -INFINITY;
             l[h] = 0.f;
-            pos[h] = it.pos0 + min(16 * mt + 8 * h + (lane >> 2), it.rows - 1) / G;
+            pos[h] = it.pos0 + min(8 * h + (lane >> 2), it.rows - 1) / G;
             low[h] = a.window > 0 ? pos[h] - a.window + 1 : 0;
 #pragma unroll
             for (int j = 0; j < kDT; ++j) o[j][2 * h] = o[j][2 * h + 1] = 0.f;
@@ -268,33 +265,38 @@ __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
             ++taken;
             const bool bad = ms->bad[ks];
             const int t0 = it.lo * CSLA_PAGE_TOKENS + s * C::kTok + tok0;   // position of the warp's first token
-            float acc[kNT][4];
+            // one sum per term of Q: two chains of products, half as long
+            float acc[kNT][4], rest[kNT][4];
 #pragma unroll
-            for (int j = 0; j < kNT; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+            for (int j = 0; j < kNT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[j][e] = rest[j][e] = 0.f;
             const uint32_t kb = ring + ks * C::kStage;
-            if (!idle) {
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    uint32_t b[kNT / 2][4];
+            for (int k = 0; k < D / 16; ++k) {
+                uint32_t b[kNT / 2][4];
+#pragma unroll
+                for (int j = 0; j < kNT / 2; ++j) {
+                    const int tok = tok0 + 16 * j + 8 * (mi >> 1) + mr, ch = 2 * k + (mi & 1);
+                    ldsm(b[j], kb + (ch >> 3) * C::kBlk + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
+                }
+#pragma unroll
+                for (int term = 0; term < 2; ++term) {
+                    uint32_t q[4];
+                    const int row = 8 * (mi & 1) + mr, ch = 2 * k + (mi >> 1);
+                    ldsm(q, work + term * (kRows * 2 * D) + row * 2 * D + ((ch ^ (row & 7)) << 4));
 #pragma unroll
                     for (int j = 0; j < kNT / 2; ++j) {
-                        const int tok = tok0 + 16 * j + 8 * (mi >> 1) + mr, ch = 2 * k + (mi & 1);
-                        ldsm(b[j], kb + (ch >> 3) * C::kBlk + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
-                    }
-#pragma unroll
-                    for (int term = 0; term < 2; ++term) {
-                        uint32_t q[4];
-                        const int row = 16 * mt + 8 * (mi & 1) + mr, ch = 2 * k + (mi >> 1);
-                        ldsm(q, work + term * (MT * 16 * 2 * D) + row * 2 * D + ((ch ^ (row & 7)) << 4));
-#pragma unroll
-                        for (int j = 0; j < kNT / 2; ++j) {
-                            mma16816(acc[2 * j], q, b[j][0], b[j][1]);
-                            mma16816(acc[2 * j + 1], q, b[j][2], b[j][3]);
-                        }
+                        mma16816(term ? rest[2 * j] : acc[2 * j], q, b[j][0], b[j][1]);
+                        mma16816(term ? rest[2 * j + 1] : acc[2 * j + 1], q, b[j][2], b[j][3]);
                     }
                 }
             }
             mbar_arrive_warp(&ms->empty[ks]);
+#pragma unroll
+            for (int j = 0; j < kNT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[j][e] += rest[j][e];
             // ---- mask, maximum, P
             const int vs = taken % C::kStages;
             const bool edge = bad || t0 + C::kWT > it.pos0 + 1 || t0 < it.k_lo + it.T;   // some row may not see some token
@@ -350,37 +352,35 @@ __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
             if (!ok) break;
             ++taken;
             const uint32_t vb = ring + vs * C::kStage;
-            if (!idle) {
 #pragma unroll
-                for (int k = 0; k < kNT / 2; ++k) {
-                    const uint32_t p[4] = {pack_bf16(acc[2 * k][0], acc[2 * k][1]), pack_bf16(acc[2 * k][2], acc[2 * k][3]),
-                                           pack_bf16(acc[2 * k + 1][0], acc[2 * k + 1][1]),
-                                           pack_bf16(acc[2 * k + 1][2], acc[2 * k + 1][3])};
-                    // tokens that no row sees count nothing, whatever they hold (0 * NaN is not 0)
-                    uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+            for (int k = 0; k < kNT / 2; ++k) {
+                const uint32_t p[4] = {pack_bf16(acc[2 * k][0], acc[2 * k][1]), pack_bf16(acc[2 * k][2], acc[2 * k][3]),
+                                       pack_bf16(acc[2 * k + 1][0], acc[2 * k + 1][1]),
+                                       pack_bf16(acc[2 * k + 1][2], acc[2 * k + 1][3])};
+                // tokens that no row sees count nothing, whatever they hold (0 * NaN is not 0)
+                uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+                if (edge) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int t = t0 + 16 * k + 8 * h + 2 * (lane & 3);
+                        keep[h] = bad ? 0u
+                                      : (t >= it.k_lo && t < it.k_hi ? 0xFFFFu : 0u) |
+                                            (t + 1 >= it.k_lo && t + 1 < it.k_hi ? 0xFFFF0000u : 0u);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kDT / 2; ++j) {
+                    uint32_t b[4];
+                    const int tok = tok0 + 16 * k + 8 * (mi & 1) + mr, ch = 2 * j + (mi >> 1);
+                    ldsm_t(b, vb + (ch >> 3) * C::kBlk + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
                     if (edge) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int t = t0 + 16 * k + 8 * h + 2 * (lane & 3);
-                            keep[h] = bad ? 0u
-                                          : (t >= it.k_lo && t < it.k_hi ? 0xFFFFu : 0u) |
-                                                (t + 1 >= it.k_lo && t + 1 < it.k_hi ? 0xFFFF0000u : 0u);
-                        }
+                        b[0] &= keep[0];
+                        b[1] &= keep[1];
+                        b[2] &= keep[0];
+                        b[3] &= keep[1];
                     }
-#pragma unroll
-                    for (int j = 0; j < kDT / 2; ++j) {
-                        uint32_t b[4];
-                        const int tok = tok0 + 16 * k + 8 * (mi & 1) + mr, ch = 2 * j + (mi >> 1);
-                        ldsm_t(b, vb + (ch >> 3) * C::kBlk + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
-                        if (edge) {
-                            b[0] &= keep[0];
-                            b[1] &= keep[1];
-                            b[2] &= keep[0];
-                            b[3] &= keep[1];
-                        }
-                        mma16816(o[2 * j], p, b[0], b[1]);
-                        mma16816(o[2 * j + 1], p, b[2], b[3]);
-                    }
+                    mma16816(o[2 * j], p, b[0], b[1]);
+                    mma16816(o[2 * j + 1], p, b[2], b[3]);
                 }
             }
             mbar_arrive_warp(&ms->empty[vs]);
@@ -392,14 +392,14 @@ __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
         }
-        sync_consumers<C::kConsumers>();   // Q is no longer read
+        sync_consumers<kConsumers>();   // Q is no longer read
 #pragma unroll 1
         for (int step = 2; step >= 1; --step) {
             // (step 2: groups 2, 3 write buffers 0, 1; step 1: group 1 writes buffer 1)
             const bool gives = warp >= step && warp < 2 * step, takes = warp < step;
             const int side = gives || step == 2 ? warp & 1 : 1;
-            float4 *buf = reinterpret_cast<float4 *>(smem + C::kOffWork + side * C::kOut) + mt * (kDT / 2) * 32;
-            float4 *ml = reinterpret_cast<float4 *>(smem + C::kOffMl + side * C::kMl) + mt * 32;
+            float4 *buf = reinterpret_cast<float4 *>(smem + C::kOffWork + side * C::kOut);
+            float4 *ml = reinterpret_cast<float4 *>(smem + C::kOffMl + side * C::kMl);
             float f[2] = {1.f, 1.f}, g[2] = {0.f, 0.f};
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -411,7 +411,7 @@ __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
                     }
                     if (half == 0) ml[lane] = make_float4(m[0], l[0], m[1], l[1]);
                 }
-                sync_consumers<C::kConsumers>();
+                sync_consumers<kConsumers>();
                 if (takes) {
                     if (half == 0) {
                         const float4 x = ml[lane];
@@ -435,13 +435,13 @@ __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
                         o[i][3] = o[i][3] * f[1] + y.w * g[1];
                     }
                 }
-                sync_consumers<C::kConsumers>();
+                sync_consumers<kConsumers>();
             }
         }
         if (warp == 0 && !*(volatile int *)&ms->abort) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int r = 16 * mt + 8 * h + (lane >> 2);
+                const int r = 8 * h + (lane >> 2);
                 if (r >= it.rows) continue;
                 const int d = 2 * (lane & 3);
                 if (it.part >= 0) {
@@ -472,12 +472,12 @@ __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
     }
 }
 
-template <int D, int MT, bool QBF16, bool OBF16>
-__global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtas) kv_few_kernel(const __grid_constant__ KvAttendArgs a,
+template <int D, bool QBF16, bool OBF16>
+__global__ void __launch_bounds__(kThreads, 2) kv_few_kernel(const __grid_constant__ KvAttendArgs a,
                                                              const __grid_constant__ CUtensorMap km,
                                                              const __grid_constant__ CUtensorMap vm) {
     CSLA_TL_SCOPE(kTlKvFew);
-    using C = Cfg<D, MT>;
+    using C = Cfg<D>;
     extern __shared__ uint8_t raw_smem[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
     Misc *ms = reinterpret_cast<Misc *>(smem + C::kOffMisc);
@@ -486,11 +486,11 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtas) kv_fe
     if (threadIdx.x == 64) {
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&ms->item_full[i], 1);
-            mbar_init(&ms->item_empty[i], C::kConsumers);
+            mbar_init(&ms->item_empty[i], kConsumers);
         }
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&ms->full[i], 1);
-            mbar_init(&ms->empty[i], C::kConsumers);
+            mbar_init(&ms->empty[i], kConsumers);
         }
         ms->abort = 0;
         fence_mbar_init();
@@ -500,39 +500,33 @@ __global__ void __launch_bounds__(Cfg<D, MT>::kThreads, Cfg<D, MT>::kCtas) kv_fe
     __syncthreads();
     pdl_wait();
     CSLA_TL_WAITED();
-    if (threadIdx.x >= 32 * C::kConsumers)
-        producer<D, MT>(a, km, vm, smem, ms);
+    if (threadIdx.x >= 32 * kConsumers)
+        producer<D>(a, km, vm, smem, ms);
     else
-        consumer<D, MT, QBF16, OBF16>(a, smem, ms);
+        consumer<D, QBF16, OBF16>(a, smem, ms);
 }
 
-template <int D, int MT, bool QB, bool OB>
+template <int D, bool QB, bool OB>
 cudaError_t launch(const KvAttendArgs &a, const CUtensorMap &km, const CUtensorMap &vm, unsigned grid, cudaStream_t s) {
-    auto kern = kv_few_kernel<D, MT, QB, OB>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D, MT>());
+    auto kern = kv_few_kernel<D, QB, OB>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(grid), dim3(Cfg<D, MT>::kThreads), smem_bytes<D, MT>(), s, a, km, vm);
+    return launch_pdl(kern, dim3(grid), dim3(kThreads), smem_bytes<D>(), s, a, km, vm);
 }
-template <int D, int MT>
+template <int D>
 cudaError_t launch_types(const KvAttendArgs &a, bool qb, bool ob, const CUtensorMap &km, const CUtensorMap &vm,
                          unsigned grid, cudaStream_t s) {
-    if (qb) return ob ? launch<D, MT, true, true>(a, km, vm, grid, s) : launch<D, MT, true, false>(a, km, vm, grid, s);
-    return ob ? launch<D, MT, false, true>(a, km, vm, grid, s) : launch<D, MT, false, false>(a, km, vm, grid, s);
+    if (qb) return ob ? launch<D, true, true>(a, km, vm, grid, s) : launch<D, true, false>(a, km, vm, grid, s);
+    return ob ? launch<D, false, true>(a, km, vm, grid, s) : launch<D, false, false>(a, km, vm, grid, s);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_few(const KvAttendArgs &a, bool q_bf16, bool out_bf16, int rows, const CUtensorMap &km,
+cudaError_t launch_kv_few(const KvAttendArgs &a, bool q_bf16, bool out_bf16, const CUtensorMap &km,
                           const CUtensorMap &vm, int num_sms, long long items, cudaStream_t stream) {
-    const int ctas = (rows <= 32 ? 2 : 1) * num_sms;
-    const unsigned grid = (unsigned)(items < ctas ? items : ctas);
-    if (a.D == 64)
-        return rows <= 16   ? launch_types<64, 1>(a, q_bf16, out_bf16, km, vm, grid, stream)
-               : rows <= 32 ? launch_types<64, 2>(a, q_bf16, out_bf16, km, vm, grid, stream)
-                            : launch_types<64, 4>(a, q_bf16, out_bf16, km, vm, grid, stream);
-    return rows <= 16   ? launch_types<128, 1>(a, q_bf16, out_bf16, km, vm, grid, stream)
-           : rows <= 32 ? launch_types<128, 2>(a, q_bf16, out_bf16, km, vm, grid, stream)
-                        : launch_types<128, 4>(a, q_bf16, out_bf16, km, vm, grid, stream);
+    const unsigned grid = (unsigned)(items < 2 * num_sms ? items : 2 * num_sms);
+    return a.D == 64 ? launch_types<64>(a, q_bf16, out_bf16, km, vm, grid, stream)
+                     : launch_types<128>(a, q_bf16, out_bf16, km, vm, grid, stream);
 }
 
 }  // namespace csla
