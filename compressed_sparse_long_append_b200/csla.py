@@ -154,7 +154,8 @@ def _ptr(x):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: the Stream object around it costs more than a launch
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -299,18 +300,21 @@ def csla_version():
     return int(_lib.csla_version())
 
 
-_KV_DTYPES = {CSLA_F32: "torch.float32", CSLA_BF16: "torch.bfloat16"}
+_KV_DTYPES = {}
 
 
 def _kv_tensors(fn, dtype, *tensors):
     """Tensors of a dense layer's call (addresses pass unchecked): of the given dtype code, on the current device."""
     import torch
+    if not _KV_DTYPES:
+        _KV_DTYPES.update({CSLA_F32: torch.float32, CSLA_BF16: torch.bfloat16})
+    want, dev = _KV_DTYPES.get(dtype), torch._C._cuda_getDevice()
     for t in tensors:
         if t is None or isinstance(t, int):
             continue
-        if str(t.dtype) != _KV_DTYPES.get(dtype):
+        if t.dtype is not want:
             raise ValueError("%s: a %s tensor where dtype code %s was given" % (fn, t.dtype, dtype))
-        if t.device.index != torch.cuda.current_device():
+        if t.get_device() != dev:
             raise ValueError("%s: a tensor on %s, not on the current device" % (fn, t.device))
 
 

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 namespace csla {
@@ -253,6 +254,22 @@ __host__ __device__ inline int attend_max_chunks(long long n) {
 }
 
 // ---------------------------------------------------------------- dense paged layers
+// A kernel's dynamic shared memory beyond the default, allowed once per device.
+struct KvSmemOnce {
+    std::atomic<unsigned long long> done{0};   // by device
+    template <typename... KArgs>
+    cudaError_t allow(void (*kernel)(KArgs...), int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+        if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+        return e;
+    }
+};
+
 // RoPE frequencies theta^(-2i/d_rope) of a dense layer (d_rope up to 128) as
 // turns per position, in units of 2^-64 turn: position times frequency
 // modulo one turn is then one 64-bit integer product, exact in the product and

@@ -67,19 +67,30 @@ constexpr int smem_bytes() {
     return Cfg<D>::kOffMisc + (int)sizeof(Misc) + 1024;
 }
 
+// The loads and products are plain (not volatile) statements, so that the
+// compiler can run loads ahead of products; held() ties them to the waits and
+// arrivals around them: an address that passed through it after a wait is not
+// loaded from before the wait, a sum that passed through it before an
+// arrival has its operands loaded by then.
+__device__ __forceinline__ uint32_t held(uint32_t x) {
+    asm volatile("" : "+r"(x)::"memory");
+    return x;
+}
+__device__ __forceinline__ void held(float (&c)[4]) {
+    asm volatile("" : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])::"memory");
+}
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
+    asm("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(addr));
 }
 __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
+    asm("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(addr));
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -224,7 +235,7 @@ __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = a.HQ / a.HK;
     const float sc = a.scale * kLog2e;
-    const uint32_t ring = smem_u32(smem), work = smem_u32(smem + C::kOffWork);
+    const uint32_t ring = smem_u32(smem), work0 = smem_u32(smem + C::kOffWork);
     // ldmatrix addresses: K (rows = tokens): matrix i = lane / 8 is (tokens 8 (i>>1), dims 8 (i&1));
     // V (transposed): (tokens 8 (i&1), dims 8 (i>>1)); Q: (rows 8 (i&1), dims 8 (i>>1))
     const int mi = lane >> 3, mr = lane & 7;
@@ -271,7 +282,7 @@ __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
             for (int j = 0; j < kNT; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[j][e] = rest[j][e] = 0.f;
-            const uint32_t kb = ring + ks * C::kStage;
+            const uint32_t kb = held(ring + ks * C::kStage), work = held(work0);
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 uint32_t b[kNT / 2][4];
@@ -291,6 +302,11 @@ __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
                         mma16816(term ? rest[2 * j + 1] : acc[2 * j + 1], q, b[j][2], b[j][3]);
                     }
                 }
+            }
+#pragma unroll
+            for (int j = 0; j < kNT; ++j) {
+                held(acc[j]);
+                held(rest[j]);
             }
             mbar_arrive_warp(&ms->empty[ks]);
 #pragma unroll
@@ -351,7 +367,7 @@ __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
             ok = warp_all(kv_wait(&ms->full[vs], (taken / C::kStages) & 1, &ms->abort));
             if (!ok) break;
             ++taken;
-            const uint32_t vb = ring + vs * C::kStage;
+            const uint32_t vb = held(ring + vs * C::kStage);
 #pragma unroll
             for (int k = 0; k < kNT / 2; ++k) {
                 const uint32_t p[4] = {pack_bf16(acc[2 * k][0], acc[2 * k][1]), pack_bf16(acc[2 * k][2], acc[2 * k][3]),
@@ -383,6 +399,8 @@ __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
                     mma16816(o[2 * j + 1], p, b[2], b[3]);
                 }
             }
+#pragma unroll
+            for (int j = 0; j < kDT; ++j) held(o[j]);
             mbar_arrive_warp(&ms->empty[vs]);
         }
 
@@ -509,7 +527,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv_few_kernel(const __grid_consta
 template <int D, bool QB, bool OB>
 cudaError_t launch(const KvAttendArgs &a, const CUtensorMap &km, const CUtensorMap &vm, unsigned grid, cudaStream_t s) {
     auto kern = kv_few_kernel<D, QB, OB>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<D>());
+    static KvSmemOnce once;
+    const cudaError_t e = once.allow(kern, smem_bytes<D>());
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(grid), dim3(kThreads), smem_bytes<D>(), s, a, km, vm);
 }
