@@ -750,13 +750,13 @@ static long long kv_most_tiles(const csla_kv_cfg *c, int max_new, int max_len) {
 
 // Partial rows that a batch within these bounds may need (kv_plan: a chunk
 // is at least kv_min_tiles tiles, and a request at most kv_units items, unless
-// its keys are not cut at all).
+// its keys are not cut at all or only those of its last row tiles).
 static long long kv_most_part_rows(const csla_kv_cfg *c, int B, int N, int max_new, int max_len) {
     const long long G = c->HQ / c->HK, HK = c->HK, nt = kv_most_tiles(c, max_new, max_len);
     auto least = [](long long x, long long y) { return x < y ? x : y; };
     auto parts = [&](int kind) {
-        const long long m = kv_min_tiles(kind), most = kv_units(kind) / HK > 1 ? kv_units(kind) / HK : 1;
-        return least((nt + m - 1) / m, most);
+        const long long fit = nt / kv_min_tiles(kind, c->D), n = least(fit, kv_units(kind) / HK);
+        return n > 1 ? n : 1;
     };
     if (nt <= 1) return 0;
     // (tokens of all requests of a kind) * (parts of a row)
@@ -766,7 +766,7 @@ static long long kv_most_part_rows(const csla_kv_cfg *c, int B, int N, int max_n
         tokens = least(N, B * least(max_new, 128 / G));
         rows += tokens * c->HQ * 2 * parts(kKvSingle);
     }
-    if (max_new * G > 128 && nt > kv_min_tiles(kKvPaired)) {
+    if (max_new * G > 128 && nt > kv_min_tiles(kKvPaired, c->D)) {
         // a request has chunks * 256 * R * HK rows at most, chunks <= units / (R * HK)
         const long long each = 256ll * kv_units(kKvPaired), n = least(B, N * G / 129);
         rows += least(n * each, (long long)N * c->HQ * parts(kKvPaired));
@@ -838,7 +838,7 @@ int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
         if (!encode_bf16_2d(&km, kv->k, cfg->D, cache_rows, kv_few_box(cfg->D)) ||
             !encode_bf16_2d(&vm, kv->v, cfg->D, cache_rows, kv_few_box(cfg->D)))
             return CSLA_ERR_CUDA;
-        const long long m = kv_min_tiles(kKvFew);
+        const long long m = kv_min_tiles(kKvFew, cfg->D);
         e = launch_kv_few(a, q16, o16, km, vm, num_sms_current(),
                           (long long)B * cfg->HK * ((nt + m - 1) / m), st);
     }
@@ -847,7 +847,7 @@ int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
         if (!encode_bf16_2d(&km, kv->k, cfg->D, cache_rows, CSLA_PAGE_TOKENS) ||
             !encode_bf16_2d(&vm, kv->v, cfg->D, cache_rows, CSLA_PAGE_TOKENS))
             return CSLA_ERR_CUDA;
-        const long long m = kv_min_tiles(kKvSingle);
+        const long long m = kv_min_tiles(kKvSingle, cfg->D);
         e = launch_kv_attend(a, q16, o16, km, vm, num_sms_current(),
                              ((long long)N * G / 256 + B) * cfg->HK * ((nt + m - 1) / m), st);
     }

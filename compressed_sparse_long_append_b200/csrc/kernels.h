@@ -311,7 +311,9 @@ struct KvAppendArgs {
 cudaError_t launch_kv_append(const KvAppendArgs &a, bool bf16, cudaStream_t stream);
 
 struct KvJoin {
-    int n0, T, L, pad;   // T = 0: nothing to join
+    int n0, rows_s;      // the request's first row of out; rows to join per KV head (0: none)
+    int parts;           // of each row; 0: by row tile, see T and L
+    int T, L, pad;
     long long base;      // first partial row
 };
 struct KvAttendArgs {
@@ -346,7 +348,7 @@ struct KvPlan {
 constexpr int kKvFewRows = 16;
 // items that a long request is cut into (all heads), and the least tiles of a chunk, by kind
 __host__ __device__ constexpr int kv_units(int kind) { return kind == kKvPaired ? 148 : 296; }
-__host__ __device__ constexpr int kv_min_tiles(int kind) { return kind == kKvPaired ? 8 : (kind == kKvSingle ? 8 : 2); }
+__host__ __device__ constexpr int kv_min_tiles(int kind, int D) { return kind == kKvFew ? 512 / D : (kind == kKvSingle ? 16 : 8); }
 
 // Key tiles of row tile i: [lo, hi); of its two halves: first half [lo, hi0), second [lo1, hi).
 // [k_lo, k_hi): the positions that some row sees.
@@ -388,14 +390,15 @@ __host__ __device__ inline KvPlan kv_plan(int T, int L, int G, int HK, int windo
         const int w = (window + (p.kind == kKvPaired ? 256 / G + 1 : T) + CSLA_PAGE_TOKENS - 2) / CSLA_PAGE_TOKENS + 1;
         nt = w < nt ? w : nt;
     }
+    // chunks: kv_units items in all at most, kv_min_tiles tiles at least, of even sizes
     // (32-bit divisions only: this runs ahead of every item's first load)
-    const unsigned most = kv_units(p.kind) / (unsigned)(HK * p.R);   // chunks
-    int c = most > 1 ? (int)((nt + most - 1) / most) : nt;
-    const int least = kv_min_tiles(p.kind);
-    if (c < least) c = least;
-    if (c > nt) c = nt;
+    int n = (int)(kv_units(p.kind) / (unsigned)(HK * p.R));
+    const int fit = nt / kv_min_tiles(p.kind, D);
+    n = n < fit ? n : fit;
+    const bool many = HK * p.R >= kv_units(p.kind);
+    int c = n > 1 ? (nt + n - 1) / n : nt;
     p.Rs = p.kind == kKvSingle || c < nt ? p.R : 0;
-    if (p.kind == kKvPaired && most <= 1 && window == 0 && L - T >= T) {
+    if (p.kind == kKvPaired && many && window == 0 && L - T >= T) {
         // more row tiles than SMs, all of about nt tiles
         const int sms = kv_units(kKvPaired), left = HK * p.R % sms, cuts = left ? sms / left : 1;
         if (cuts > 1 && nt >= 32 && HK * p.R < 16 * sms) {

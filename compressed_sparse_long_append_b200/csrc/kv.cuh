@@ -47,7 +47,8 @@ __device__ __forceinline__ KvReq kv_request(const KvBatch &a, int b, int max_new
 // A warp's walk over the batch: the items of the requests whose kind is in
 // `kinds`, numbered through the batch; this CTA takes item c, 2*grid-1-c,
 // 2*grid+c, ... (there and back, so that sizes that fall along the
-// numbering even out).  32 requests are held at a time, one per lane.
+// numbering even out).  32 requests are held at a time, one per lane, those
+// of the largest chunks first.
 struct KvWalk {
     int first = -32, total = 0, before = 0, round = 0, incl = 0;
     long long part_before = 0, part_total = 0, part_excl = 0;
@@ -66,7 +67,7 @@ struct KvWalk {
             part_before += part_total;
             first += 32;
             if (first >= a.bt.B) return false;
-            const int b = first + lane;
+            int b = first + lane;
             int items = 0;
             long long parts = 0;
             if (b < a.bt.B) {
@@ -77,6 +78,25 @@ struct KvWalk {
                     items = (kinds >> p.kind) & 1 ? kv_items(p, a.HK) : 0;
                     parts = kv_part_rows(p, a.HK);
                 }
+            }
+            // largest chunks first: the CTAs' loads even out on the small ones
+            if (a.bt.B > 1) {
+                unsigned key = (unsigned)(r.ok && b < a.bt.B ? p.c : 0) << 5 | (31 - lane);
+#pragma unroll 1
+                for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll 1
+                    for (int j = k >> 1; j > 0; j >>= 1) {
+                        const unsigned o = __shfl_xor_sync(0xffffffffu, key, j);
+                        const bool larger = ((lane & k) == 0) == ((lane & j) == 0);
+                        key = larger ? max(key, o) : min(key, o);
+                    }
+                const int from = 31 - (int)(key & 31);
+                auto take = [&](int &x) { x = __shfl_sync(0xffffffffu, x, from); };
+                take(b); take(items);
+                parts = __shfl_sync(0xffffffffu, parts, from);
+                take(r.n0); take(r.T); take(r.L); take(r.slot);
+                take(p.rows); take(p.R); take(p.Rs); take(p.rows_s); take(p.kind); take(p.c); take(p.nch);
+                take(p.T); take(p.G); take(p.heads_inside);
             }
             incl = items;
             long long pincl = parts;
@@ -93,8 +113,10 @@ struct KvWalk {
             total = __shfl_sync(0xffffffffu, incl, 31);
             part_total = __shfl_sync(0xffffffffu, pincl, 31);
             // (every attention kernel of the call writes the same)
-            if (a.part_req && blockIdx.x == 0 && b < a.bt.B)
-                a.part_req[b] = KvJoin{r.n0, parts ? r.T : 0, r.L, 0, part_before + part_excl};
+            if (a.part_req && blockIdx.x == 0 && b < a.bt.B) {
+                const int same = p.kind != kKvPaired && parts ? kv_parts(p, kv_range(p, r.L - r.T, 0, a.window), 0) : 0;
+                a.part_req[b] = KvJoin{r.n0, parts && same != 1 ? p.rows_s : 0, same, r.T, r.L, 0, part_before + part_excl};
+            }
         }
         *src = __ffs(__ballot_sync(0xffffffffu, incl > u - before)) - 1;
         const int prev = __shfl_sync(0xffffffffu, incl, max(*src - 1, 0));

@@ -821,33 +821,34 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
 // one of many is a block's, a range of parts per warp, the warps' sums added
 // in order (a long context of one KV head leaves hundreds of parts on a few
 // rows: 4 rows x 64 heads x 256 parts took 75 us with a warp per row).
-constexpr int kJoinWarps = 8, kJoinFew = 16;
+constexpr int kJoinWarps = 8, kJoinFew = 32;
 
-// Weighted sum of O over parts [i0, i1) of the row at pr; w of lane i & 31 holds part i's weight (0: nothing written).
+// o += sum of 2^(m_i - top) O_i over parts [i0, i1), (m, l) of part i0 + i in
+// lane i's ml (i1 - i0 <= 32).  The parts' loads are issued eight at a time, ahead of their weights.
 template <int D>
-__device__ __forceinline__ void join_parts(const KvAttendArgs &a, long long pr, long long step, int i0, int i1, float top,
-                                           float (&o)[D / 32]) {
+__device__ __forceinline__ void join_parts(const float *part_o, long long pr, long long step, int n, float w, float (&o)[D / 32]) {
     constexpr int kDims = D / 32;
     const int lane = threadIdx.x & 31;
-    for (int j0 = i0; j0 < i1; j0 += 32) {
-        float w = 0.f;
-        if (j0 + lane < i1) w = ex2(a.part_ml[pr + (j0 + lane) * step].x - top);   // (-inf: 0)
-        const int cnt = min(32, i1 - j0);
-#pragma unroll 8
-        for (int i = 0; i < cnt; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, w, i);
-            const float *src = a.part_o + (pr + (j0 + i) * step) * D + kDims * lane;
-            float v[kDims];
-            if constexpr (kDims == 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(src);
-                v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-            } else {
-                const float2 x = *reinterpret_cast<const float2 *>(src);
-                v[0] = x.x; v[1] = x.y;
-            }
-            // (a part of weight zero may never have been written)
+    const float *src = part_o + pr * D + kDims * lane;
+    for (int j = 0; j < n; j += 8) {
+        float v[8][kDims];
 #pragma unroll
-            for (int d = 0; d < kDims; ++d) o[d] = wi == 0.f ? o[d] : fmaf(wi, v[d], o[d]);
+        for (int i = 0; i < 8; ++i) {
+            const float *p = src + min(j + i, n - 1) * step * D;
+            if constexpr (kDims == 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(p);
+                v[i][0] = x.x; v[i][1] = x.y; v[i][2] = x.z; v[i][3] = x.w;
+            } else {
+                const float2 x = *reinterpret_cast<const float2 *>(p);
+                v[i][0] = x.x; v[i][1] = x.y;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, (j + i) & 31);
+            // (a part of weight zero may never have been written; past n there is none)
+#pragma unroll
+            for (int d = 0; d < kDims; ++d) o[d] = j + i < n && wi != 0.f ? fmaf(wi, v[i][d], o[d]) : o[d];
         }
     }
 }
@@ -858,43 +859,55 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_c
     constexpr int kDims = D / 32;
     __shared__ float sum[kJoinWarps][D];
     pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.HQ / a.HK;
     pdl_wait();
     CSLA_TL_WAITED();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = blockIdx.y, G = a.HQ / a.HK;
-    const KvJoin rq = a.part_req[b];
-    if (rq.T == 0) return;
-    const KvPlan p = kv_plan(rq.T, rq.L, G, a.HK, a.window, D);
-    const long long base = rq.base, step = (long long)a.HK * p.rows_s;
-    // (the request's most parts decide, so that a block's warps agree)
-    const bool block = (p.kind == kKvSingle ? 2 : 1) * p.nch > kJoinFew;
-    const int per = block ? 1 : kJoinWarps;
-    for (int u0 = blockIdx.x * per; u0 < p.rows_s * a.HK; u0 += gridDim.x * per) {
-        const int u = block ? u0 : u0 + warp;
-        if (u >= p.rows_s * a.HK) break;
-        const int r = u / a.HK, hk = u % a.HK;
-        const int parts = kv_parts(p, kv_range(p, rq.L - rq.T, r / 256, a.window), r / 256);
-        if (parts <= 1) continue;   // (all warps of a block that shares the row)
-        const long long pr = base + (long long)hk * p.rows_s + r;
-        const int hq = hk * G + r % G;
+    const KvJoin rq = a.part_req[blockIdx.y];
+    if (rq.rows_s == 0) return;
+    KvPlan p;
+    if (rq.parts == 0) p = kv_plan(rq.T, rq.L, G, a.HK, a.window, D);   // parts by row tile
+    const long long step = (long long)a.HK * rq.rows_s;
+    const bool block = rq.parts > kJoinFew;
+    const int per = block ? 1 : kJoinWarps, units = rq.rows_s * a.HK;
+    for (int u0 = blockIdx.x * per; u0 < units; u0 += gridDim.x * per) {
+        const int u = block ? u0 : u0 + warp;   // row of the partials, head by head
+        if (u >= units) break;
+        const int hk = u / rq.rows_s, r = u - hk * rq.rows_s, t = r / G, hq = hk * G + r - t * G;
+        const int parts = rq.parts ? rq.parts : kv_parts(p, kv_range(p, rq.L - rq.T, r / 256, a.window), r / 256);
+        if (parts <= 1) continue;
+        const long long pr = rq.base + u;
         const float sink = a.sink ? a.sink[hq] * kLog2e : -INFINITY;
-        float top = -INFINITY;
-        for (int i = lane; i < parts; i += 32) top = fmaxf(top, a.part_ml[pr + i * step].x);
-        top = warp_max(top);
-        const bool none = top == -INFINITY;
-        top = none ? 0.f : fmaxf(top, sink);
-        float den = 0.f;
-        for (int i = lane; i < parts; i += 32) {
-            const float2 ml = a.part_ml[pr + i * step];
-            den += ml.x == -INFINITY ? 0.f : ex2(ml.x - top) * ml.y;
-        }
-        den = warp_sum(den) + (a.sink ? ex2(sink - top) : 0.f);
-        const float inv = none ? 0.f : 1.f / den;
         float o[kDims] = {};
-        if (!block) {
-            join_parts<D>(a, pr, step, 0, parts, top, o);
+        float inv;
+        if (parts <= 32 && !block) {
+            const float2 ml = lane < parts ? a.part_ml[pr + lane * step] : make_float2(-INFINITY, 0.f);
+            const float mx = warp_max(ml.x), top = mx == -INFINITY ? 0.f : fmaxf(mx, sink);
+            const float w = ex2(ml.x - top);   // (-inf: 0)
+            const float den = warp_sum(w * ml.y) + (a.sink ? ex2(sink - top) : 0.f);
+            inv = mx == -INFINITY ? 0.f : 1.f / den;
+            join_parts<D>(a.part_o, pr, step, parts, w, o);
         } else {
-            const int n = (parts + kJoinWarps - 1) / kJoinWarps;
-            join_parts<D>(a, pr, step, min(parts, warp * n), min(parts, (warp + 1) * n), top, o);
+            // the largest maximum and the sum over all parts (every warp the
+            // same), then O over all parts, or over this warp's share
+            float mx = -INFINITY;
+            for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, a.part_ml[pr + i * step].x);
+            mx = warp_max(mx);
+            const float top = mx == -INFINITY ? 0.f : fmaxf(mx, sink);
+            float den = 0.f;
+            for (int i = lane; i < parts; i += 32) {
+                const float2 ml = a.part_ml[pr + i * step];
+                den += ex2(ml.x - top) * ml.y;
+            }
+            den = warp_sum(den) + (a.sink ? ex2(sink - top) : 0.f);
+            inv = mx == -INFINITY ? 0.f : 1.f / den;
+            const int share = block ? (parts + kJoinWarps - 1) / kJoinWarps : parts;
+            const int i0 = block ? min(parts, warp * share) : 0, i1 = min(parts, i0 + share);
+            for (int i = i0; i < i1; i += 32) {
+                const float w = i + lane < i1 ? ex2(a.part_ml[pr + (i + lane) * step].x - top) : 0.f;
+                join_parts<D>(a.part_o, pr + i * step, step, min(32, i1 - i), w, o);
+            }
+        }
+        if (block) {
 #pragma unroll
             for (int d = 0; d < kDims; ++d) sum[warp][kDims * lane + d] = o[d];
             __syncthreads();
@@ -907,7 +920,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_c
             __syncthreads();
             if (warp != 0) continue;
         }
-        const long long at = ((long long)(rq.n0 + r / G) * a.HQ + hq) * D + kDims * lane;
+        const long long at = ((long long)(rq.n0 + t) * a.HQ + hq) * D + kDims * lane;
         if constexpr (OBF16) {
             uint32_t *dst = reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(a.out) + at);
 #pragma unroll
