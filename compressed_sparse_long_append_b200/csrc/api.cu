@@ -751,7 +751,8 @@ static long long kv_most_tiles(const csla_kv_cfg *c, int max_new, int max_len) {
 // Partial rows that a batch within these bounds may need (kv_plan: a chunk
 // is at least kv_min_tiles tiles, and a request at most kv_units items, unless
 // its keys are not cut at all or only those of its last row tiles).
-static long long kv_most_part_rows(const csla_kv_cfg *c, int B, int N, int max_new, int max_len) {
+// `same_new`: every request has so many new tokens (0: any number up to max_new).
+static long long kv_most_part_rows(const csla_kv_cfg *c, int B, int N, int max_new, int max_len, int same_new) {
     const long long G = c->HQ / c->HK, HK = c->HK, nt = kv_most_tiles(c, max_new, max_len);
     auto least = [](long long x, long long y) { return x < y ? x : y; };
     auto parts = [&](int kind) {
@@ -759,6 +760,9 @@ static long long kv_most_part_rows(const csla_kv_cfg *c, int B, int N, int max_n
         return n > 1 ? n : 1;
     };
     if (nt <= 1) return 0;
+    if (same_new && same_new * G > 128 && (same_new * G + 255) / 256 * HK >= kv_units(kKvPaired) &&
+        (nt < 32 || (long long)same_new * 2 > max_len))
+        return 0;   // row tiles for all SMs, none left over to be cut
     // (tokens of all requests of a kind) * (parts of a row)
     long long tokens = least(N, B * least(max_new, kKvFewRows / G));
     long long rows = parts(kKvFew) > 1 ? tokens * c->HQ * parts(kKvFew) : 0;
@@ -791,7 +795,7 @@ static KvWorkspace kv_workspace(const csla_kv_cfg *c, int B, long long rows) {
 
 size_t csla_kv_workspace_size(const csla_kv_cfg *cfg, int32_t B, int32_t N, int32_t max_new, int32_t max_len) {
     if (check_kv_cfg(cfg) != CSLA_OK || B < 1 || N < 1 || max_new < 1 || max_len < 1) return 0;
-    return kv_workspace(cfg, B, kv_most_part_rows(cfg, B, N, max_new, max_len)).total;
+    return kv_workspace(cfg, B, kv_most_part_rows(cfg, B, N, max_new, max_len, 0)).total;
 }
 
 int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_t *slots, int32_t B,
@@ -816,7 +820,7 @@ int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
     a.freq = kv_freq(cfg->rope_theta, cfg->d_rope);
     a.q = q; a.q_stride = q_stride; a.sink = sink; a.gamma_q = gamma_q;
     a.out = out;
-    const long long rows = kv_most_part_rows(cfg, B, N, max_new, max_len);
+    const long long rows = kv_most_part_rows(cfg, B, N, max_new, max_len, q_start ? 0 : a.bt.T);
     const KvWorkspace w = kv_workspace(cfg, B, rows);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     if (rows) {

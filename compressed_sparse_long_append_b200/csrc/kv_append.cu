@@ -7,10 +7,13 @@
 // requests by counting the request starts at or below each token, resolves
 // each token's page once, and evaluates the rotation's cosines and sines once
 // per token and pair in shared memory; then D/8 lanes move one (token, head)
-// row, 16 or 32 bytes per lane, several rows of a thread in flight together.
-// The bytes bound it (each row read once and written once); short calls are
-// bound by the chain offsets -> slot -> length -> page, which runs while the
-// first rows' loads are in flight.
+// row, 16 or 32 bytes per lane: the K rows of its tokens, then the V rows (a
+// copy), four rows of a thread at a time and the next four in flight.
+// The bytes bound a long call (each row read once and written once) and leave
+// about 170 instructions per warp for two rows, so a thread's (token, head) is
+// carried from row to row, not divided out.  Short calls are bound by the
+// chain offsets -> slot -> length -> page, which runs while the first rows'
+// loads are in flight.
 #include "kv.cuh"
 
 namespace csla {
@@ -18,10 +21,26 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTok = 16;   // tokens per block
-constexpr int kFly = 4;       // rows of a thread in flight
+constexpr int kFly = 2;       // rows of a thread at a time (and as many in flight)
+constexpr int kBlocks = 4;    // blocks per SM
+constexpr int kPass = 8;      // K rows of a thread in a long call, at most
+
+// Where a thread is among the rows of a block: rows go head by head through
+// the tokens, kRows apart for a thread.
+struct RowPos {
+    int t, h;
+};
+__device__ __forceinline__ void advance(RowPos &p, int dt, int dh, int HK) {
+    p.t += dt;
+    p.h += dh;
+    if (p.h >= HK) {
+        p.h -= HK;
+        ++p.t;
+    }
+}
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ KvAppendArgs a, int tok) {
+__global__ void __launch_bounds__(kThreads, kBlocks) kv_append_kernel(const __grid_constant__ KvAppendArgs a, int tok) {
     CSLA_TL_SCOPE(kTlKvAppend);
     constexpr int kLanes = D / 8, kRows = kThreads / kLanes;   // rows per pass
     __shared__ int s_cnt[kMaxTok];
@@ -32,28 +51,26 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     pdl_trigger();
     const int tid = threadIdx.x, c = tid % kLanes;
     const int n0 = blockIdx.x * tok, nt = min(tok, a.bt.N - n0);
-    const int rows = nt * 2 * a.HK;   // (token, K or V, head)
     const int half = a.d_rope / 2;
     const RowLane rl = row_lane<D>(c, a.d_rope, a.pairs);
     if (tid < kMaxTok) s_cnt[tid] = 0;
     if (tid < half) s_turn[tid] = a.freq.turn[tid];
+    const int dt = kRows / a.HK, dh = kRows % a.HK;
+    const RowPos start{tid / kLanes / a.HK, tid / kLanes % a.HK};
     pdl_wait();
     CSLA_TL_WAITED();
 
-    Raw8<BF16> raw[kFly];
-    auto fetch = [&](int r0) {
+    Raw8<BF16> raw[kFly], ahead[kFly];
+    // the next kFly rows of a thread from p on
+    auto fetch = [&](const void *src, long long stride, RowPos &p, Raw8<BF16> (&x)[kFly]) {
 #pragma unroll
         for (int j = 0; j < kFly; ++j) {
-            const int r = r0 + j * kRows + tid / kLanes;
-            if (r < rows) {
-                const int t = r / (2 * a.HK), w = r % (2 * a.HK);
-                const long long n = n0 + t;
-                raw[j] = w < a.HK ? load8<BF16>(a.k_new, n * a.k_stride + (long long)w * D, rl)
-                                  : load8<BF16>(a.v_new, n * a.v_stride + (long long)(w - a.HK) * D, rl);
-            }
+            if (p.t < nt) x[j] = load8<BF16>(src, (long long)(n0 + p.t) * stride + p.h * D, rl);
+            advance(p, dt, dh, a.HK);
         }
     };
-    fetch(0);
+    RowPos load = start;
+    fetch(a.k_new, a.k_stride, load, raw);
 
     __syncthreads();
     // the request of token n is the number of starts q_start[1..B] at or below n
@@ -90,64 +107,75 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
         s_dst[tid] = dst;
         s_pos[tid] = pos;
     }
-    __syncthreads();
-    for (int i = tid; i < nt * half; i += kThreads) {
-        const int t = i / half, p = i % half;
-        s_cs[t][p] = kv_cos_sin(s_pos[t], s_turn[p]);
-    }
     float g[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) g[i] = a.gamma_k ? a.gamma_k[i < 4 ? rl.d0 + i : rl.d1 + i - 4] : 1.f;
     __syncthreads();
+    for (int i = tid; i < nt * half; i += kThreads) {
+        const int t = i / half, p = i - t * half;
+        s_cs[t][p] = kv_cos_sin(s_pos[t], s_turn[p]);
+    }
+    __syncthreads();
 
+    auto store = [&](uint16_t *pool, const RowPos &p, const float (&y)[8]) {
+        const long long dst = p.t < nt ? s_dst[p.t] : -1;
+        if (dst < 0) return;
+        uint16_t *out = pool + dst + p.h * (CSLA_PAGE_TOKENS * D);
+        *reinterpret_cast<uint2 *>(out + rl.d0) = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+        *reinterpret_cast<uint2 *>(out + rl.d1) = make_uint2(pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+    };
+    const int rows = nt * a.HK;
+    // K rows; every lane of a warp takes the norm's shuffles
+    RowPos at = start;
     for (int r0 = 0; r0 < rows; r0 += kFly * kRows) {
-        if (r0) fetch(r0);
+        if (r0 + kFly * kRows < rows) {
+            fetch(a.k_new, a.k_stride, load, ahead);
+        } else {
+            load = start;
+            fetch(a.v_new, a.v_stride, load, ahead);
+        }
 #pragma unroll
         for (int j = 0; j < kFly; ++j) {
-            const int r = r0 + j * kRows + tid / kLanes;
-            if (r0 + j * kRows >= rows) break;   // uniform in the block
-            const int rr = min(r, rows - 1);
-            const int t = rr / (2 * a.HK), w = rr % (2 * a.HK);
             float x[8];
             widen8<BF16>(raw[j], x);
-            // every lane of a warp takes the shuffles; V rows keep their values
-            float y[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = x[i];
-            if (a.gamma_k) row_norm<D>(y, g, a.eps);
+            if (a.gamma_k) row_norm<D>(x, g, a.eps);
             if (rl.pair >= 0) {
                 float2 cs[4];
+                const int t = min(at.t, nt - 1);
 #pragma unroll
                 for (int p = 0; p < 4; ++p) cs[p] = s_cs[t][rl.pair + p];
-                row_rope(y, a.pairs, cs);
+                row_rope(x, a.pairs, cs);
             }
-            const bool is_k = w < a.HK;
-            uint2 o[2];
+            store(a.k, at, x);
+            advance(at, dt, dh, a.HK);
+            raw[j] = ahead[j];
+        }
+    }
+    // V rows
+    at = start;
+    for (int r0 = 0; r0 < rows; r0 += kFly * kRows) {
+        if (r0 + kFly * kRows < rows) fetch(a.v_new, a.v_stride, load, ahead);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                o[i] = is_k ? make_uint2(pack_bf16(y[4 * i], y[4 * i + 1]), pack_bf16(y[4 * i + 2], y[4 * i + 3]))
-                            : make_uint2(pack_bf16(x[4 * i], x[4 * i + 1]), pack_bf16(x[4 * i + 2], x[4 * i + 3]));
-            const long long dst = s_dst[t];
-            if (r < rows && dst >= 0) {
-                const int h = is_k ? w : w - a.HK;
-                uint16_t *out = (is_k ? a.k : a.v) + dst + (long long)h * CSLA_PAGE_TOKENS * D;
-                *reinterpret_cast<uint2 *>(out + rl.d0) = o[0];
-                *reinterpret_cast<uint2 *>(out + rl.d1) = o[1];
-            }
+        for (int j = 0; j < kFly; ++j) {
+            float x[8];
+            widen8<BF16>(raw[j], x);
+            store(a.v, at, x);
+            advance(at, dt, dh, a.HK);
+            raw[j] = ahead[j];
         }
     }
 }
 
 template <int D>
 cudaError_t launch(const KvAppendArgs &a, bool bf16, cudaStream_t s) {
-    // One pass of a block is 2048 / D rows.  Short calls: one token per block, so
-    // that all SMs share the latency.  Long ones: enough tokens for kFly rows
-    // per thread.
-    int tok = 1;
-    if (a.bt.N > 4 * 148) {
-        tok = kFly * (kThreads * 8 / D) / (2 * a.HK);
-        tok = tok < 1 ? 1 : (tok > kMaxTok ? kMaxTok : tok);
-    }
+    // As few tokens per block as one round of blocks over the SMs allows: a
+    // block's latencies (requests, pages) are what a short call costs, and what a long
+    // one pays per round (8192 tokens of 8 heads x 128: 16.2 us in one round, 21.5 in
+    // four); up to kPass K rows per thread.
+    const int slots = kBlocks * 148, most = kPass * (kThreads * 8 / D) / a.HK;
+    int tok = (a.bt.N + slots - 1) / slots;
+    tok = tok > most ? most : tok;
+    tok = tok < 1 ? 1 : (tok > kMaxTok ? kMaxTok : tok);
     const dim3 grid((a.bt.N + tok - 1) / tok);
     return bf16 ? launch_pdl(kv_append_kernel<D, true>, grid, dim3(kThreads), 0, s, a, tok)
                 : launch_pdl(kv_append_kernel<D, false>, grid, dim3(kThreads), 0, s, a, tok);
