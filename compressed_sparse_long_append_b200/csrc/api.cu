@@ -781,21 +781,24 @@ static long long kv_most_part_rows(const csla_kv_cfg *c, int B, int N, int max_n
     return rows;
 }
 
-struct KvWorkspace {
-    size_t ml, o, total;
-};
-static KvWorkspace kv_workspace(const csla_kv_cfg *c, int B, long long rows) {
-    KvWorkspace w{0, 0, 0};
-    if (rows == 0) return w;
-    w.ml = up16((size_t)B * sizeof(KvJoin));
-    w.o = w.ml + up16((size_t)rows * 8);
-    w.total = w.o + (size_t)rows * c->D * 4;
-    return w;
+// Workspace of csla_kv_attend: what the join needs per request, (m, l) of the
+// partial rows, and their O, which starts at a 32-byte boundary whatever
+// the (16-byte aligned) workspace's own: its rows are stored 32 bytes at a time.
+static size_t kv_workspace_bytes(const csla_kv_cfg *c, int B, long long rows) {
+    if (rows == 0) return 0;
+    return up16((size_t)B * sizeof(KvJoin)) + up16((size_t)rows * 8) + 16 + (size_t)rows * c->D * 4;
+}
+static void kv_workspace_parts(uint8_t *ws, int B, long long rows, KvAttendArgs *a) {
+    a->part_req = reinterpret_cast<KvJoin *>(ws);
+    ws += up16((size_t)B * sizeof(KvJoin));
+    a->part_ml = reinterpret_cast<float2 *>(ws);
+    ws += up16((size_t)rows * 8);
+    a->part_o = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(ws) + 31) & ~uintptr_t(31));
 }
 
 size_t csla_kv_workspace_size(const csla_kv_cfg *cfg, int32_t B, int32_t N, int32_t max_new, int32_t max_len) {
     if (check_kv_cfg(cfg) != CSLA_OK || B < 1 || N < 1 || max_new < 1 || max_len < 1) return 0;
-    return kv_workspace(cfg, B, kv_most_part_rows(cfg, B, N, max_new, max_len, 0)).total;
+    return kv_workspace_bytes(cfg, B, kv_most_part_rows(cfg, B, N, max_new, max_len, 0));
 }
 
 int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_t *slots, int32_t B,
@@ -821,13 +824,7 @@ int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
     a.q = q; a.q_stride = q_stride; a.sink = sink; a.gamma_q = gamma_q;
     a.out = out;
     const long long rows = kv_most_part_rows(cfg, B, N, max_new, max_len, q_start ? 0 : a.bt.T);
-    const KvWorkspace w = kv_workspace(cfg, B, rows);
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
-    if (rows) {
-        a.part_req = reinterpret_cast<KvJoin *>(ws);
-        a.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
-        a.part_o = reinterpret_cast<float *>(ws + w.o);
-    }
+    if (rows) kv_workspace_parts(static_cast<uint8_t *>(workspace), B, rows, &a);
     // which kinds of requests there may be (KvPlan); a box is 64 dims of a
     // page's rows
     const int G = cfg->HQ / cfg->HK, least_rows = q_start ? G : a.bt.T * G;
@@ -852,6 +849,7 @@ int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
             !encode_bf16_2d(&vm, kv->v, cfg->D, cache_rows, CSLA_PAGE_TOKENS))
             return CSLA_ERR_CUDA;
         const long long m = kv_min_tiles(kKvSingle, cfg->D);
+        a.beside = least_rows <= kKvFewRows;
         e = launch_kv_attend(a, q16, o16, km, vm, num_sms_current(),
                              ((long long)N * G / 256 + B) * cfg->HK * ((nt + m - 1) / m), st);
     }

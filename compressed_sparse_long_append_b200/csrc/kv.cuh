@@ -212,16 +212,27 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return r;
 }
 
-// RMSNorm over the row (all lanes of the row take part; fixed-order sum).
-template <int D>
-__device__ __forceinline__ void row_norm(float (&x)[8], const float (&g)[8], float eps) {
-    float s = (x[0] * x[0] + x[1] * x[1]) + (x[2] * x[2] + x[3] * x[3]);
-    s += (x[4] * x[4] + x[5] * x[5]) + (x[6] * x[6] + x[7] * x[7]);
+// RMSNorm over each of N rows (all lanes of a row take part; fixed-order sum).
+// The rows' chains of shuffles run beside one another, so callers take several
+// rows through a step, not one row through all steps.
+template <int D, int N>
+__device__ __forceinline__ void rows_norm(float (&x)[N][8], const float (&g)[8], float eps) {
+    float s[N];
 #pragma unroll
-    for (int o = D / 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float f = rsqrtf(s * (1.0f / D) + eps);
+    for (int k = 0; k < N; ++k) {
+        s[k] = (x[k][0] * x[k][0] + x[k][1] * x[k][1]) + (x[k][2] * x[k][2] + x[k][3] * x[k][3]);
+        s[k] += (x[k][4] * x[k][4] + x[k][5] * x[k][5]) + (x[k][6] * x[k][6] + x[k][7] * x[k][7]);
+    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * f * g[i];
+    for (int o = D / 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < N; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const float f = rsqrtf(s[k] * (1.0f / D) + eps);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[k][i] = x[k][i] * f * g[i];
+    }
 }
 
 // cos and sin of position times frequency (turns, see KvFreq): the integer

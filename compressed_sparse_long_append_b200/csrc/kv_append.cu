@@ -134,19 +134,20 @@ __global__ void __launch_bounds__(kThreads, kBlocks) kv_append_kernel(const __gr
             load = start;
             fetch(a.v_new, a.v_stride, load, ahead);
         }
+        float x[kFly][8];
+#pragma unroll
+        for (int j = 0; j < kFly; ++j) widen8<BF16>(raw[j], x[j]);
+        if (a.gamma_k) rows_norm<D>(x, g, a.eps);
 #pragma unroll
         for (int j = 0; j < kFly; ++j) {
-            float x[8];
-            widen8<BF16>(raw[j], x);
-            if (a.gamma_k) row_norm<D>(x, g, a.eps);
             if (rl.pair >= 0) {
                 float2 cs[4];
                 const int t = min(at.t, nt - 1);
 #pragma unroll
                 for (int p = 0; p < 4; ++p) cs[p] = s_cs[t][rl.pair + p];
-                row_rope(x, a.pairs, cs);
+                row_rope(x[j], a.pairs, cs);
             }
-            store(a.k, at, x);
+            store(a.k, at, x[j]);
             advance(at, dt, dh, a.HK);
             raw[j] = ahead[j];
         }

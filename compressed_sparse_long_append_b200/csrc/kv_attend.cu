@@ -267,7 +267,7 @@ template <int D, bool QBF16>
 __device__ void q_role(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
     using C = Cfg<D>;
     constexpr int kLanes = D / 8, kPer = 32 / kLanes;   // lanes per row, rows per step
-    constexpr int kGroup = 4;   // steps of a group: their chains of latencies overlap; a step is 4 * kPer rows
+    constexpr int kGroup = 4;   // rows of a lane at a time: their chains of latencies overlap
     const int warp = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31, c = lane % kLanes, sub = lane / kLanes;
     const int G = a.HQ / a.HK;
     const RowLane rl = row_lane<D>(c, a.d_rope, a.pairs);
@@ -283,28 +283,29 @@ __device__ void q_role(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
     for (int n = 0; next_item(ms, n, &it); ++n) {
 #pragma unroll 1
         for (int s = 0; s <= it.paired; ++s) {
-            // row of step k: 4 kPer k + first (within the 128 of the operand)
-            const int first = warp * kPer + sub, r0 = it.row0 + 128 * s;
-            const int steps = min(32 / kPer, (it.rows - r0 - warp * kPer + 4 * kPer - 1) / (4 * kPer));
-            int tok = (r0 + first) / G, head = r0 + first - tok * G;   // the lane's row, 4 kPer further each step
+            // a lane takes four neighbouring rows of a group (mostly heads of one
+            // token: one rotation for all), the warp 4 kPer rows, the four warps 16 kPer
+            const int r0 = it.row0 + 128 * s, first = 4 * (warp * kPer + sub);
+            const int groups = min(32 / (4 * kPer), (it.rows - r0 - 4 * warp * kPer + 16 * kPer - 1) / (16 * kPer));
             Raw8<QBF16> next[kGroup];
             int npos[kGroup];
-            auto fetch = [&]() {
+            auto fetch = [&](int gr) {
+                int tok = (r0 + first + 16 * kPer * gr) / G, head = r0 + first + 16 * kPer * gr - tok * G;
 #pragma unroll
                 for (int k = 0; k < kGroup; ++k) {
                     const int t = min(tok, it.T - 1);   // (rows that are not there: any)
                     npos[k] = it.pos0 + t;
                     next[k] = load8<QBF16>(a.q, (long long)(it.n0 + t) * a.q_stride + (it.hk * G + head) * D, rl);
-                    head += 4 * kPer;
-                    const int up = head / G;
-                    tok += up;
-                    head -= up * G;
+                    if (++head == G) {
+                        head = 0;
+                        ++tok;
+                    }
                 }
             };
             bool waited = n == 0;
-            if (steps > 0) fetch();
+            if (groups > 0) fetch(0);
 #pragma unroll 1
-            for (int k0 = 0; k0 < steps; k0 += kGroup) {
+            for (int gr = 0; gr < groups; ++gr) {
                 Raw8<QBF16> raw[kGroup];
                 int pos[kGroup];
 #pragma unroll
@@ -312,38 +313,60 @@ __device__ void q_role(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
                     raw[k] = next[k];
                     pos[k] = npos[k];
                 }
-                if (k0 + kGroup < steps) fetch();   // a group ahead
+                if (gr + 1 < groups) fetch(gr + 1);   // a group ahead
                 // (the first rows' loads are in flight while the operand is still in use)
                 if (!waited) {
                     if (!warp_all(kv_wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort))) return;
                     if (!it.paired && !warp_all(kv_wait(&ms->q_empty[1], (n - 1) & 1, &ms->abort))) return;
                     waited = true;
                 }
+                float x[kGroup][8];
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k) widen8<QBF16>(raw[k], x[k]);
+                if (a.gamma_q) rows_norm<D>(x, g, a.eps);
+                if (a.d_rope) {
+                    float2 cs[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) cs[j] = kv_cos_sin(pos[0], turn[j]);   // (turn 0: unchanged)
+                    const bool one = __all_sync(0xffffffffu, pos[0] == pos[kGroup - 1]);
+                    row_rope(x[0], a.pairs, cs);
+                    if (one) {
+#pragma unroll
+                        for (int k = 1; k < kGroup; ++k) row_rope(x[k], a.pairs, cs);
+                    } else {
+#pragma unroll
+                        for (int k = 1; k < kGroup; ++k) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) cs[j] = kv_cos_sin(pos[k], turn[j]);
+                            row_rope(x[k], a.pairs, cs);
+                        }
+                    }
+                }
+                const int i0 = first + 16 * kPer * gr;   // first row of the operand, a multiple of 4
+                uint8_t *dst = smem + C::kOffQ + s * C::kTileBytes + i0 * 128;
 #pragma unroll
                 for (int k = 0; k < kGroup; ++k) {
-                    float x[8];
-                    widen8<QBF16>(raw[k], x);
-                    if (a.gamma_q) row_norm<D>(x, g, a.eps);
-                    if (a.d_rope) {
-                        float2 cs[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) cs[j] = kv_cos_sin(pos[k], turn[j]);   // (turn 0: unchanged)
-                        row_rope(x, a.pairs, cs);
-                    }
-                    const int i = (k0 + k) * 4 * kPer + first;   // row of the operand
-                    uint8_t *dst = smem + C::kOffQ + s * C::kTileBytes + i * 128;
-                    const int sw = (i & 7) << 4;
+                    const int sw = ((i0 & 4) + k) << 4;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint2 o = make_uint2(pack_bf16(x[4 * h], x[4 * h + 1]), pack_bf16(x[4 * h + 2], x[4 * h + 3]));
-                        uint8_t *p = dst + ((h ? b1 : b0) ^ sw);
-                        if (i < 128) *reinterpret_cast<uint2 *>(p) = o;
-                        if (!it.paired && i < 128)   // the rest of the rounding
-                            *reinterpret_cast<uint2 *>(p + C::kTileBytes) =
-                                make_uint2(pack_bf16(x[4 * h] - __uint_as_float(o.x << 16),
-                                                     x[4 * h + 1] - __uint_as_float(o.x & 0xFFFF0000u)),
-                                           pack_bf16(x[4 * h + 2] - __uint_as_float(o.y << 16),
-                                                     x[4 * h + 3] - __uint_as_float(o.y & 0xFFFF0000u)));
+                        const uint2 o = make_uint2(pack_bf16(x[k][4 * h], x[k][4 * h + 1]),
+                                                   pack_bf16(x[k][4 * h + 2], x[k][4 * h + 3]));
+                        *reinterpret_cast<uint2 *>(dst + k * 128 + ((h ? b1 : b0) ^ sw)) = o;
+                        x[k][4 * h] -= __uint_as_float(o.x << 16);
+                        x[k][4 * h + 1] -= __uint_as_float(o.x & 0xFFFF0000u);
+                        x[k][4 * h + 2] -= __uint_as_float(o.y << 16);
+                        x[k][4 * h + 3] -= __uint_as_float(o.y & 0xFFFF0000u);
+                    }
+                }
+                if (!it.paired) {   // the rest of the rounding
+#pragma unroll
+                    for (int k = 0; k < kGroup; ++k) {
+                        const int sw = ((i0 & 4) + k) << 4;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            *reinterpret_cast<uint2 *>(dst + C::kTileBytes + k * 128 + ((h ? b1 : b0) ^ sw)) =
+                                make_uint2(pack_bf16(x[k][4 * h], x[k][4 * h + 1]),
+                                           pack_bf16(x[k][4 * h + 2], x[k][4 * h + 3]));
                     }
                 }
             }
@@ -541,6 +564,13 @@ __device__ void pv_role(uint8_t *smem, Misc *ms) {
 }
 
 // ---------------------------------------------------------------- softmax role
+// 32 bytes of a row: one whole sector per thread.
+__device__ __forceinline__ void store32(void *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
+                                        uint32_t g, uint32_t h) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d),
+                 "r"(e), "r"(f), "r"(g), "r"(h)
+                 : "memory");
+}
 // Two fp32 lanes of one 64-bit register.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
     uint64_t r;
@@ -697,9 +727,8 @@ __device__ void softmax_role(const KvAttendArgs &a, Misc *ms, int s) {
                     tmem_wait_ld();
                     if (mine) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            *reinterpret_cast<uint4 *>(po + 32 * c + 4 * i) =
-                                make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                        for (int i = 0; i < 32; i += 8)
+                            store32(po + 32 * c + i, v[i], v[i + 1], v[i + 2], v[i + 3], v[i + 4], v[i + 5], v[i + 6], v[i + 7]);
                     }
                 }
             }
@@ -711,6 +740,7 @@ __device__ void softmax_role(const KvAttendArgs &a, Misc *ms, int s) {
             const float den = fmaf(l, f, a.sink && !none ? ex2(sink - top) : 0.f);
             const float w = none ? 0.f : f / den;
             const long long at = ((long long)(it.n0 + r / G) * a.HQ + hq) * D;
+            const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;   // (16 bytes are promised)
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t v[32];
@@ -721,15 +751,23 @@ __device__ void softmax_role(const KvAttendArgs &a, Misc *ms, int s) {
                 for (int i = 0; i < 32; ++i) x[i] = none ? 0.f : __uint_as_float(v[i]) * w;
                 if (mine) {
                     if constexpr (OBF16) {
-                        uint4 *p = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(a.out) + at + 32 * c);
+                        uint16_t *p = reinterpret_cast<uint16_t *>(a.out) + at + 32 * c;
+                        uint32_t y[16];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            p[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
-                                              pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+                        for (int i = 0; i < 16; ++i) y[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+                        if (wide) {
+                            store32(p, y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]);
+                            store32(p + 16, y[8], y[9], y[10], y[11], y[12], y[13], y[14], y[15]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                *reinterpret_cast<uint4 *>(p + 8 * i) = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                        }
                     } else {
-                        float4 *p = reinterpret_cast<float4 *>(reinterpret_cast<float *>(a.out) + at + 32 * c);
+                        float *p = reinterpret_cast<float *>(a.out) + at + 32 * c;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) p[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<float4 *>(p + 4 * i) = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
                     }
                 }
             }
@@ -786,7 +824,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
     __syncthreads();
     tc_fence_after();
     pdl_trigger();
-    pdl_wait();
+    // (behind kv_few_kernel of the same call, which lets this kernel start only
+    // when all before it has ended, the two run side by side; the
+    // end of this one waits for the other)
+    if (!a.beside) pdl_wait();
     CSLA_TL_WAITED();
     // registers: 2 x 128 x 176 + 128 x 96 + 128 x 64 = 65536, the launch's 512 x 128
     if (warp < 8) {
@@ -813,6 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
         tc_fence_after();
         tmem_dealloc(ms->tmem, 512);
     }
+    if (a.beside) pdl_wait();
 }
 
 // ---------------------------------------------------------------- join

@@ -202,13 +202,13 @@ __device__ void stage_q(const KvAttendArgs &a, const Item &it, uint8_t *qs, cons
         float2 cs[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) cs[j] = kv_cos_sin(it.pos0 + t, rl.pair >= 0 ? ms->turn[rl.pair + j] : 0);
-        float x[8];
+        float xr[1][8], (&x)[8] = xr[0];
         widen8<QBF16>(raw, x);
         if (a.gamma_q) {
             float g[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) g[i] = a.gamma_q[i < 4 ? rl.d0 + i : rl.d1 + i - 4];
-            row_norm<D>(x, g, a.eps);
+            rows_norm<D>(xr, g, a.eps);
         }
         if (a.d_rope) row_rope(x, a.pairs, cs);
         if (r0 + sub < it.rows) {
@@ -499,7 +499,6 @@ __global__ void __launch_bounds__(kThreads, 2) kv_few_kernel(const __grid_consta
     extern __shared__ uint8_t raw_smem[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
     Misc *ms = reinterpret_cast<Misc *>(smem + C::kOffMisc);
-    pdl_trigger();
     if (threadIdx.x < 64) ms->turn[threadIdx.x] = a.freq.turn[threadIdx.x];
     if (threadIdx.x == 64) {
         for (int i = 0; i < kItems; ++i) {
@@ -517,6 +516,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_few_kernel(const __grid_consta
     }
     __syncthreads();
     pdl_wait();
+    pdl_trigger();   // after the wait: what starts now finds everything before this kernel ended
     CSLA_TL_WAITED();
     if (threadIdx.x >= 32 * kConsumers)
         producer<D>(a, km, vm, smem, ms);
