@@ -263,121 +263,146 @@ __device__ void load_role(const KvAttendArgs &a, const CUtensorMap &km, const CU
 }
 
 // ---------------------------------------------------------------- Q role
+// Q rows of one stream's operand by four warps (warp = 0..3 of them): norm and
+// rotation in fp32, rounded to bf16 into the swizzled operand; an unpaired item keeps
+// the rounding's rest in the second operand.
 template <int D, bool QBF16>
-__device__ void q_role(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
+struct QRows {
     using C = Cfg<D>;
-    constexpr int kLanes = D / 8, kPer = 32 / kLanes;   // lanes per row, rows per step
-    constexpr int kGroup = 4;   // rows of a lane at a time: their chains of latencies overlap
-    const int warp = (threadIdx.x >> 5) - 8, lane = threadIdx.x & 31, c = lane % kLanes, sub = lane / kLanes;
-    const int G = a.HQ / a.HK;
-    const RowLane rl = row_lane<D>(c, a.d_rope, a.pairs);
+    static constexpr int kLanes = D / 8, kPer = 32 / kLanes;   // lanes per row, rows per step
+    static constexpr int kGroup = 4;   // rows of a lane at a time: their chains of latencies overlap
+    const KvAttendArgs &a;
+    uint8_t *smem;
+    Misc *ms;
+    int warp, lane, sub, G, b0, b1;
+    RowLane rl;
     float g[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = a.gamma_q ? a.gamma_q[i < 4 ? rl.d0 + i : rl.d1 + i - 4] : 1.f;
     unsigned long long turn[4];
+
+    __device__ __forceinline__ QRows(const KvAttendArgs &a_, uint8_t *smem_, Misc *ms_) : a(a_), smem(smem_), ms(ms_) {
+        warp = (threadIdx.x >> 5) & 3;
+        lane = threadIdx.x & 31;
+        const int c = lane % kLanes;
+        sub = lane / kLanes;
+        G = a.HQ / a.HK;
+        rl = row_lane<D>(c, a.d_rope, a.pairs);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) turn[j] = rl.pair >= 0 ? ms->turn[rl.pair + j] : 0;
-    // byte offsets of the lane's runs in a row of the operand (row 0's swizzle)
-    const int b0 = (rl.d0 >> 6) * C::kBlk + (rl.d0 & 63) * 2, b1 = (rl.d1 >> 6) * C::kBlk + (rl.d1 & 63) * 2;
-    Item it;
-    for (int n = 0; next_item(ms, n, &it); ++n) {
-#pragma unroll 1
-        for (int s = 0; s <= it.paired; ++s) {
-            // a lane takes four neighbouring rows of a group (mostly heads of one
-            // token: one rotation for all), the warp 4 kPer rows, the four warps 16 kPer
-            const int r0 = it.row0 + 128 * s, first = 4 * (warp * kPer + sub);
-            const int groups = min(32 / (4 * kPer), (it.rows - r0 - 4 * warp * kPer + 16 * kPer - 1) / (16 * kPer));
-            Raw8<QBF16> next[kGroup];
-            int npos[kGroup];
-            auto fetch = [&](int gr) {
-                int tok = (r0 + first + 16 * kPer * gr) / G, head = r0 + first + 16 * kPer * gr - tok * G;
+        for (int i = 0; i < 8; ++i) g[i] = a.gamma_q ? a.gamma_q[i < 4 ? rl.d0 + i : rl.d1 + i - 4] : 1.f;
 #pragma unroll
-                for (int k = 0; k < kGroup; ++k) {
-                    const int t = min(tok, it.T - 1);   // (rows that are not there: any)
-                    npos[k] = it.pos0 + t;
-                    next[k] = load8<QBF16>(a.q, (long long)(it.n0 + t) * a.q_stride + (it.hk * G + head) * D, rl);
-                    if (++head == G) {
-                        head = 0;
-                        ++tok;
-                    }
-                }
-            };
-            bool waited = n == 0;
-            if (groups > 0) fetch(0);
-#pragma unroll 1
-            for (int gr = 0; gr < groups; ++gr) {
-                Raw8<QBF16> raw[kGroup];
-                int pos[kGroup];
-#pragma unroll
-                for (int k = 0; k < kGroup; ++k) {
-                    raw[k] = next[k];
-                    pos[k] = npos[k];
-                }
-                if (gr + 1 < groups) fetch(gr + 1);   // a group ahead
-                // (the first rows' loads are in flight while the operand is still in use)
-                if (!waited) {
-                    if (!warp_all(kv_wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort))) return;
-                    if (!it.paired && !warp_all(kv_wait(&ms->q_empty[1], (n - 1) & 1, &ms->abort))) return;
-                    waited = true;
-                }
-                float x[kGroup][8];
-#pragma unroll
-                for (int k = 0; k < kGroup; ++k) widen8<QBF16>(raw[k], x[k]);
-                if (a.gamma_q) rows_norm<D>(x, g, a.eps);
-                if (a.d_rope) {
-                    float2 cs[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) cs[j] = kv_cos_sin(pos[0], turn[j]);   // (turn 0: unchanged)
-                    const bool one = __all_sync(0xffffffffu, pos[0] == pos[kGroup - 1]);
-                    row_rope(x[0], a.pairs, cs);
-                    if (one) {
-#pragma unroll
-                        for (int k = 1; k < kGroup; ++k) row_rope(x[k], a.pairs, cs);
-                    } else {
-#pragma unroll
-                        for (int k = 1; k < kGroup; ++k) {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) cs[j] = kv_cos_sin(pos[k], turn[j]);
-                            row_rope(x[k], a.pairs, cs);
+        for (int j = 0; j < 4; ++j) turn[j] = rl.pair >= 0 ? ms->turn[rl.pair + j] : 0;
+        // byte offsets of the lane's runs in a row of the operand (row 0's swizzle)
+        b0 = (rl.d0 >> 6) * C::kBlk + (rl.d0 & 63) * 2;
+        b1 = (rl.d1 >> 6) * C::kBlk + (rl.d1 & 63) * 2;
+    }
+    // Operand s of the CTA's n-th item.
+    __device__ __forceinline__ bool stage(const Item &it, int s, int n) {
+                    // a lane takes four neighbouring rows of a group (mostly heads of one
+                    // token: one rotation for all), the warp 4 kPer rows, the four warps 16 kPer
+                    const int r0 = it.row0 + 128 * s, first = 4 * (warp * kPer + sub);
+                    const int groups = min(32 / (4 * kPer), (it.rows - r0 - 4 * warp * kPer + 16 * kPer - 1) / (16 * kPer));
+                    Raw8<QBF16> next[kGroup];
+                    int npos[kGroup];
+                    auto fetch = [&](int gr) {
+                        int tok = (r0 + first + 16 * kPer * gr) / G, head = r0 + first + 16 * kPer * gr - tok * G;
+        #pragma unroll
+                        for (int k = 0; k < kGroup; ++k) {
+                            const int t = min(tok, it.T - 1);   // (rows that are not there: any)
+                            npos[k] = it.pos0 + t;
+                            next[k] = load8<QBF16>(a.q, (long long)(it.n0 + t) * a.q_stride + (it.hk * G + head) * D, rl);
+                            if (++head == G) {
+                                head = 0;
+                                ++tok;
+                            }
+                        }
+                    };
+                    bool waited = n == 0;
+                    if (groups > 0) fetch(0);
+        #pragma unroll 1
+                    for (int gr = 0; gr < groups; ++gr) {
+                        Raw8<QBF16> raw[kGroup];
+                        int pos[kGroup];
+        #pragma unroll
+                        for (int k = 0; k < kGroup; ++k) {
+                            raw[k] = next[k];
+                            pos[k] = npos[k];
+                        }
+                        if (gr + 1 < groups) fetch(gr + 1);   // a group ahead
+                        // (the first rows' loads are in flight while the operand is still in use)
+                        if (!waited) {
+                            if (!warp_all(kv_wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort))) return false;
+                            if (!it.paired && !warp_all(kv_wait(&ms->q_empty[1], (n - 1) & 1, &ms->abort))) return false;
+                            waited = true;
+                        }
+                        float x[kGroup][8];
+        #pragma unroll
+                        for (int k = 0; k < kGroup; ++k) widen8<QBF16>(raw[k], x[k]);
+                        if (a.gamma_q) rows_norm<D>(x, g, a.eps);
+                        if (a.d_rope) {
+                            float2 cs[4];
+        #pragma unroll
+                            for (int j = 0; j < 4; ++j) cs[j] = kv_cos_sin(pos[0], turn[j]);   // (turn 0: unchanged)
+                            const bool one = __all_sync(0xffffffffu, pos[0] == pos[kGroup - 1]);
+                            row_rope(x[0], a.pairs, cs);
+                            if (one) {
+        #pragma unroll
+                                for (int k = 1; k < kGroup; ++k) row_rope(x[k], a.pairs, cs);
+                            } else {
+        #pragma unroll
+                                for (int k = 1; k < kGroup; ++k) {
+        #pragma unroll
+                                    for (int j = 0; j < 4; ++j) cs[j] = kv_cos_sin(pos[k], turn[j]);
+                                    row_rope(x[k], a.pairs, cs);
+                                }
+                            }
+                        }
+                        const int i0 = first + 16 * kPer * gr;   // first row of the operand, a multiple of 4
+                        uint8_t *dst = smem + C::kOffQ + s * C::kTileBytes + i0 * 128;
+        #pragma unroll
+                        for (int k = 0; k < kGroup; ++k) {
+                            const int sw = ((i0 & 4) + k) << 4;
+        #pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint2 o = make_uint2(pack_bf16(x[k][4 * h], x[k][4 * h + 1]),
+                                                           pack_bf16(x[k][4 * h + 2], x[k][4 * h + 3]));
+                                *reinterpret_cast<uint2 *>(dst + k * 128 + ((h ? b1 : b0) ^ sw)) = o;
+                                x[k][4 * h] -= __uint_as_float(o.x << 16);
+                                x[k][4 * h + 1] -= __uint_as_float(o.x & 0xFFFF0000u);
+                                x[k][4 * h + 2] -= __uint_as_float(o.y << 16);
+                                x[k][4 * h + 3] -= __uint_as_float(o.y & 0xFFFF0000u);
+                            }
+                        }
+                        if (!it.paired) {   // the rest of the rounding
+        #pragma unroll
+                            for (int k = 0; k < kGroup; ++k) {
+                                const int sw = ((i0 & 4) + k) << 4;
+        #pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    *reinterpret_cast<uint2 *>(dst + C::kTileBytes + k * 128 + ((h ? b1 : b0) ^ sw)) =
+                                        make_uint2(pack_bf16(x[k][4 * h], x[k][4 * h + 1]),
+                                                   pack_bf16(x[k][4 * h + 2], x[k][4 * h + 3]));
+                            }
                         }
                     }
-                }
-                const int i0 = first + 16 * kPer * gr;   // first row of the operand, a multiple of 4
-                uint8_t *dst = smem + C::kOffQ + s * C::kTileBytes + i0 * 128;
-#pragma unroll
-                for (int k = 0; k < kGroup; ++k) {
-                    const int sw = ((i0 & 4) + k) << 4;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint2 o = make_uint2(pack_bf16(x[k][4 * h], x[k][4 * h + 1]),
-                                                   pack_bf16(x[k][4 * h + 2], x[k][4 * h + 3]));
-                        *reinterpret_cast<uint2 *>(dst + k * 128 + ((h ? b1 : b0) ^ sw)) = o;
-                        x[k][4 * h] -= __uint_as_float(o.x << 16);
-                        x[k][4 * h + 1] -= __uint_as_float(o.x & 0xFFFF0000u);
-                        x[k][4 * h + 2] -= __uint_as_float(o.y << 16);
-                        x[k][4 * h + 3] -= __uint_as_float(o.y & 0xFFFF0000u);
+                    if (!waited) {   // (no row of this warp: the operand's phases are kept in step all the same)
+                        if (!warp_all(kv_wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort))) return false;
+                        if (!it.paired && !warp_all(kv_wait(&ms->q_empty[1], (n - 1) & 1, &ms->abort))) return false;
                     }
-                }
-                if (!it.paired) {   // the rest of the rounding
-#pragma unroll
-                    for (int k = 0; k < kGroup; ++k) {
-                        const int sw = ((i0 & 4) + k) << 4;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            *reinterpret_cast<uint2 *>(dst + C::kTileBytes + k * 128 + ((h ? b1 : b0) ^ sw)) =
-                                make_uint2(pack_bf16(x[k][4 * h], x[k][4 * h + 1]),
-                                           pack_bf16(x[k][4 * h + 2], x[k][4 * h + 3]));
-                    }
-                }
-            }
-            if (!waited) {   // (no row of this warp: the operand's phases are kept in step all the same)
-                if (!warp_all(kv_wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort))) return;
-                if (!it.paired && !warp_all(kv_wait(&ms->q_empty[1], (n - 1) & 1, &ms->abort))) return;
-            }
-            fence_proxy_async_smem();
-            mbar_arrive_warp(&ms->q_full[s]);
-            if (!it.paired) mbar_arrive_warp(&ms->q_full[1]);
-        }
+        fence_proxy_async_smem();
+        mbar_arrive_warp(&ms->q_full[s]);
+        if (!it.paired) mbar_arrive_warp(&ms->q_full[1]);
+        return true;
+    }
+};
+
+template <int D, bool QBF16>
+__device__ void q_role(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
+    QRows<D, QBF16> q(a, smem, ms);
+    Item it;
+    for (int n = 0; next_item(ms, n, &it); ++n) {
+        if (n == 0) continue;   // the softmax warps', which have nothing else to do yet
+#pragma unroll 1
+        for (int s = 0; s <= it.paired; ++s)
+            if (!q.stage(it, s, n)) return;
     }
 }
 
@@ -591,8 +616,8 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-template <int D, bool OBF16>
-__device__ void softmax_role(const KvAttendArgs &a, Misc *ms, int s) {
+template <int D, bool QBF16, bool OBF16>
+__device__ void softmax_role(const KvAttendArgs &a, uint8_t *smem, Misc *ms, int s) {
     using C = Cfg<D>;
     const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const uint32_t tw = ms->tmem + ((uint32_t)(warp * 32) << 16);
@@ -611,6 +636,12 @@ __device__ void softmax_role(const KvAttendArgs &a, Misc *ms, int s) {
             return;
         }
         const bool paired = it.paired;
+        // the first item's Q is on nobody's time but the SM's: each stream's
+        // four warps stage their own (256 rows: 11 us by the Q warps, half by these)
+        if (n == 0 && (paired || s == 0)) {
+            QRows<D, QBF16> q(a, smem, ms);
+            if (!q.stage(it, s, 0)) return;
+        }
         const int row = it.row0 + (it.paired ? 128 * s : 0) + 32 * warp + lane;
         const bool mine = row < it.rows;
         const bool idle = it.row0 + (it.paired ? 128 * s : 0) + 32 * warp >= it.rows;   // no row of the warp is real
@@ -832,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
     // registers: 2 x 128 x 176 + 128 x 96 + 128 x 64 = 65536, the launch's 512 x 128
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
-        softmax_role<D, OBF16>(a, ms, warp >> 2);
+        softmax_role<D, QBF16, OBF16>(a, smem, ms, warp >> 2);
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
         q_role<D, QBF16>(a, smem, ms);
