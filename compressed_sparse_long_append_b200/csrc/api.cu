@@ -756,7 +756,8 @@ static long long kv_most_part_rows(const csla_kv_cfg *c, int B, int N, int max_n
     const long long G = c->HQ / c->HK, HK = c->HK, nt = kv_most_tiles(c, max_new, max_len);
     auto least = [](long long x, long long y) { return x < y ? x : y; };
     auto parts = [&](int kind) {
-        const long long fit = nt / kv_min_tiles(kind, c->D), n = least(fit, kv_units(kind) / HK);
+        // (a context of 8 pages has 4 chunks, as one of 16)
+        const long long fit = nt / kv_min_tiles(kind, c->D, 9), n = least(fit < 4 ? 4 : fit, kv_units(kind) / HK);
         return n > 1 ? n : 1;
     };
     if (nt <= 1) return 0;
@@ -770,7 +771,7 @@ static long long kv_most_part_rows(const csla_kv_cfg *c, int B, int N, int max_n
         tokens = least(N, B * least(max_new, 128 / G));
         rows += tokens * c->HQ * 2 * parts(kKvSingle);
     }
-    if (max_new * G > 128 && nt > kv_min_tiles(kKvPaired, c->D)) {
+    if (max_new * G > 128 && nt > kv_min_tiles(kKvPaired, c->D, 9)) {
         // a request has chunks * 256 * R * HK rows at most, chunks <= units / (R * HK)
         const long long each = 256ll * kv_units(kKvPaired), n = least(B, N * G / 129);
         rows += least(n * each, (long long)N * c->HQ * parts(kKvPaired));
@@ -797,7 +798,9 @@ static void kv_workspace_parts(uint8_t *ws, int B, long long rows, KvAttendArgs 
 }
 
 size_t csla_kv_workspace_size(const csla_kv_cfg *cfg, int32_t B, int32_t N, int32_t max_new, int32_t max_len) {
-    if (check_kv_cfg(cfg) != CSLA_OK || B < 1 || N < 1 || max_new < 1 || max_len < 1) return 0;
+    if (check_kv_cfg(cfg) != CSLA_OK || B < 1 || B > 65535 || N < 1 || max_new < 1 || max_len < 1 ||
+        max_len > (1 << 30))
+        return 0;
     return kv_workspace_bytes(cfg, B, kv_most_part_rows(cfg, B, N, max_new, max_len, 0));
 }
 
@@ -812,7 +815,7 @@ int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
     if (rc) return rc;
     if (!kv_rows_ok(q, q_stride, (int64_t)cfg->HQ * cfg->D, q_dtype)) return CSLA_ERR_ARG;
     if (!out || !aligned16(out) || (out_dtype != CSLA_F32 && out_dtype != CSLA_BF16)) return CSLA_ERR_ARG;
-    if (max_new < 1 || max_len < 1 || (!q_start && a.bt.T > max_new)) return CSLA_ERR_ARG;
+    if (max_new < 1 || max_len < 1 || max_len > (1 << 30) || (!q_start && a.bt.T > max_new)) return CSLA_ERR_ARG;
     if ((long long)kv->n_pages * cfg->HK * CSLA_PAGE_TOKENS >= (1ll << 31) || (long long)N * cfg->HQ >= (1ll << 31))
         return CSLA_ERR_UNSUPPORTED;
     const size_t need = csla_kv_workspace_size(cfg, B, N, max_new, max_len);
@@ -839,7 +842,7 @@ int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
         if (!encode_bf16_2d(&km, kv->k, cfg->D, cache_rows, kv_few_box(cfg->D)) ||
             !encode_bf16_2d(&vm, kv->v, cfg->D, cache_rows, kv_few_box(cfg->D)))
             return CSLA_ERR_CUDA;
-        const long long m = kv_min_tiles(kKvFew, cfg->D);
+        const long long m = kv_min_tiles(kKvFew, cfg->D, 1);
         e = launch_kv_few(a, q16, o16, km, vm, num_sms_current(),
                           (long long)B * cfg->HK * ((nt + m - 1) / m), st);
     }
@@ -848,7 +851,7 @@ int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
         if (!encode_bf16_2d(&km, kv->k, cfg->D, cache_rows, CSLA_PAGE_TOKENS) ||
             !encode_bf16_2d(&vm, kv->v, cfg->D, cache_rows, CSLA_PAGE_TOKENS))
             return CSLA_ERR_CUDA;
-        const long long m = kv_min_tiles(kKvSingle, cfg->D);
+        const long long m = kv_min_tiles(kKvSingle, cfg->D, 1);
         a.beside = least_rows <= kKvFewRows;
         e = launch_kv_attend(a, q16, o16, km, vm, num_sms_current(),
                              ((long long)N * G / 256 + B) * cfg->HK * ((nt + m - 1) / m), st);

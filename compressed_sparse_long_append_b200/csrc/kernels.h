@@ -347,9 +347,19 @@ struct KvPlan {
     int rows, R, Rs, rows_s, kind, c, nch, T, G, heads_inside;   // rows_s: rows of the cut row tiles
 };
 constexpr int kKvFewRows = 16;
-// items that a long request is cut into (all heads), and the least tiles of a chunk, by kind
+// items that a long request is cut into (all heads), and the least tiles of a
+// chunk, by kind.  An item costs about as much as two pages of 128 dims (its
+// Q, its join), so short chunks cost throughput, and long ones the latency of
+// a lone short request:
+//   few    4 pages of 128 dims (64 ragged requests: 143 us, with 2 pages 151), but 2
+//          in a context of up to 8 (one user, 901 tokens, 8 heads: 13.5 us, with 4
+//          pages 15.5); 8 of 64 dims (32 requests, window of 9 pages, 16 heads: 33 us whole, 39 in two);
+//   single 16 (32 requests of 20 rows: 144 us, with 8 tiles 166);
+//   paired 8, and only when the row tiles do not fill the SMs.
 __host__ __device__ constexpr int kv_units(int kind) { return kind == kKvPaired ? 148 : 296; }
-__host__ __device__ constexpr int kv_min_tiles(int kind, int D) { return kind == kKvFew ? 512 / D : (kind == kKvSingle ? 16 : 8); }
+__host__ __device__ constexpr int kv_min_tiles(int kind, int D, int nt) {
+    return kind == kKvFew ? (D == 64 ? 8 : (nt <= 8 ? 2 : 4)) : (kind == kKvSingle ? 16 : 8);
+}
 
 // Key tiles of row tile i: [lo, hi); of its two halves: first half [lo, hi0), second [lo1, hi).
 // [k_lo, k_hi): the positions that some row sees.
@@ -388,18 +398,18 @@ __host__ __device__ inline KvPlan kv_plan(int T, int L, int G, int HK, int windo
     // key tiles of the longest row tile (with a window: an upper bound)
     int nt = (L - 1) / CSLA_PAGE_TOKENS + 1;
     if (window > 0 && window < L) {
-        const int w = (window + (p.kind == kKvPaired ? 256 / G + 1 : T) + CSLA_PAGE_TOKENS - 2) / CSLA_PAGE_TOKENS + 1;
+        const int w = (window - 2 + (p.kind == kKvPaired ? 256 / G + 1 : T) + CSLA_PAGE_TOKENS) / CSLA_PAGE_TOKENS + 1;
         nt = w < nt ? w : nt;
     }
     // chunks: kv_units items in all at most, kv_min_tiles tiles at least, of even sizes
     // (32-bit divisions only: this runs ahead of every item's first load)
     int n = (int)(kv_units(p.kind) / (unsigned)(HK * p.R));
-    const int fit = nt / kv_min_tiles(p.kind, D);
+    const int fit = nt / kv_min_tiles(p.kind, D, nt);
     n = n < fit ? n : fit;
     const bool many = HK * p.R >= kv_units(p.kind);
     int c = n > 1 ? (nt + n - 1) / n : nt;
     p.Rs = p.kind == kKvSingle || c < nt ? p.R : 0;
-    if (p.kind == kKvPaired && many && window == 0 && L - T >= T) {
+    if (p.kind == kKvPaired && many && (window == 0 || window >= L) && L - T >= T) {
         // more row tiles than SMs, all of about nt tiles
         const int sms = kv_units(kKvPaired), left = HK * p.R % sms, cuts = left ? sms / left : 1;
         if (cuts > 1 && nt >= 32 && HK * p.R < 16 * sms) {

@@ -744,7 +744,7 @@ __device__ void softmax_role(const KvAttendArgs &a, uint8_t *smem, Misc *ms, int
             mbar_arrive_warp(&ms->item_empty[slot]);
             continue;
         }
-        const bool none = m == -INFINITY;
+        const bool none = m == -INFINITY && l == 0.f;   // no token at all (scores that are all NaN leave l NaN)
         if (it.part >= 0) {
             // partial: O and (m, l), of part `part` (+ s for a shared row tile)
             const long long pr = it.base + ((long long)(it.part + (it.paired ? 0 : s)) * a.HK + it.hk) * it.rows_s + r;
@@ -956,8 +956,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_c
             const float2 ml = lane < parts ? a.part_ml[pr + lane * step] : make_float2(-INFINITY, 0.f);
             const float mx = warp_max(ml.x), top = mx == -INFINITY ? 0.f : fmaxf(mx, sink);
             const float w = ex2(ml.x - top);   // (-inf: 0)
-            const float den = warp_sum(w * ml.y) + (a.sink ? ex2(sink - top) : 0.f);
-            inv = mx == -INFINITY ? 0.f : 1.f / den;
+            const float all = warp_sum(w * ml.y);
+            inv = mx == -INFINITY && all == 0.f ? 0.f : 1.f / (all + (a.sink ? ex2(sink - top) : 0.f));
             join_parts<D>(a.part_o, pr, step, parts, w, o);
         } else {
             // the largest maximum and the sum over all parts (every warp the
@@ -971,8 +971,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_c
                 const float2 ml = a.part_ml[pr + i * step];
                 den += ex2(ml.x - top) * ml.y;
             }
-            den = warp_sum(den) + (a.sink ? ex2(sink - top) : 0.f);
-            inv = mx == -INFINITY ? 0.f : 1.f / den;
+            den = warp_sum(den);
+            inv = mx == -INFINITY && den == 0.f ? 0.f : 1.f / (den + (a.sink ? ex2(sink - top) : 0.f));
             const int share = block ? (parts + kJoinWarps - 1) / kJoinWarps : parts;
             const int i0 = block ? min(parts, warp * share) : 0, i1 = min(parts, i0 + share);
             for (int i = i0; i < i1; i += 32) {

@@ -470,7 +470,7 @@ __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
                         *reinterpret_cast<float2 *>(a.part_o + pr * D + 8 * j + d) = make_float2(o[j][2 * h], o[j][2 * h + 1]);
                 } else {
                     const int t = r / G, hq = it.hk * G + r - t * G;
-                    const bool none = m[h] == -INFINITY;
+                    const bool none = m[h] == -INFINITY && l[h] == 0.f;   // no token at all (scores that are all NaN leave l NaN)
                     const float sink = a.sink ? a.sink[hq] * kLog2e : -INFINITY;
                     const float top = fmaxf(m[h], sink);
                     const float f = none ? 0.f : ex2(m[h] - top);

@@ -576,7 +576,7 @@ int csla_kv_append(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
  * not must be finite for the others too (it enters with weight zero).
  *   q [N][HQ][D] q_dtype, rows q_stride elements apart; sink f32 [HQ] or
  *   NULL; gamma_q f32 [D] or NULL; out [N][HQ][D] out_dtype, 16-byte aligned.
- *   max_new >= every T_b, max_len >= every len (host bounds).
+ *   max_new >= every T_b, max_len >= every len (host bounds; max_len <= 2^30).
  * Batch invariant: how a request is split and joined is a function of its
  * own T_b and len and of the layer's shape.
  * workspace: csla_kv_workspace_size(cfg, B, N, max_new, max_len) bytes,

@@ -286,7 +286,109 @@ def test_same_request_twice_and_idle_slots():
     assert torch.equal(out[0], out[1])
 
 
+@pytest.mark.parametrize("T,L", [(1, [300, 1, 4097]), (5, [5, 700, 2100]), (40, [900, 41]), (300, [300, 1000])])
+def test_equal_numbers_of_new_tokens_need_no_offsets(T, L):
+    for D, HQ, HK in ((128, 8, 2), (64, 3, 3)):
+        b, out = _run(DenseShape(D=D, HQ=HQ, HK=HK, d_rope=64, window=0 if T < 40 else 200), [T] * len(L), L, seed=T,
+                      uniform=True)
+        b.start = torch.tensor(b.start_l, dtype=torch.int32, device=DEV)
+        assert torch.equal(b.attend(), out)
+
+
+def test_long_chunk_over_a_long_context():
+    """Row tiles of more than a round over the SMs, the last ones' keys cut."""
+    b = Batch(DenseShape(D=128, HQ=16, HK=16, d_rope=64), [2500], [7000], seed=40)
+    b.fill()
+    out = b.attend(F32)
+    no_device_error()
+    rows = [0, 1, 127, 128, 255, 256, 300, 511, 512, 1000, 1791, 1792, 2047, 2048, 2499]   # of the first and last row tiles
+    from kv_reference import attend_request, with_output_step
+    k, v = b.rows(0, b.lb.k), b.rows(0, b.lb.v)
+    q = b.q.reshape(b.N, 16, 128)
+    for r in rows:
+        n = 4500 + r + 1
+        o, tol = attend_request(q[r:r + 1], k[:n], v[:n], n - 1, b.shape, False, b.sink, b.gamma_q)
+        assert bool(((out[r:r + 1].double() - o).abs() <= with_output_step(o, tol, F32)).all()), r
+    assert bool(torch.isfinite(out).all())
+
+
+def test_a_nan_stays_in_the_rows_that_see_it():
+    """NaN in one token's query, in one visible key, in one visible value: rows that see it are NaN, others are as without."""
+    for T, L in (([1, 1], [700, 700]), ([40, 40], [300, 300]), ([200, 200], [500, 500])):
+        b = Batch(DenseShape(D=64, HQ=4, HK=2, d_rope=0), T, L, seed=41)
+        b.fill()
+        clean = b.attend(F32)
+        b.q = b.q.clone()
+        b.q[T[0] - 1, 5] = float("nan")           # request 0, last token, head 0
+        out = b.attend(F32)
+        assert bool(torch.isnan(out[T[0] - 1, 0]).all())
+        out[T[0] - 1, 0] = clean[T[0] - 1, 0]
+        assert torch.equal(out, clean)
+        b.q[T[0] - 1, 5] = 0.0
+        clean = b.attend(F32)
+        for pool in (b.lb.k, b.lb.v):              # request 1, its very first token, KV head 1: every row of heads 2, 3 sees it
+            page = b.table[b.slots_l[1], 0].item()
+            old = pool[page, 1, 0].clone()
+            pool[page, 1, 0] = float("nan")
+            out = b.attend(F32)
+            assert bool(torch.isnan(out[T[0]:, 2:]).all())
+            out[T[0]:, 2:] = clean[T[0]:, 2:]
+            assert torch.equal(out, clean)
+            pool[page, 1, 0] = old
+    no_device_error()
+
+
+def test_workspace_is_enough_and_kept_within():
+    """The bytes asked for suffice at any 16-byte boundary, and nothing behind them is touched."""
+    import random
+    rng = random.Random(42)
+    for i in range(24):
+        HK = rng.choice([1, 2, 3, 8])
+        G = rng.choice([1, 2, 4, 7, 16])
+        B = rng.randint(1, 4)
+        T = [rng.choice([0, 1, 1, 3, rng.randint(1, 40), rng.randint(1, 400)]) for _ in range(B)]
+        T[0] = max(T[0], 1)
+        L = [t + rng.choice([0, 50, rng.randint(0, 3000), rng.randint(0, 9000)]) for t in T]
+        b = Batch(DenseShape(D=rng.choice([64, 128]), HQ=HK * G, HK=HK, d_rope=32, window=rng.choice([0, 0, 700])), T, L, seed=i)
+        b.fill()
+        want = b.attend()
+        need = C.csla_kv_workspace_size(b.lb.cfg(), b.B, b.N, b.max_new, b.max_len)
+        buf = torch.full((need + 64 + 4096,), 77, dtype=torch.uint8, device=DEV)
+        for off in (0, 16, 32, 48):
+            buf.fill_(77)
+            out = b.attend(ws=buf[off:])
+            assert torch.equal(out, want)
+            assert bool((buf[:off] == 77).all()) and bool((buf[off + need:] == 77).all()), (i, off)
+    no_device_error()
+
+
 # ---------------------------------------------------------------- streams and graphs
+def test_two_graphs_share_a_workspace_in_turn():
+    """Two captured calls on one workspace, replayed one after the other, and an eager call in between."""
+    bs = [Batch(DenseShape(D=128, HQ=16, HK=4, d_rope=64), T, L, seed=50 + i)
+          for i, (T, L) in enumerate([([1, 1], [3000, 9000]), ([1, 20, 200], [2500, 1300, 2000])])]
+    for b in bs:
+        b.fill()
+    want = [b.attend() for b in bs]
+    need = max(C.csla_kv_workspace_size(b.lb.cfg(), b.B, b.N, b.max_new, b.max_len) for b in bs)
+    ws = torch.full((max(need // 4 + 4, 4),), float("nan"), dtype=torch.float32, device=DEV)
+    outs, graphs = [torch.zeros_like(w) for w in want], []
+    torch.cuda.synchronize()
+    for b, o in zip(bs, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            b.attend(out=o, ws=ws)
+        graphs.append(g)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        for i in (0, 1, 1, 0):
+            graphs[i].replay()
+            assert torch.equal(bs[1].attend(ws=ws), want[1])
+        assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+    no_device_error()
+
+
 def test_other_stream_and_two_calls_at_once():
     s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
     bs = [Batch(DenseShape(D=128, HQ=32, HK=8, d_rope=64), [1, 200], [6000, 900], seed=22 + i) for i in range(2)]

@@ -91,7 +91,8 @@ def test_bad_append_rows(bad):
 
 
 @pytest.mark.parametrize("bad", [dict(q=None), dict(out=None), dict(q=FAKE + 4), dict(out=FAKE + 8), dict(qs=8188),
-                                 dict(qs=8196), dict(qdt=2), dict(odt=3), dict(mn=0), dict(ml=0), dict(q_start=None, mn=1)])
+                                 dict(qs=8196), dict(qdt=2), dict(odt=3), dict(mn=0), dict(ml=0), dict(q_start=None, mn=1),
+                                 dict(ml=(1 << 30) + 1)])
 def test_bad_attend_rows(bad):
     assert _attend(**bad) == C.CSLA_ERR_ARG
 
