@@ -757,7 +757,9 @@ static long long kv_most_part_rows(const csla_kv_cfg *c, int B, int N, int max_n
     auto least = [](long long x, long long y) { return x < y ? x : y; };
     auto parts = [&](int kind) {
         // (a context of 8 pages has 4 chunks, as one of 16)
-        const long long fit = nt / kv_min_tiles(kind, c->D, 9), n = least(fit < 4 ? 4 : fit, kv_units(kind) / HK);
+        // (single: of 12 tiles at least)
+        const long long fit = nt / (kind == kKvSingle ? 12 : kv_min_tiles(kind, c->D, 9)),
+                        n = least(fit < 4 ? 4 : fit, kv_units(kind) / HK);
         return n > 1 ? n : 1;
     };
     if (nt <= 1) return 0;

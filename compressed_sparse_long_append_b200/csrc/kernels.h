@@ -405,7 +405,10 @@ __host__ __device__ inline KvPlan kv_plan(int T, int L, int G, int HK, int windo
     // (32-bit divisions only: this runs ahead of every item's first load)
     int n = (int)(kv_units(p.kind) / (unsigned)(HK * p.R));
     const int fit = nt / kv_min_tiles(p.kind, D, nt);
-    n = n < fit ? n : fit;
+    if (p.kind == kKvSingle && n > fit && n / 2 * 12 <= nt && n / 2 > fit)
+        n /= 2;   // one round over the SMs with chunks of 12 to 16 tiles rather than less than one
+    else
+        n = n < fit ? n : fit;
     const bool many = HK * p.R >= kv_units(p.kind);
     int c = n > 1 ? (nt + n - 1) / n : nt;
     p.Rs = p.kind == kKvSingle || c < nt ? p.R : 0;

@@ -270,7 +270,9 @@ template <int D, bool QBF16>
 struct QRows {
     using C = Cfg<D>;
     static constexpr int kLanes = D / 8, kPer = 32 / kLanes;   // lanes per row, rows per step
-    static constexpr int kGroup = 4;   // rows of a lane at a time: their chains of latencies overlap
+    // Rows of a lane at a time: enough for two chains of latencies to overlap, and
+    // little code, which the instruction cache has lost since the item before.
+    static constexpr int kGroup = 2;
     const KvAttendArgs &a;
     uint8_t *smem;
     Misc *ms;
@@ -296,97 +298,98 @@ struct QRows {
     }
     // Operand s of the CTA's n-th item.
     __device__ __forceinline__ bool stage(const Item &it, int s, int n) {
-                    // a lane takes four neighbouring rows of a group (mostly heads of one
-                    // token: one rotation for all), the warp 4 kPer rows, the four warps 16 kPer
-                    const int r0 = it.row0 + 128 * s, first = 4 * (warp * kPer + sub);
-                    const int groups = min(32 / (4 * kPer), (it.rows - r0 - 4 * warp * kPer + 16 * kPer - 1) / (16 * kPer));
-                    Raw8<QBF16> next[kGroup];
-                    int npos[kGroup];
-                    auto fetch = [&](int gr) {
-                        int tok = (r0 + first + 16 * kPer * gr) / G, head = r0 + first + 16 * kPer * gr - tok * G;
-        #pragma unroll
-                        for (int k = 0; k < kGroup; ++k) {
-                            const int t = min(tok, it.T - 1);   // (rows that are not there: any)
-                            npos[k] = it.pos0 + t;
-                            next[k] = load8<QBF16>(a.q, (long long)(it.n0 + t) * a.q_stride + (it.hk * G + head) * D, rl);
-                            if (++head == G) {
-                                head = 0;
-                                ++tok;
-                            }
-                        }
-                    };
-                    bool waited = n == 0;
-                    if (groups > 0) fetch(0);
-        #pragma unroll 1
-                    for (int gr = 0; gr < groups; ++gr) {
-                        Raw8<QBF16> raw[kGroup];
-                        int pos[kGroup];
-        #pragma unroll
-                        for (int k = 0; k < kGroup; ++k) {
-                            raw[k] = next[k];
-                            pos[k] = npos[k];
-                        }
-                        if (gr + 1 < groups) fetch(gr + 1);   // a group ahead
-                        // (the first rows' loads are in flight while the operand is still in use)
-                        if (!waited) {
-                            if (!warp_all(kv_wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort))) return false;
-                            if (!it.paired && !warp_all(kv_wait(&ms->q_empty[1], (n - 1) & 1, &ms->abort))) return false;
-                            waited = true;
-                        }
-                        float x[kGroup][8];
-        #pragma unroll
-                        for (int k = 0; k < kGroup; ++k) widen8<QBF16>(raw[k], x[k]);
-                        if (a.gamma_q) rows_norm<D>(x, g, a.eps);
-                        if (a.d_rope) {
-                            float2 cs[4];
-        #pragma unroll
-                            for (int j = 0; j < 4; ++j) cs[j] = kv_cos_sin(pos[0], turn[j]);   // (turn 0: unchanged)
-                            const bool one = __all_sync(0xffffffffu, pos[0] == pos[kGroup - 1]);
-                            row_rope(x[0], a.pairs, cs);
-                            if (one) {
-        #pragma unroll
-                                for (int k = 1; k < kGroup; ++k) row_rope(x[k], a.pairs, cs);
-                            } else {
-        #pragma unroll
-                                for (int k = 1; k < kGroup; ++k) {
-        #pragma unroll
-                                    for (int j = 0; j < 4; ++j) cs[j] = kv_cos_sin(pos[k], turn[j]);
-                                    row_rope(x[k], a.pairs, cs);
-                                }
-                            }
-                        }
-                        const int i0 = first + 16 * kPer * gr;   // first row of the operand, a multiple of 4
-                        uint8_t *dst = smem + C::kOffQ + s * C::kTileBytes + i0 * 128;
-        #pragma unroll
-                        for (int k = 0; k < kGroup; ++k) {
-                            const int sw = ((i0 & 4) + k) << 4;
-        #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const uint2 o = make_uint2(pack_bf16(x[k][4 * h], x[k][4 * h + 1]),
-                                                           pack_bf16(x[k][4 * h + 2], x[k][4 * h + 3]));
-                                *reinterpret_cast<uint2 *>(dst + k * 128 + ((h ? b1 : b0) ^ sw)) = o;
-                                x[k][4 * h] -= __uint_as_float(o.x << 16);
-                                x[k][4 * h + 1] -= __uint_as_float(o.x & 0xFFFF0000u);
-                                x[k][4 * h + 2] -= __uint_as_float(o.y << 16);
-                                x[k][4 * h + 3] -= __uint_as_float(o.y & 0xFFFF0000u);
-                            }
-                        }
-                        if (!it.paired) {   // the rest of the rounding
-        #pragma unroll
-                            for (int k = 0; k < kGroup; ++k) {
-                                const int sw = ((i0 & 4) + k) << 4;
-        #pragma unroll
-                                for (int h = 0; h < 2; ++h)
-                                    *reinterpret_cast<uint2 *>(dst + C::kTileBytes + k * 128 + ((h ? b1 : b0) ^ sw)) =
-                                        make_uint2(pack_bf16(x[k][4 * h], x[k][4 * h + 1]),
-                                                   pack_bf16(x[k][4 * h + 2], x[k][4 * h + 3]));
-                            }
-                        }
+        // a lane takes kGroup neighbouring rows (mostly heads of one token: one
+        // rotation for all), the four warps kPass rows
+        constexpr int kPass = 4 * kGroup * kPer;
+        const int r0 = it.row0 + 128 * s, first = kGroup * (warp * kPer + sub);
+        const int groups = min(128 / kPass, (it.rows - r0 - kGroup * warp * kPer + kPass - 1) / kPass);
+        Raw8<QBF16> next[kGroup];
+        int npos[kGroup];
+        auto fetch = [&](int gr) {
+            int tok = (r0 + first + kPass * gr) / G, head = r0 + first + kPass * gr - tok * G;
+#pragma unroll
+            for (int k = 0; k < kGroup; ++k) {
+                const int t = min(tok, it.T - 1);   // (rows that are not there: any)
+                npos[k] = it.pos0 + t;
+                next[k] = load8<QBF16>(a.q, (long long)(it.n0 + t) * a.q_stride + (it.hk * G + head) * D, rl);
+                if (++head == G) {
+                    head = 0;
+                    ++tok;
+                }
+            }
+        };
+        bool waited = n == 0;
+        if (groups > 0) fetch(0);
+#pragma unroll 1
+        for (int gr = 0; gr < groups; ++gr) {
+            Raw8<QBF16> raw[kGroup];
+            int pos[kGroup];
+#pragma unroll
+            for (int k = 0; k < kGroup; ++k) {
+                raw[k] = next[k];
+                pos[k] = npos[k];
+            }
+            if (gr + 1 < groups) fetch(gr + 1);   // a group ahead
+            // (the first rows' loads are in flight while the operand is still in use)
+            if (!waited) {
+                if (!warp_all(kv_wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort))) return false;
+                if (!it.paired && !warp_all(kv_wait(&ms->q_empty[1], (n - 1) & 1, &ms->abort))) return false;
+                waited = true;
+            }
+            float x[kGroup][8];
+#pragma unroll
+            for (int k = 0; k < kGroup; ++k) widen8<QBF16>(raw[k], x[k]);
+            if (a.gamma_q) rows_norm<D>(x, g, a.eps);
+            if (a.d_rope) {
+                float2 cs[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) cs[j] = kv_cos_sin(pos[0], turn[j]);   // (turn 0: unchanged)
+                const bool one = __all_sync(0xffffffffu, pos[0] == pos[kGroup - 1]);
+                row_rope(x[0], a.pairs, cs);
+                if (one) {
+#pragma unroll
+                    for (int k = 1; k < kGroup; ++k) row_rope(x[k], a.pairs, cs);
+                } else {
+#pragma unroll
+                    for (int k = 1; k < kGroup; ++k) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) cs[j] = kv_cos_sin(pos[k], turn[j]);
+                        row_rope(x[k], a.pairs, cs);
                     }
-                    if (!waited) {   // (no row of this warp: the operand's phases are kept in step all the same)
-                        if (!warp_all(kv_wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort))) return false;
-                        if (!it.paired && !warp_all(kv_wait(&ms->q_empty[1], (n - 1) & 1, &ms->abort))) return false;
-                    }
+                }
+            }
+            const int i0 = first + kPass * gr;   // first row of the operand, a multiple of kGroup
+            uint8_t *dst = smem + C::kOffQ + s * C::kTileBytes + i0 * 128;
+#pragma unroll
+            for (int k = 0; k < kGroup; ++k) {
+                const int sw = ((i0 & 7) + k) << 4;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint2 o = make_uint2(pack_bf16(x[k][4 * h], x[k][4 * h + 1]),
+                                               pack_bf16(x[k][4 * h + 2], x[k][4 * h + 3]));
+                    *reinterpret_cast<uint2 *>(dst + k * 128 + ((h ? b1 : b0) ^ sw)) = o;
+                    x[k][4 * h] -= __uint_as_float(o.x << 16);
+                    x[k][4 * h + 1] -= __uint_as_float(o.x & 0xFFFF0000u);
+                    x[k][4 * h + 2] -= __uint_as_float(o.y << 16);
+                    x[k][4 * h + 3] -= __uint_as_float(o.y & 0xFFFF0000u);
+                }
+            }
+            if (!it.paired) {   // the rest of the rounding
+#pragma unroll
+                for (int k = 0; k < kGroup; ++k) {
+                    const int sw = ((i0 & 7) + k) << 4;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        *reinterpret_cast<uint2 *>(dst + C::kTileBytes + k * 128 + ((h ? b1 : b0) ^ sw)) =
+                            make_uint2(pack_bf16(x[k][4 * h], x[k][4 * h + 1]),
+                                       pack_bf16(x[k][4 * h + 2], x[k][4 * h + 3]));
+                }
+            }
+        }
+        if (!waited) {   // (no row of this warp: the operand's phases are kept in step all the same)
+            if (!warp_all(kv_wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort))) return false;
+            if (!it.paired && !warp_all(kv_wait(&ms->q_empty[1], (n - 1) & 1, &ms->abort))) return false;
+        }
         fence_proxy_async_smem();
         mbar_arrive_warp(&ms->q_full[s]);
         if (!it.paired) mbar_arrive_warp(&ms->q_full[1]);
