@@ -254,6 +254,15 @@ __host__ __device__ inline int attend_max_chunks(long long n) {
 }
 
 // ---------------------------------------------------------------- dense paged layers
+// Integer division out of line on the device: a divisor that the compiler does
+// not know costs some 30 instructions each time it is written, and code that runs once per item
+// or launch is paid for by the instruction (it comes from L2).
+#ifdef __CUDA_ARCH__
+static __device__ __noinline__ int kv_div(int a, int b) { return a / b; }
+#else
+inline int kv_div(int a, int b) { return a / b; }
+#endif
+
 // A kernel's dynamic shared memory beyond the default, allowed once per device.
 struct KvSmemOnce {
     std::atomic<unsigned long long> done{0};   // by device
@@ -370,7 +379,7 @@ __host__ __device__ inline KvRange kv_range(const KvPlan &p, int pos0, int i, in
     KvRange g;
     const int r0 = p.kind == kKvPaired ? 256 * i : 0, rows_left = p.rows - r0;
     const int n = rows_left < 256 ? rows_left : 256;
-    const int first = r0 / p.G, last = (r0 + n - 1) / p.G;
+    const int first = kv_div(r0, p.G), last = kv_div(r0 + n - 1, p.G);
     g.k_lo = window > 0 && pos0 + first - window + 1 > 0 ? pos0 + first - window + 1 : 0;
     g.k_hi = pos0 + last + 1;
     g.lo = g.k_lo / CSLA_PAGE_TOKENS;
@@ -381,8 +390,8 @@ __host__ __device__ inline KvRange kv_range(const KvPlan &p, int pos0, int i, in
         if (n <= 128) {
             g.lo1 = g.hi;
         } else {
-            g.hi0 = (pos0 + (r0 + 127) / p.G) / CSLA_PAGE_TOKENS + 1;
-            const int lo = window > 0 ? pos0 + (r0 + 128) / p.G - window + 1 : 0;
+            g.hi0 = (pos0 + kv_div(r0 + 127, p.G)) / CSLA_PAGE_TOKENS + 1;
+            const int lo = window > 0 ? pos0 + kv_div(r0 + 128, p.G) - window + 1 : 0;
             g.lo1 = lo > 0 ? lo / CSLA_PAGE_TOKENS : 0;
         }
     }
@@ -398,30 +407,30 @@ __host__ __device__ inline KvPlan kv_plan(int T, int L, int G, int HK, int windo
     // key tiles of the longest row tile (with a window: an upper bound)
     int nt = (L - 1) / CSLA_PAGE_TOKENS + 1;
     if (window > 0 && window < L) {
-        const int w = (window - 2 + (p.kind == kKvPaired ? 256 / G + 1 : T) + CSLA_PAGE_TOKENS) / CSLA_PAGE_TOKENS + 1;
+        const int w = (window - 2 + (p.kind == kKvPaired ? kv_div(256, G) + 1 : T) + CSLA_PAGE_TOKENS) / CSLA_PAGE_TOKENS + 1;
         nt = w < nt ? w : nt;
     }
     // chunks: kv_units items in all at most, kv_min_tiles tiles at least, of even sizes
     // (32-bit divisions only: this runs ahead of every item's first load)
-    int n = (int)(kv_units(p.kind) / (unsigned)(HK * p.R));
+    int n = kv_div(kv_units(p.kind), HK * p.R);
     const int fit = nt / kv_min_tiles(p.kind, D, nt);
     if (p.kind == kKvSingle && n > fit && n / 2 * 12 <= nt && n / 2 > fit)
         n /= 2;   // one round over the SMs with chunks of 12 to 16 tiles rather than less than one
     else
         n = n < fit ? n : fit;
     const bool many = HK * p.R >= kv_units(p.kind);
-    int c = n > 1 ? (nt + n - 1) / n : nt;
+    int c = n > 1 ? kv_div(nt + n - 1, n) : nt;
     p.Rs = p.kind == kKvSingle || c < nt ? p.R : 0;
     if (p.kind == kKvPaired && many && (window == 0 || window >= L) && L - T >= T) {
         // more row tiles than SMs, all of about nt tiles
-        const int sms = kv_units(kKvPaired), left = HK * p.R % sms, cuts = left ? sms / left : 1;
+        const int sms = kv_units(kKvPaired), left = HK * p.R % sms, cuts = left ? kv_div(sms, left) : 1;
         if (cuts > 1 && nt >= 32 && HK * p.R < 16 * sms) {
-            p.Rs = (left + HK - 1) / HK;
-            c = (nt + (cuts < 4 ? cuts : 4) - 1) / (cuts < 4 ? cuts : 4);
+            p.Rs = kv_div(left + HK - 1, HK);
+            c = kv_div(nt + (cuts < 4 ? cuts : 4) - 1, cuts < 4 ? cuts : 4);
         }
     }
     p.c = c;
-    p.nch = p.Rs ? (nt + c - 1) / c : 1;
+    p.nch = p.Rs ? kv_div(nt + c - 1, c) : 1;
     p.rows_s = p.Rs == p.R ? p.rows : 256 * p.Rs;
     // K and V of all heads below half of L2: heads in turn, longest row tiles first
     p.heads_inside = (long long)L * HK * D * 4 <= (64ll << 20);
@@ -432,7 +441,7 @@ __host__ __device__ inline int kv_items(const KvPlan &p, int HK) { return HK * (
 // Partials of a row of row tile i (keys g): 1 means it is written out at once.
 __host__ __device__ inline int kv_parts(const KvPlan &p, const KvRange &g, int i) {
     if (i >= p.Rs) return 1;
-    const int nt = g.hi - g.lo, n = (nt + p.c - 1) / p.c;
+    const int nt = g.hi - g.lo, n = kv_div(nt + p.c - 1, p.c);
     return p.kind == kKvSingle && nt > 1 ? 2 * n : n;
 }
 // Partial rows that a request may need (rows_s of each part and head).

@@ -96,18 +96,20 @@ __device__ __forceinline__ bool make_item(const KvAttendArgs &a, const KvReq &r,
     int i, hk, j = 0, n = a.HK * (p.R - p.Rs), top = p.R - 1, tiles = p.R - p.Rs;   // whole row tiles first
     if (local >= n) {
         local -= n;
-        j = local % p.nch;
-        local /= p.nch;
+        const int x = kv_div(local, p.nch);
+        j = local - x * p.nch;
+        local = x;
         top = p.Rs - 1;
         tiles = p.Rs;
     }
     const bool cut = top < p.Rs;
     if (p.heads_inside) {
-        hk = local % a.HK;
-        i = top - local / a.HK;
+        const int x = kv_div(local, a.HK);
+        hk = local - x * a.HK;
+        i = top - x;
     } else {
-        i = top - local % tiles;
-        hk = local / tiles;
+        hk = kv_div(local, tiles);
+        i = top - (local - hk * tiles);
     }
     const KvRange g = kv_range(p, r.L - r.T, i, a.window);
     const int lo = g.lo + j * p.c, hi = cut ? min(g.hi, lo + p.c) : g.hi;
@@ -671,10 +673,14 @@ __device__ void softmax_role(const KvAttendArgs &a, uint8_t *smem, Misc *ms, int
                 mbar_arrive_warp(&ms->s_free[s]);
                 if (cut) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 4; ++c) {
+                        // bit i: column 32 c + i is visible
+                        const uint32_t below = last < 32 * c ? 0u : (last >= 32 * c + 31 ? ~0u : (2u << (last - 32 * c)) - 1u);
+                        const uint32_t above = from <= 32 * c ? ~0u : (from > 32 * c + 31 ? 0u : ~0u << (from - 32 * c));
+                        const uint32_t see = below & above;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (32 * c + i > last || 32 * c + i < from) v[c][i] = 0xFF800000u;
+                        for (int i = 0; i < 32; ++i) v[c][i] = see >> i & 1 ? v[c][i] : 0xFF800000u;
+                    }
                 }
                 float mx[4];
 #pragma unroll
@@ -948,7 +954,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(const __grid_c
     for (int u0 = blockIdx.x * per; u0 < units; u0 += gridDim.x * per) {
         const int u = block ? u0 : u0 + warp;   // row of the partials, head by head
         if (u >= units) break;
-        const int hk = u / rq.rows_s, r = u - hk * rq.rows_s, t = r / G, hq = hk * G + r - t * G;
+        const int hk = kv_div(u, rq.rows_s), r = u - hk * rq.rows_s, t = kv_div(r, G), hq = hk * G + r - t * G;
         const int parts = rq.parts ? rq.parts : kv_parts(p, kv_range(p, rq.L - rq.T, r / 256, a.window), r / 256);
         if (parts <= 1) continue;
         const long long pr = rq.base + u;

@@ -127,13 +127,13 @@ __device__ void producer(const KvAttendArgs &a, const CUtensorMap &km, const CUt
         Item it;
         it.end = !more;
         if (more && lane == src) {
-            const int j = local % w.p.nch;
+            const int head = kv_div(local, w.p.nch), j = local - head * w.p.nch;
             const KvRange g = kv_range(w.p, w.r.L - w.r.T, 0, a.window);
             it.n0 = w.r.n0;
             it.T = w.r.T;
             it.pos0 = w.r.L - w.r.T;
             it.slot = w.r.slot;
-            it.hk = local / w.p.nch;
+            it.hk = head;
             it.rows = w.p.rows;
             it.lo = g.lo + j * w.p.c;
             it.hi = min(g.hi, it.lo + w.p.c);   // (with a window the last chunk may be empty)
