@@ -731,6 +731,7 @@ int csla_kv_append(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
     const int64_t width = (int64_t)cfg->HK * cfg->D;
     if (!kv_rows_ok(k_new, k_stride, width, dtype) || !kv_rows_ok(v_new, v_stride, width, dtype)) return CSLA_ERR_ARG;
     a.D = cfg->D; a.HK = cfg->HK; a.d_rope = cfg->d_rope; a.pairs = cfg->rope_pairs; a.eps = cfg->eps;
+    a.inv_hk = (65536 + cfg->HK - 1) / cfg->HK;
     a.freq = kv_freq(cfg->rope_theta, cfg->d_rope);
     a.k_new = k_new; a.v_new = v_new; a.k_stride = k_stride; a.v_stride = v_stride; a.gamma_k = gamma_k;
     a.k = static_cast<uint16_t *>(kv->k); a.v = static_cast<uint16_t *>(kv->v);

@@ -310,6 +310,7 @@ struct KvBatch {
 struct KvAppendArgs {
     KvBatch bt;
     int D, HK, d_rope, pairs;
+    int inv_hk;                     // 2^16 / HK, rounded up
     float eps;
     KvFreq freq;
     const void *k_new, *v_new;

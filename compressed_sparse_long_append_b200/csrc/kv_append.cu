@@ -55,8 +55,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) kv_append_kernel(const __gr
     const RowLane rl = row_lane<D>(c, a.d_rope, a.pairs);
     if (tid < kMaxTok) s_cnt[tid] = 0;
     if (tid < half) s_turn[tid] = a.freq.turn[tid];
-    const int dt = kRows / a.HK, dh = kRows % a.HK;
-    const RowPos start{tid / kLanes / a.HK, tid / kLanes % a.HK};
+    // (row / HK of the at most 32 rows of a pass, HK <= 1024: exact)
+    const int dt = kRows * a.inv_hk >> 16, dh = kRows - dt * a.HK, row = tid / kLanes, t0 = row * a.inv_hk >> 16;
+    const RowPos start{t0, row - t0 * a.HK};
     pdl_wait();
     CSLA_TL_WAITED();
 
@@ -111,10 +112,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) kv_append_kernel(const __gr
 #pragma unroll
     for (int i = 0; i < 8; ++i) g[i] = a.gamma_k ? a.gamma_k[i < 4 ? rl.d0 + i : rl.d1 + i - 4] : 1.f;
     __syncthreads();
-    for (int i = tid; i < nt * half; i += kThreads) {
-        const int t = i / half, p = i - t * half;
-        s_cs[t][p] = kv_cos_sin(s_pos[t], s_turn[p]);
-    }
+    if (tid % (D / 2) < half)
+        for (int t = tid / (D / 2); t < nt; t += kThreads / (D / 2))
+            s_cs[t][tid % (D / 2)] = kv_cos_sin(s_pos[t], s_turn[tid % (D / 2)]);
     __syncthreads();
 
     auto store = [&](uint16_t *pool, const RowPos &p, const float (&y)[8]) {
