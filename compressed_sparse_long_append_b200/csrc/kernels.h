@@ -292,8 +292,10 @@ inline KvFreq kv_freq(float theta, int d_rope) {
     KvFreq f{};
     if (d_rope <= 0) return f;
     const long double ratio = expl(-2.0L / d_rope * logl((long double)theta));
-    long double x = 18446744073709551616.0L / 6.283185307179586476925286766559L;   // 2^64 / 2 pi
-    for (int i = 0; i < d_rope / 2 && i < 64; ++i, x *= ratio) f.turn[i] = x < 18446744073709551615.0L ? (unsigned long long)x : 0;
+    const long double whole = 18446744073709551616.0L;   // 2^64: one turn
+    long double x = whole / 6.283185307179586476925286766559L;
+    for (int i = 0; i < d_rope / 2 && i < 64; ++i, x *= ratio)
+        f.turn[i] = (unsigned long long)(x < whole ? x : fmodl(x, whole));   // (theta below 1: turns of more than one)
     return f;
 }
 

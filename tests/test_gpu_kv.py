@@ -49,6 +49,19 @@ def test_append_long_chunk_far_positions_and_many_requests():
     assert bool(((b.lb.k.double() - k).abs()[hit] <= tol[hit]).all()) and bool(torch.isnan(b.lb.k[~hit]).all())
 
 
+@pytest.mark.parametrize("theta", [2.0 ** -7, 1.0, 1.5])
+def test_small_rotation_bases(theta):
+    """A base below 1 makes the later pairs the faster ones, past a whole turn per position."""
+    for pairs in (ADJ, HALF):
+        b = Batch(DenseShape(D=64, HQ=4, HK=2, d_rope=64, rope_pairs=pairs, theta=theta), [300, 2], [900, 300], seed=60)
+        k, tol, v, hit = b.expected_append()
+        b.append()
+        assert bool(((b.lb.k.double() - k).abs()[hit] <= tol[hit]).all())
+        b.fill()
+        b.check_attend(b.attend(F32))
+    no_device_error()
+
+
 def test_append_keeps_special_values():
     shape = DenseShape(D=64, HQ=1, HK=1, d_rope=0)
     b = Batch(shape, [4], [6], norm=False)
