@@ -738,6 +738,10 @@ int csla_kv_append(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
     return cuda_status(launch_kv_append(a, dtype == CSLA_BF16, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// Longest context of an attention call: a row tile's keys (2^20 tiles of less
+// than a microsecond) have to end well inside the 2 s bound of the kernels' waits.
+constexpr int32_t kKvMaxLen = 1 << 27;
+
 // Key tiles that a row tile may have, at most.
 static long long kv_most_tiles(const csla_kv_cfg *c, int max_new, int max_len) {
     long long nt = ((long long)max_len + CSLA_PAGE_TOKENS - 1) / CSLA_PAGE_TOKENS;
@@ -801,8 +805,8 @@ static void kv_workspace_parts(uint8_t *ws, int B, long long rows, KvAttendArgs 
 }
 
 size_t csla_kv_workspace_size(const csla_kv_cfg *cfg, int32_t B, int32_t N, int32_t max_new, int32_t max_len) {
-    if (check_kv_cfg(cfg) != CSLA_OK || B < 1 || B > 65535 || N < 1 || max_new < 1 || max_len < 1 ||
-        max_len > (1 << 30))
+    if (check_kv_cfg(cfg) != CSLA_OK || B < 1 || B > 65535 || N < 1 || N > (1 << 30) || max_new < 1 || max_len < 1 ||
+        max_len > kKvMaxLen)
         return 0;
     return kv_workspace_bytes(cfg, B, kv_most_part_rows(cfg, B, N, max_new, max_len, 0));
 }
@@ -818,7 +822,7 @@ int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
     if (rc) return rc;
     if (!kv_rows_ok(q, q_stride, (int64_t)cfg->HQ * cfg->D, q_dtype)) return CSLA_ERR_ARG;
     if (!out || !aligned16(out) || (out_dtype != CSLA_F32 && out_dtype != CSLA_BF16)) return CSLA_ERR_ARG;
-    if (max_new < 1 || max_len < 1 || max_len > (1 << 30) || (!q_start && a.bt.T > max_new)) return CSLA_ERR_ARG;
+    if (max_new < 1 || max_len < 1 || max_len > kKvMaxLen || (!q_start && a.bt.T > max_new)) return CSLA_ERR_ARG;
     if ((long long)kv->n_pages * cfg->HK * CSLA_PAGE_TOKENS >= (1ll << 31) || (long long)N * cfg->HQ >= (1ll << 31))
         return CSLA_ERR_UNSUPPORTED;
     const size_t need = csla_kv_workspace_size(cfg, B, N, max_new, max_len);

@@ -497,11 +497,11 @@ int csla_cp_place(const csla_cfg *cfg, const csla_state *st, const csla_cache *c
  *     csla_compress_append of the same tokens serves too); neither call
  *     writes it, so both may be repeated.
  *
- * A call covers B requests (slots as above) and N new tokens in one ragged
- * row block: request b owns rows q_start[b] .. q_start[b+1]-1 (T_b of them,
- * 0 allowed: its slot is not looked at), its i-th new token at position
- * p = len[slots[b]] - T_b + i; rows from q_start[B] on belong to nobody and
- * are left alone (N may be a capacity).
+ * A call covers B <= 65535 requests (slots as above) and N <= 2^30 new
+ * tokens in one ragged row block: request b owns rows q_start[b] ..
+ * q_start[b+1]-1 (T_b of them, 0 allowed: its slot is not looked at), its
+ * i-th new token at position p = len[slots[b]] - T_b + i; rows from
+ * q_start[B] on belong to nobody and are left alone (N may be a capacity).
  * q_start NULL: every request has N / B new tokens (N divisible by B).
  * Rows are `stride` elements apart (a slice of a fused projection is fine),
  * heads contiguous inside a row; base addresses 16-byte aligned, strides
@@ -514,9 +514,9 @@ int csla_cp_place(const csla_cfg *cfg, const csla_state *st, const csla_cache *c
  * Device-detected errors: a slot outside [0, n_slots), or q_start not
  * ascending within [0, N] (CSLA_DEVERR_INDEX), or len outside
  * [T_b, 128*bt_stride], or (attention) len above max_len or T_b above
- * max_new (CSLA_DEVERR_LEN): the request is skipped, its outputs untouched.  A page
- * id outside the pool (CSLA_DEVERR_PAGE): the append skips the tokens in
- * it, the attention treats them as masked.
+ * max_new (CSLA_DEVERR_LEN): the request is skipped, its outputs untouched.
+ * A page id outside the pool (CSLA_DEVERR_PAGE): the append skips the
+ * tokens in it, the attention treats them as masked.
  */
 enum { CSLA_ROPE_ADJACENT = 0, CSLA_ROPE_HALVES = 1 };
 
@@ -576,13 +576,13 @@ int csla_kv_append(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
  * not must be finite for the others too (it enters with weight zero).
  *   q [N][HQ][D] q_dtype, rows q_stride elements apart; sink f32 [HQ] or
  *   NULL; gamma_q f32 [D] or NULL; out [N][HQ][D] out_dtype, 16-byte aligned.
- *   max_new >= every T_b, max_len >= every len (host bounds; max_len <= 2^30).
+ *   max_new >= every T_b, max_len >= every len (host bounds; max_len <= 2^27).
  * Batch invariant: how a request is split and joined is a function of its
  * own T_b and len and of the layer's shape.
  * workspace: csla_kv_workspace_size(cfg, B, N, max_new, max_len) bytes,
  * 16-byte aligned, not shared with a call that may run at the same time.
- * Errors: CSLA_ERR_ARG, CSLA_ERR_UNSUPPORTED (shapes; n_pages*HK*128 >=
- * 2^31); device bits INDEX, LEN, PAGE.
+ * Errors: CSLA_ERR_ARG, CSLA_ERR_UNSUPPORTED (shapes; n_pages*HK*128 or
+ * N*HQ >= 2^31); device bits INDEX, LEN, PAGE.
  */
 int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_t *slots, int32_t B,
                    const int32_t *q_start, int32_t N, int32_t max_new, int32_t max_len, const void *q,

@@ -109,7 +109,9 @@ def test_workspace_is_checked():
         assert _attend(cfg, wsb=need - 1, **bad) == C.CSLA_ERR_ARG
         assert _attend(cfg, ws=None, **bad) == C.CSLA_ERR_ARG
         assert _attend(cfg, ws=FAKE + 8, **bad) == C.CSLA_ERR_ARG
-    for args in ((0, 1, 1, 1), (1, 0, 1, 1), (1, 1, 0, 1), (1, 1, 1, 0)):
+    assert _attend(cfg, N=2, mn=1, ml=(1 << 27) + 1) == C.CSLA_ERR_ARG   # longer than a call may be
+    assert C.csla_kv_workspace_size(cfg, 2, 2, 1, 1 << 27) > 0
+    for args in ((0, 1, 1, 1), (1, 0, 1, 1), (1, 1, 0, 1), (1, 1, 1, 0), (1, 1, 1, (1 << 27) + 1), (1, (1 << 30) + 1, 1, 9000)):
         assert C.csla_kv_workspace_size(cfg, *args) == 0
 
 
