@@ -255,8 +255,8 @@ __host__ __device__ inline int attend_max_chunks(long long n) {
 
 // ---------------------------------------------------------------- dense paged layers
 // Integer division out of line on the device: a divisor that the compiler does
-// not know costs some 30 instructions each time it is written, and code that runs once per item
-// or launch is paid for by the instruction (it comes from L2).
+// not know costs some 30 instructions each time it is written, and code that
+// runs once per item or launch is paid for by the instruction (it comes from L2).
 #ifdef __CUDA_ARCH__
 static __device__ __noinline__ int kv_div(int a, int b) { return a / b; }
 #else

@@ -8,12 +8,15 @@
 // each token's page once, and evaluates the rotation's cosines and sines once
 // per token and pair in shared memory; then D/8 lanes move one (token, head)
 // row, 16 or 32 bytes per lane: the K rows of its tokens, then the V rows (a
-// copy), four rows of a thread at a time and the next four in flight.
+// copy), two rows of a thread at a time and the next two in flight.
 // The bytes bound a long call (each row read once and written once) and leave
 // about 170 instructions per warp for two rows, so a thread's (token, head) is
-// carried from row to row, not divided out.  Short calls are bound by the
+// carried from row to row, not divided out: 8192 tokens of 8 heads x 128 take
+// 16.0 us for 67 MB, 4.2 TB/s or 0.64 of a plain copy's rate, with instruction issue
+// 64 % busy (norm and rotation) and one round of blocks, whose start and end
+// are not overlapped by another.  Short calls are bound by the
 // chain offsets -> slot -> length -> page, which runs while the first rows'
-// loads are in flight.
+// loads are in flight, and by the call itself on the host (about 7 us).
 #include "kv.cuh"
 
 namespace csla {

@@ -1,5 +1,6 @@
 // kv_attend.cu -- attention of new tokens over the dense paged cache
-// (csla_kv_attend).
+// (csla_kv_attend): requests of more than 16 rows per KV head (shorter ones
+// are kv_few.cu's), and the join of rows whose keys were cut.
 //
 //   s_j = scale <R(p) norm(q), K_j>,  o = sum_j e^{s_j} V_j / (e^{sink} + sum_j e^{s_j})
 //
@@ -7,32 +8,50 @@
 // make T*G rows of one matrix (row = token * G + head): they share every key.
 // A page (128 tokens of one KV head) is one tile of keys and values.
 //
-// Work.  A CTA works on items.  A request of at most 128 rows per KV head
-// (decode, a few tokens) is one row tile, its keys cut into chunks of tiles;
-// one item is a chunk, and the CTA's two streams take its tiles in turn.  A
-// request of more rows is cut into row tiles of 256; one item is such a tile
-// (and a chunk of its keys when there are few row tiles), each stream
-// takes 128 of the rows and both share every key tile.  How a request is cut depends
-// on its own T and len and the layer's shape alone (kv_plan), so its
-// results do not depend on the batch.  Rows whose keys were cut are left as
-// partial (m, l, O) in the workspace and joined, in order, by kv_join_kernel.
+// Work.  A CTA works on items.  A request of 17 to 128 rows per KV head is
+// one row tile, its keys cut into chunks of tiles; one item is a chunk, and
+// the CTA's two streams take its tiles in turn.  A request of more rows is
+// cut into row tiles of 256; one item is such a tile (and a chunk of its keys
+// when there are few row tiles), each stream takes 128 of the rows and both
+// share every key tile.  How a request is cut depends on its own T and len
+// and the layer's shape alone (kv_plan), so its results do not depend on the
+// batch.  Rows whose keys were cut are left as partial (m, l, O) in the
+// workspace and joined, in order, by kv_join_kernel.
 //
 // Roles (one persistent CTA per SM, 16 warps):
 //   warps 0-3, 4-7  softmax of stream 0, 1: a thread per row; a running maximum
-//                   and sum in fp32, P in bf16 back to tensor memory; O is rescaled only when the
-//                   maximum has grown by more than 2^8 (kept exact: the
-//                   reference maximum of a row is whatever its weights were formed with);
-//   warps 8-11      Q: norm and rotation in fp32, rounded to bf16 into the swizzled operand;
-//                   a row tile of few rows keeps the rounding's rest as a second bf16
-//                   operand (its product costs what memory-bound items have to spare);
+//                   and sum in fp32, P in bf16 back to tensor memory.  O is
+//                   rescaled only when the maximum has grown by more than 2^8:
+//                   a row's weights are all formed with one reference, so any
+//                   reference cancels in O / sum, and 2^8 keeps both in range;
+//   warps 8-11      Q: norm and rotation in fp32, rounded to bf16 into the
+//                   swizzled operand;
 //   warp 12         tcgen05.mma S = Q K^T;
 //   warp 13         TMA: K and V tiles into a ring each;
 //   warp 14         the items: walks the batch 32 requests at a time;
 //   warp 15         tcgen05.mma O += P V (P from tensor memory).
 // Tensor memory (512 columns): O of both streams 256, P of both 128, and one S
-// of 128 that the streams use in turn.  A softmax thread takes its whole row of S
-// into registers at once, so the S columns are free for the other stream's
+// of 128 that the streams use in turn.  A softmax thread takes its whole row of
+// S into registers at once, so the S columns are free for the other stream's
 // scores while it forms its weights, and a stream's next scores wait for it.
+//
+// Roundings.  P is rounded to bf16 (half a step of each weight; their sum is
+// of the unrounded ones).  The rotated query is rounded to bf16: a row tile
+// of 17 to 128 rows keeps the rounding's rest as a second bf16 operand (its S
+// costs twice, which an item bound by its keys' bytes has to spare), a row tile of
+// 256 has neither the shared memory for it nor tensor time to spare (half again
+// as many products), so its scores carry half a bf16 step of the query.
+//
+// Bound and measured (32 query and 8 KV heads of 128 dims, unless said).
+// Row tiles of 256 are bound by the tensor cores and, beside them, by the
+// exponentials (16 per clock and SM: 128 x 128 take 1024 clocks, the tile's
+// products 1024 too): 4096 tokens after 16384 (4 KV heads) take 1.09 ms, 1.13 PFLOP/s, 0.69
+// of what one large library product measures in a burst; at that length the
+// clock falls to about 1.4 GHz under the power limit.  2048 tokens alone: 59 us
+// (0.36; 64 row tiles of unequal length on 148 SMs).  One chunk of 17 to 128
+// rows is bound by its stream of K and V: 32 requests of 20 rows 138 us for
+// 526 MB (3.8 TB/s), 4 requests of 64 rows on one KV head over 262144
+// tokens 154 us for 537 MB (3.5 TB/s).
 #include "kv.cuh"
 
 namespace csla {
@@ -903,10 +922,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
 // one of many is a block's, a range of parts per warp, the warps' sums added
 // in order (a long context of one KV head leaves hundreds of parts on a few
 // rows: 4 rows x 64 heads x 256 parts took 75 us with a warp per row).
+// Bound by the partials' bytes, which the attention has just left in L2: 8
+// requests of 16384 tokens and 32 heads, 10.0 us beside 94 us of attention.
 constexpr int kJoinWarps = 8, kJoinFew = 32;
 
 // o += sum of 2^(m_i - top) O_i over parts [i0, i1), (m, l) of part i0 + i in
-// lane i's ml (i1 - i0 <= 32).  The parts' loads are issued eight at a time, ahead of their weights.
+// lane i's ml (i1 - i0 <= 32).  The parts' loads are issued eight at a time,
+// ahead of their weights.
 template <int D>
 __device__ __forceinline__ void join_parts(const float *part_o, long long pr, long long step, int n, float w, float (&o)[D / 32]) {
     constexpr int kDims = D / 32;

@@ -1,23 +1,33 @@
 // kv_few.cu -- attention of requests of few rows (up to 16 per KV head:
-// decode) over the dense paged cache: a part of
-// csla_kv_attend.
+// decode) over the dense paged cache: a part of csla_kv_attend.
 //
 //   s_j = scale <R(p) norm(q), K_j>,  o = sum_j e^{s_j} V_j / (e^{sink} + sum_j e^{s_j})
 //
-// Each K and V byte is used by at most 16 rows, so the kernel is bound by
-// HBM and by how much of it is asked for at a time; the products are small.  So
-// they stay in registers: mma.sync on 16-row fragments needs no tensor memory, no handing
-// over between roles and no padding to 128 rows, and its rate is several times what the bytes leave time for.
+// Each K and V byte is used by at most 16 rows, so the kernel is bound by HBM
+// and by how much of it is asked for at a time; the products are small.  So
+// they stay in registers: mma.sync on 16-row fragments needs no tensor
+// memory, no handing over between roles and no padding to 128 rows, and its
+// rate is several times what the bytes leave time for.
 //
 // An item is a chunk of pages of one (request, KV head).  Two persistent CTAs
-// per SM; a CTA's producer warp walks the batch and streams K and V stages (16 KB each)
-// by TMA into a ring, across items; four consumer warps each take
-// a quarter of the stage's tokens with a running maximum m, sum l and O of their own:
+// per SM; a CTA's producer warp walks the batch and streams K and V stages
+// (16 KB each) by TMA into a ring, across items; four consumer warps each
+// take a quarter of the stage's tokens with a running maximum m, sum l and O
+// of their own:
 //   S = Q K^T (Q as two bf16 terms: the rounding of the rotated query is kept),
-//   P = 2^(S - m) straight from the accumulators into the A operand of O += P V.
+//   P = 2^(S - m) straight from the accumulators into the A operand of O += P V
+//       (rounded to bf16, half a step of each weight).
 // At the end of an item the four (m, l, O) are joined through shared memory in
 // a fixed order and written out, or left as a partial for kv_join_kernel
 // when the request's keys were cut.
+//
+// Measured (8 KV heads of 128 dims, 4 or 8 query heads each, join included): 8 requests
+// of 131072 tokens 658 us for 4.29 GB, 6.53 TB/s or 0.995 of a plain copy's
+// rate; 64 ragged requests of 1 to 32768 tokens 142 us for 757 MB (5.3 TB/s: the last
+// items' latency and the join); a window of 1024 in 32 requests (64 dims, 16 KV
+// heads) 34 us for 131 MB.  One request of 901 tokens: 12 us, a chain
+// of two launches and one item's latency.  The same items in the tensor-memory
+// kernel took 1.17 ms, 156 us and 47 us.
 #include "kv.cuh"
 
 namespace csla {
