@@ -21,13 +21,14 @@
 // a fixed order and written out, or left as a partial for kv_join_kernel
 // when the request's keys were cut.
 //
-// Measured (8 KV heads of 128 dims, 4 or 8 query heads each, join included): 8 requests
-// of 131072 tokens 658 us for 4.29 GB, 6.53 TB/s or 0.995 of a plain copy's
-// rate; 64 ragged requests of 1 to 32768 tokens 142 us for 757 MB (5.3 TB/s: the last
-// items' latency and the join); a window of 1024 in 32 requests (64 dims, 16 KV
-// heads) 34 us for 131 MB.  One request of 901 tokens: 12 us, a chain
-// of two launches and one item's latency.  The same items in the tensor-memory
-// kernel took 1.17 ms, 156 us and 47 us.
+// Measured (8 KV heads of 128 dims, 4 or 8 query heads each, join included): 8
+// requests of 131072 tokens 636 us for 4.29 GB, 6.75 TB/s or 1.03 of a plain
+// copy's rate (which writes half of its bytes); 64 ragged requests of 1 to 32768 tokens
+// 134 us for 757 MB (5.6 TB/s: the last items' latency and the join); a window of
+// 1000 in 32 requests (64 dims, 16 KV heads) 31.6 us for 131 MB.  One request
+// of 901 tokens: 11.6 us, a chain of two launches and one item's latency.  The
+// same items in the tensor-memory kernel took 1.17 ms, 156 us and 47 us;
+// rows as rows only (no narrow_item) 657 us, 141 us and 36 us.
 #include "kv.cuh"
 
 namespace csla {
@@ -36,6 +37,7 @@ namespace {
 constexpr int kConsumers = 4;   // warps, a quarter of a stage's tokens each
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kRows = 16;       // of an item
+constexpr int kNarrow = 8;      // rows up to which the products are taken with the rows as columns
 constexpr int kItems = 4;
 constexpr int kMaxStages = 6;
 
@@ -49,11 +51,12 @@ struct Cfg {
     static constexpr int kStages = 6;
     static constexpr int kWT = kTok / kConsumers;         // tokens of a stage per warp
     static constexpr int kOut = kRows * D * 2;           // half the dims of one warp's O
-    // work area: the Q terms [2][16][D] bf16; at an item's end half of two O, and their (m, l)
+    // work area: the Q terms [2][16][D] bf16; at an item's end half of two O, or
+    // three whole O of up to 8 rows, and their (m, l)
     static constexpr int kOffWork = kStages * kStage;
     static constexpr int kMl = 32 * 16;                  // (m, l) of both row groups, per lane
-    static constexpr int kOffMl = kOffWork + 2 * kOut;
-    static constexpr int kOffMisc = kOffMl + 2 * kMl;
+    static constexpr int kOffMl = kOffWork + 3 * kOut;
+    static constexpr int kOffMisc = kOffMl + 3 * kMl;
 };
 
 struct Item {
@@ -198,13 +201,15 @@ __device__ void producer(const KvAttendArgs &a, const CUtensorMap &km, const CUt
 }
 
 // ---------------------------------------------------------------- consumers
-// Q rows of the item as two bf16 terms, rows of 2D bytes, 16-byte chunk ^ (row & 7).
+// Q rows of the item as two bf16 terms, rows of 2D bytes, 16-byte chunk ^ (row & 7):
+// the terms 16 rows apart, or in rows r and r + 8 of one operand (up to 8 rows).
 template <int D, bool QBF16>
 __device__ void stage_q(const KvAttendArgs &a, const Item &it, uint8_t *qs, const Misc *ms) {
     constexpr int kLanes = D / 8, kPer = 32 / kLanes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % kLanes, sub = lane / kLanes;
     const int G = a.HQ / a.HK;
     const RowLane rl = row_lane<D>(c, a.d_rope, a.pairs);
+    const int rest = (it.rows <= kNarrow ? kNarrow : kRows) * 2 * D;
 #pragma unroll 1
     for (int r0 = warp * kPer; r0 < it.rows; r0 += kConsumers * kPer) {
         const int r = min(r0 + sub, it.rows - 1), t = r / G;
@@ -228,13 +233,254 @@ __device__ void stage_q(const KvAttendArgs &a, const Item &it, uint8_t *qs, cons
                 uint8_t *p = qs + (r0 + sub) * 2 * D + ((byte & ~15) ^ ((r0 + sub) & 7) << 4) + (byte & 15);
                 const uint2 o = make_uint2(pack_bf16(x[4 * h], x[4 * h + 1]), pack_bf16(x[4 * h + 2], x[4 * h + 3]));
                 *reinterpret_cast<uint2 *>(p) = o;
-                *reinterpret_cast<uint2 *>(p + kRows * 2 * D) =
+                *reinterpret_cast<uint2 *>(p + rest) =
                     make_uint2(pack_bf16(x[4 * h] - __uint_as_float(o.x << 16), x[4 * h + 1] - __uint_as_float(o.x & 0xFFFF0000u)),
                                pack_bf16(x[4 * h + 2] - __uint_as_float(o.y << 16),
                                          x[4 * h + 3] - __uint_as_float(o.y & 0xFFFF0000u)));
             }
         }
     }
+}
+
+// An item of up to 8 rows.  The terms of Q are the two halves of one operand
+// (rows r and r + 8), kept in registers, so one product gives both terms'
+// scores; and P, as it lies in the accumulators of S, is the B operand of
+// O^T += V^T P^T: half the products, and half the sums, of 16 rows.
+//   S, P: row lane / 4, tokens 2 (lane % 4) + {0, 1} of each 8;
+//   o[i]: dims 16 i + lane / 4 (+ 8), rows 2 (lane % 4) + {0, 1}.
+// Returns false when a wait gave up; the barriers are passed all the same.
+template <int D, bool OBF16>
+__device__ __forceinline__ bool narrow_item(const KvAttendArgs &a, const Item &it, uint8_t *smem, Misc *ms, int &taken) {
+    using C = Cfg<D>;
+    constexpr int kNT = C::kWT / 8;   // 8-token tiles per warp and stage
+    constexpr int kDT = D / 16;       // 16-dim tiles of O
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mi = lane >> 3, mr = lane & 7;
+    const int tok0 = warp * C::kWT, G = a.HQ / a.HK;
+    const float sc = a.scale * kLog2e;
+    const uint32_t ring = smem_u32(smem), work = held(smem_u32(smem + C::kOffWork));
+    uint32_t q[D / 16][4];
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+        const int row = 8 * (mi & 1) + mr, ch = 2 * k + (mi >> 1);
+        ldsm(q[k], work + row * 2 * D + ((ch ^ (row & 7)) << 4));
+    }
+    const int row = lane >> 2;
+    const int pos = it.pos0 + min(row, it.rows - 1) / G, low = a.window > 0 ? pos - a.window + 1 : 0;
+    float m = -INFINITY, l = 0.f, o[kDT][4];
+#pragma unroll
+    for (int i = 0; i < kDT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+    // a row's value for the lanes that hold its column of O
+    auto column = [&](float x, int e) { return __shfl_sync(0xffffffffu, x, 8 * (lane & 3) + 4 * e); };
+    const int parts = (it.hi - it.lo) * C::kPer;
+    bool ok = true;
+#pragma unroll 1
+    for (int s = 0; s < parts; ++s) {
+        // ---- S
+        const int ks = taken % C::kStages;
+        ok = warp_all(kv_wait(&ms->full[ks], (taken / C::kStages) & 1, &ms->abort));
+        if (!ok) break;
+        ++taken;
+        const bool bad = ms->bad[ks];
+        const int t0 = it.lo * CSLA_PAGE_TOKENS + s * C::kTok + tok0;   // position of the warp's first token
+        float acc[kNT][2][4];   // (two chains of products)
+#pragma unroll
+        for (int j = 0; j < kNT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][0][e] = acc[j][1][e] = 0.f;
+        const uint32_t kb = held(ring + ks * C::kStage);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+            for (int j = 0; j < kNT / 2; ++j) {
+                uint32_t b[4];
+                const int tok = tok0 + 16 * j + 8 * (mi >> 1) + mr, ch = 2 * k + (mi & 1);
+                ldsm(b, kb + (ch >> 3) * C::kBlk + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
+                mma16816(acc[2 * j][k & 1], q[k], b[0], b[1]);
+                mma16816(acc[2 * j + 1][k & 1], q[k], b[2], b[3]);
+            }
+#pragma unroll
+        for (int j = 0; j < kNT; ++j) {
+            held(acc[j][0]);
+            held(acc[j][1]);
+        }
+        mbar_arrive_warp(&ms->empty[ks]);
+        // ---- both terms together, mask, maximum, P
+        float x[kNT][2];
+#pragma unroll
+        for (int j = 0; j < kNT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                x[j][e] = (acc[j][0][e] + acc[j][1][e]) + (acc[j][0][e + 2] + acc[j][1][e + 2]);
+        const int vs = taken % C::kStages;
+        const bool edge = bad || t0 + C::kWT > it.pos0 + 1 || t0 < it.k_lo + it.T;   // some row may not see some token
+        if (edge) {
+#pragma unroll
+            for (int j = 0; j < kNT; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int t = t0 + 8 * j + 2 * (lane & 3) + e;
+                    if (bad || t > pos || t < low) x[j][e] = -INFINITY;
+                }
+        }
+        float mn = fmaxf(x[0][0], x[0][1]);
+#pragma unroll
+        for (int j = 1; j < kNT; ++j) mn = fmaxf(mn, fmaxf(x[j][0], x[j][1]));
+        mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 1));
+        mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 2));
+        mn = fmaxf(m, mn * sc);
+        const bool grow = mn > m + kGrow;
+        if (__any_sync(0xffffffffu, grow)) {
+            const float f = !grow ? 1.f : (m == -INFINITY ? 0.f : ex2(m - mn));
+            if (grow) m = mn;
+            l *= f;
+            const float f0 = column(f, 0), f1 = column(f, 1);
+#pragma unroll
+            for (int i = 0; i < kDT; ++i) {
+                o[i][0] *= f0;
+                o[i][1] *= f1;
+                o[i][2] *= f0;
+                o[i][3] *= f1;
+            }
+        }
+        const float sub = m == -INFINITY ? 0.f : m;
+        uint32_t p[kNT];
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < kNT; ++j) {
+            const float p0 = ex2(fmaf(x[j][0], sc, -sub)), p1 = ex2(fmaf(x[j][1], sc, -sub));
+            sum += p0 + p1;
+            p[j] = pack_bf16(p0, p1);
+        }
+        l += sum;
+        // ---- O^T += V^T P^T
+        ok = warp_all(kv_wait(&ms->full[vs], (taken / C::kStages) & 1, &ms->abort));
+        if (!ok) break;
+        ++taken;
+        const uint32_t vb = held(ring + vs * C::kStage);
+#pragma unroll
+        for (int k = 0; k < kNT / 2; ++k) {
+            // tokens that no row sees count nothing, whatever they hold (0 * NaN is not 0)
+            uint32_t keep[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+            if (edge) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int t = t0 + 16 * k + 8 * h + 2 * (lane & 3);
+                    keep[h] = bad ? 0u
+                                  : (t >= it.k_lo && t < it.k_hi ? 0xFFFFu : 0u) |
+                                        (t + 1 >= it.k_lo && t + 1 < it.k_hi ? 0xFFFF0000u : 0u);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kDT; ++i) {
+                uint32_t v[4];
+                const int tok = tok0 + 16 * k + 8 * (mi >> 1) + mr, ch = 2 * i + (mi & 1);
+                ldsm_t(v, vb + (ch >> 3) * C::kBlk + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4));
+                if (edge) {
+                    v[0] &= keep[0];
+                    v[1] &= keep[0];
+                    v[2] &= keep[1];
+                    v[3] &= keep[1];
+                }
+                mma16816(o[i], v, p[2 * k], p[2 * k + 1]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kDT; ++i) held(o[i]);
+        mbar_arrive_warp(&ms->empty[vs]);
+    }
+
+    // ---- join the four token groups, in order, by the first warp
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    sync_consumers<kConsumers>();   // Q is in everyone's registers
+    if (warp > 0) {
+        float4 *buf = reinterpret_cast<float4 *>(smem + C::kOffWork + (warp - 1) * C::kOut);
+#pragma unroll
+        for (int i = 0; i < kDT; ++i) buf[i * 32 + lane] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+        reinterpret_cast<float2 *>(smem + C::kOffMl + (warp - 1) * C::kMl)[lane] = make_float2(m, l);
+    }
+    sync_consumers<kConsumers>();
+    if (warp > 0 || *(volatile int *)&ms->abort) return ok;
+    float mo[kConsumers], lo[kConsumers];
+    mo[0] = m;
+    lo[0] = l;
+#pragma unroll
+    for (int w = 1; w < kConsumers; ++w) {
+        const float2 y = reinterpret_cast<const float2 *>(smem + C::kOffMl + (w - 1) * C::kMl)[lane];
+        mo[w] = y.x;
+        lo[w] = y.y;
+        m = fmaxf(m, y.x);
+    }
+    const float base = m == -INFINITY ? 0.f : m;
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kConsumers; ++w) {
+        const float f = ex2(mo[w] - base), f0 = column(f, 0), f1 = column(f, 1);
+        l += lo[w] * f;
+        const float4 *buf = reinterpret_cast<const float4 *>(smem + C::kOffWork + (w - 1) * C::kOut);
+#pragma unroll
+        for (int i = 0; i < kDT; ++i) {
+            if (w == 0) {
+                o[i][0] *= f0;
+                o[i][1] *= f1;
+                o[i][2] *= f0;
+                o[i][3] *= f1;
+            } else {
+                const float4 y = buf[i * 32 + lane];
+                o[i][0] = fmaf(y.x, f0, o[i][0]);
+                o[i][1] = fmaf(y.y, f1, o[i][1]);
+                o[i][2] = fmaf(y.z, f0, o[i][2]);
+                o[i][3] = fmaf(y.w, f1, o[i][3]);
+            }
+        }
+    }
+    // two neighbouring dims of one row per lane: an even lane / 4 takes its first
+    // row's dims d, d + 1, an odd one its second row's d - 1, d
+    const bool odd = row & 1;
+    const int r = 2 * (lane & 3) + odd, d = row & 6;
+    auto pair = [&](float c0, float c1) {
+        const float got = __shfl_xor_sync(0xffffffffu, odd ? c0 : c1, 4);
+        return odd ? make_float2(got, c1) : make_float2(c0, got);
+    };
+    if (it.part >= 0) {
+        const long long first = it.base + ((long long)it.part * a.HK + it.hk) * it.rows;
+        if ((lane & 3) == 0 && row < it.rows) a.part_ml[first + row] = make_float2(m, l);
+        float *po = a.part_o + (first + r) * D + d;
+#pragma unroll
+        for (int i = 0; i < kDT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float2 y = pair(o[i][2 * h], o[i][2 * h + 1]);
+                if (r < it.rows) *reinterpret_cast<float2 *>(po + 16 * i + 8 * h) = y;
+            }
+    } else {
+        const int own = min(row, it.rows - 1), hq0 = it.hk * G + own % G;
+        const bool no = m == -INFINITY && l == 0.f;   // no token at all (scores that are all NaN leave l NaN)
+        const float sink = a.sink ? a.sink[hq0] * kLog2e : -INFINITY;
+        const float top = fmaxf(m, sink);
+        const float f = no ? 0.f : ex2(m - top);
+        const float w = no ? 0.f : f / fmaf(l, f, a.sink ? ex2(sink - top) : 0.f);
+        const float mine = __shfl_sync(0xffffffffu, w, 4 * r);
+        const bool none = __shfl_sync(0xffffffffu, (int)no, 4 * r);
+        const int t = min(r, it.rows - 1) / G, hq = it.hk * G + min(r, it.rows - 1) - t * G;
+        const long long at = ((long long)(it.n0 + t) * a.HQ + hq) * D + d;
+#pragma unroll
+        for (int i = 0; i < kDT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float2 y = pair(o[i][2 * h], o[i][2 * h + 1]);
+                y = none ? make_float2(0.f, 0.f) : make_float2(y.x * mine, y.y * mine);
+                if (r < it.rows) {
+                    if constexpr (OBF16)
+                        *reinterpret_cast<uint32_t *>(reinterpret_cast<uint16_t *>(a.out) + at + 16 * i + 8 * h) = pack_bf16(y.x, y.y);
+                    else
+                        *reinterpret_cast<float2 *>(reinterpret_cast<float *>(a.out) + at + 16 * i + 8 * h) = y;
+                }
+            }
+    }
+    return ok;
 }
 
 template <int D, bool QBF16, bool OBF16>
@@ -264,6 +510,10 @@ __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
         if (it.end) return;
         stage_q<D, QBF16>(a, it, smem + C::kOffWork, ms);
         sync_consumers<kConsumers>();
+        if (it.rows <= kNarrow) {
+            ok = narrow_item<D, OBF16>(a, it, smem, ms, taken);
+            continue;
+        }
 
         float m[2], l[2], o[kDT][4];
         int pos[2], low[2];
