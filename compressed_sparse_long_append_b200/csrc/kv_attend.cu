@@ -36,11 +36,14 @@
 // scores while it forms its weights, and a stream's next scores wait for it.
 //
 // Roundings.  P is rounded to bf16 (half a step of each weight; their sum is
-// of the unrounded ones).  The rotated query is rounded to bf16: a row tile
-// of 17 to 128 rows keeps the rounding's rest as a second bf16 operand (its S
-// costs twice, which an item bound by its keys' bytes has to spare), a row tile of
-// 256 has neither the shared memory for it nor tensor time to spare (half again
-// as many products), so its scores carry half a bf16 step of the query.
+// of the unrounded ones).  The rotated query is rounded to bf16, and what the
+// rounding left is kept as a second bf16 operand: its S costs twice, which a
+// row tile bound by its keys' bytes has to spare, and so has one of 64 dims, which is
+// bound by the exponentials (a mixed batch of 28 heads x 64: 67 us without, 68
+// with, error 0.0025 and 0.0020 of the output).  A row tile of 256 rows of 128
+// dims has neither the shared memory for it nor tensor time to spare (half again
+// as many products): its scores carry half a bf16 step of the query (error
+// 0.0025 to 0.0029, where 0.0023 is the rounding of P and of the output).
 //
 // Bound and measured (32 query and 8 KV heads of 128 dims, unless said).
 // Row tiles of 256 are bound by the tensor cores and, beside them, by the
@@ -69,7 +72,11 @@ struct Cfg {
     static constexpr int kTileBytes = kKB * kBlk;
     static constexpr int kKStages = D == 128 ? 3 : 5, kVStages = D == 128 ? 2 : 5;
     static constexpr int kOffQ = 0;
-    static constexpr int kOffK = 2 * kTileBytes;
+    // the rounding's rest of Q, behind both streams' operands with 64 dims; with 128
+    // only a single row tile has one, in the other stream's place
+    static constexpr bool kPairedRest = D == 64;
+    static constexpr int kOffRest = (kPairedRest ? 2 : 1) * kTileBytes;
+    static constexpr int kOffK = (kPairedRest ? 4 : 2) * kTileBytes;
     static constexpr int kOffV = kOffK + kKStages * kTileBytes;
     static constexpr int kOffMisc = kOffV + kVStages * kTileBytes;
     // TMEM columns: one S, which the streams use in turn, P of each stream, O of each stream
@@ -285,8 +292,8 @@ __device__ void load_role(const KvAttendArgs &a, const CUtensorMap &km, const CU
 
 // ---------------------------------------------------------------- Q role
 // Q rows of one stream's operand by four warps (warp = 0..3 of them): norm and
-// rotation in fp32, rounded to bf16 into the swizzled operand; an unpaired item keeps
-// the rounding's rest in the second operand.
+// rotation in fp32, rounded to bf16 into the swizzled operand, the rounding's
+// rest into another where there is one.
 template <int D, bool QBF16>
 struct QRows {
     using C = Cfg<D>;
@@ -395,13 +402,13 @@ struct QRows {
                     x[k][4 * h + 3] -= __uint_as_float(o.y & 0xFFFF0000u);
                 }
             }
-            if (!it.paired) {   // the rest of the rounding
+            if (C::kPairedRest || !it.paired) {   // the rest of the rounding
 #pragma unroll
                 for (int k = 0; k < kGroup; ++k) {
                     const int sw = ((i0 & 7) + k) << 4;
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        *reinterpret_cast<uint2 *>(dst + C::kTileBytes + k * 128 + ((h ? b1 : b0) ^ sw)) =
+                        *reinterpret_cast<uint2 *>(dst + C::kOffRest + k * 128 + ((h ? b1 : b0) ^ sw)) =
                             make_uint2(pack_bf16(x[k][4 * h], x[k][4 * h + 1]),
                                        pack_bf16(x[k][4 * h + 2], x[k][4 * h + 3]));
                 }
@@ -481,7 +488,7 @@ __device__ void s_role(uint8_t *smem, Misc *ms) {
     uint32_t free0 = 0, free1 = 0;   // phases of s_free
     int pending = -1;                // stream of the last S, not yet waited for
     Item it;
-    // S of stream s = Q K^T (both terms of Q for an unpaired item) from K's stage, once the scores before it have been read
+    // S of stream s = Q K^T (both terms of Q where it has two) from K's stage, once the scores before it have been read
     auto step = [&](int s, bool paired, bool last) {
         if (pending >= 0) {
             if (!warp_all(kv_wait(&ms->s_free[pending], pending ? free1 : free0, &ms->abort))) return false;
@@ -498,11 +505,11 @@ __device__ void s_role(uint8_t *smem, Misc *ms) {
                 const uint32_t off = ((i >> 2) * C::kBlk + (i & 3) * 32) >> 4;
                 umma_ss(d, q + off, k + off, kId, i > 0);
             }
-            if (!paired) {
+            if (C::kPairedRest || !paired) {
 #pragma unroll
                 for (int i = 0; i < 4 * C::kKB; ++i) {
                     const uint32_t off = ((i >> 2) * C::kBlk + (i & 3) * 32) >> 4;
-                    umma_ss(d, q + (C::kTileBytes >> 4) + off, k + off, kId, 1);
+                    umma_ss(d, q + (C::kOffRest >> 4) + off, k + off, kId, 1);
                 }
             }
             umma_commit(&ms->s_full[s]);
