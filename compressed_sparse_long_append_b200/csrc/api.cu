@@ -828,6 +828,7 @@ int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
     const size_t need = csla_kv_workspace_size(cfg, B, N, max_new, max_len);
     if (workspace_bytes < need || (need && (!workspace || !aligned16(workspace)))) return CSLA_ERR_ARG;
     a.D = cfg->D; a.HQ = cfg->HQ; a.HK = cfg->HK; a.d_rope = cfg->d_rope; a.pairs = cfg->rope_pairs;
+    a.inv_g = (65536 + cfg->HQ / cfg->HK - 1) / (cfg->HQ / cfg->HK);
     a.window = cfg->window; a.max_new = max_new; a.max_len = max_len; a.eps = cfg->eps;
     a.scale = cfg->scale > 0.f ? cfg->scale : 1.0f / sqrtf((float)cfg->D);
     a.freq = kv_freq(cfg->rope_theta, cfg->d_rope);

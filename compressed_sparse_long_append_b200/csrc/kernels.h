@@ -331,6 +331,7 @@ struct KvJoin {
 struct KvAttendArgs {
     KvBatch bt;
     int D, HQ, HK, d_rope, pairs, window;
+    int inv_g;                      // 2^16 / (HQ / HK), rounded up
     int max_new, max_len;
     float eps, scale;
     KvFreq freq;

@@ -89,6 +89,7 @@ struct Item {
     int n0, T, pos0;     // request: first row of q and out, new tokens, position of the first
     int slot, hk;
     int row0, rows;      // first row of the item, rows of the request
+    int tok0, head0;     // token and head (of the KV head's) of row0
     int rows_s;          // rows whose keys are cut
     int lo, hi;          // key tiles [lo, hi)
     int hi0, lo1;        // paired: stream 0 takes [lo, hi0), stream 1 [lo1, hi)
@@ -148,6 +149,8 @@ __device__ __forceinline__ bool make_item(const KvAttendArgs &a, const KvReq &r,
     it->slot = r.slot;
     it->hk = hk;
     it->row0 = i * 256;
+    it->tok0 = kv_div(i * 256, p.G);
+    it->head0 = i * 256 - it->tok0 * p.G;
     it->rows = p.rows;
     it->rows_s = p.rows_s;
     it->lo = lo;
@@ -677,7 +680,8 @@ __device__ void softmax_role(const KvAttendArgs &a, uint8_t *smem, Misc *ms, int
         const bool mine = row < it.rows;
         const bool idle = it.row0 + (it.paired ? 128 * s : 0) + 32 * warp >= it.rows;   // no row of the warp is real
         const int r = min(row, it.rows - 1);
-        const int pos = it.pos0 + r / G;
+        // (row - row0 + head0 < 384, G <= 128: exact)
+        const int y = r - it.row0 + it.head0, pos = it.pos0 + it.tok0 + (y * a.inv_g >> 16);
         const int low = a.window > 0 ? pos - a.window + 1 : 0;
         float m = -INFINITY, l = 0.f;   // m: the maximum the weights are formed with (score * sc)
         bool any = false;
@@ -799,13 +803,13 @@ __device__ void softmax_role(const KvAttendArgs &a, uint8_t *smem, Misc *ms, int
                 }
             }
         } else if (t0 < t1) {
-            const int hq = it.hk * G + r % G;
+            const int t = pos - it.pos0, hq = it.hk * G + y - (t - it.tok0) * G;
             const float sink = a.sink ? a.sink[hq] * kLog2e : -INFINITY;
             const float top = fmaxf(m, sink);
             const float f = none ? 0.f : ex2(m - top);
             const float den = fmaf(l, f, a.sink && !none ? ex2(sink - top) : 0.f);
             const float w = none ? 0.f : f / den;
-            const long long at = ((long long)(it.n0 + r / G) * a.HQ + hq) * D;
+            const long long at = ((long long)(it.n0 + t) * a.HQ + hq) * D;
             const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;   // (16 bytes are promised)
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
