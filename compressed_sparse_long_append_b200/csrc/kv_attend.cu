@@ -337,7 +337,9 @@ struct QRows {
         Raw8<QBF16> next[kGroup];
         int npos[kGroup];
         auto fetch = [&](int gr) {
-            int tok = (r0 + first + kPass * gr) / G, head = r0 + first + kPass * gr - tok * G;
+            // (row - row0 + head0 < 384, G <= 128: exact)
+            const int y = r0 - it.row0 + first + kPass * gr + it.head0, of = y * a.inv_g >> 16;
+            int tok = it.tok0 + of, head = y - of * G;
 #pragma unroll
             for (int k = 0; k < kGroup; ++k) {
                 const int t = min(tok, it.T - 1);   // (rows that are not there: any)
