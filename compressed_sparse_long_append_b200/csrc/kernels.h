@@ -331,7 +331,7 @@ struct KvJoin {
 struct KvAttendArgs {
     KvBatch bt;
     int D, HQ, HK, d_rope, pairs, window;
-    int inv_g;                      // 2^16 / (HQ / HK), rounded up
+    int inv_g;   // 2^16 / G, rounded up, G = HQ / HK: x * inv_g >> 16 is x / G for x up to 512
     int max_new, max_len;
     float eps, scale;
     KvFreq freq;

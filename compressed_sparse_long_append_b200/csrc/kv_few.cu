@@ -212,7 +212,7 @@ __device__ void stage_q(const KvAttendArgs &a, const Item &it, uint8_t *qs, cons
     const int rest = (it.rows <= kNarrow ? kNarrow : kRows) * 2 * D;
 #pragma unroll 1
     for (int r0 = warp * kPer; r0 < it.rows; r0 += kConsumers * kPer) {
-        const int r = min(r0 + sub, it.rows - 1), t = r / G;
+        const int r = min(r0 + sub, it.rows - 1), t = r * a.inv_g >> 16;
         const Raw8<QBF16> raw = load8<QBF16>(a.q, (long long)(it.n0 + t) * a.q_stride + (it.hk * G + r - t * G) * D, rl);
         float2 cs[4];
 #pragma unroll
@@ -265,7 +265,7 @@ __device__ __forceinline__ bool narrow_item(const KvAttendArgs &a, const Item &i
         ldsm(q[k], work + row * 2 * D + ((ch ^ (row & 7)) << 4));
     }
     const int row = lane >> 2;
-    const int pos = it.pos0 + min(row, it.rows - 1) / G, low = a.window > 0 ? pos - a.window + 1 : 0;
+    const int pos = it.pos0 + (min(row, it.rows - 1) * a.inv_g >> 16), low = a.window > 0 ? pos - a.window + 1 : 0;
     float m = -INFINITY, l = 0.f, o[kDT][4];
 #pragma unroll
     for (int i = 0; i < kDT; ++i)
@@ -456,7 +456,7 @@ __device__ __forceinline__ bool narrow_item(const KvAttendArgs &a, const Item &i
                 if (r < it.rows) *reinterpret_cast<float2 *>(po + 16 * i + 8 * h) = y;
             }
     } else {
-        const int own = min(row, it.rows - 1), hq0 = it.hk * G + own % G;
+        const int own = min(row, it.rows - 1), hq0 = it.hk * G + own - (own * a.inv_g >> 16) * G;
         const bool no = m == -INFINITY && l == 0.f;   // no token at all (scores that are all NaN leave l NaN)
         const float sink = a.sink ? a.sink[hq0] * kLog2e : -INFINITY;
         const float top = fmaxf(m, sink);
@@ -464,7 +464,7 @@ __device__ __forceinline__ bool narrow_item(const KvAttendArgs &a, const Item &i
         const float w = no ? 0.f : f / fmaf(l, f, a.sink ? ex2(sink - top) : 0.f);
         const float mine = __shfl_sync(0xffffffffu, w, 4 * r);
         const bool none = __shfl_sync(0xffffffffu, (int)no, 4 * r);
-        const int t = min(r, it.rows - 1) / G, hq = it.hk * G + min(r, it.rows - 1) - t * G;
+        const int real = min(r, it.rows - 1), t = real * a.inv_g >> 16, hq = it.hk * G + real - t * G;
         const long long at = ((long long)(it.n0 + t) * a.HQ + hq) * D + d;
 #pragma unroll
         for (int i = 0; i < kDT; ++i)
@@ -521,7 +521,7 @@ __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
         for (int h = 0; h < 2; ++h) {
             m[h] = -INFINITY;
             l[h] = 0.f;
-            pos[h] = it.pos0 + min(8 * h + (lane >> 2), it.rows - 1) / G;
+            pos[h] = it.pos0 + (min(8 * h + (lane >> 2), it.rows - 1) * a.inv_g >> 16);
             low[h] = a.window > 0 ? pos[h] - a.window + 1 : 0;
 #pragma unroll
             for (int j = 0; j < kDT; ++j) o[j][2 * h] = o[j][2 * h + 1] = 0.f;
@@ -729,7 +729,7 @@ __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
                     for (int j = 0; j < kDT; ++j)
                         *reinterpret_cast<float2 *>(a.part_o + pr * D + 8 * j + d) = make_float2(o[j][2 * h], o[j][2 * h + 1]);
                 } else {
-                    const int t = r / G, hq = it.hk * G + r - t * G;
+                    const int t = r * a.inv_g >> 16, hq = it.hk * G + r - t * G;
                     const bool none = m[h] == -INFINITY && l[h] == 0.f;   // no token at all (scores that are all NaN leave l NaN)
                     const float sink = a.sink ? a.sink[hq] * kLog2e : -INFINITY;
                     const float top = fmaxf(m[h], sink);
