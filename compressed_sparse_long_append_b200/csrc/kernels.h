@@ -364,9 +364,11 @@ constexpr int kKvFewRows = 16;
 // chunk, by kind.  An item costs about as much as two pages of 128 dims (its
 // Q, its join), so short chunks cost throughput, and long ones the latency of
 // a lone short request:
-//   few    4 pages of 128 dims (64 ragged requests: 143 us, with 2 pages 151), but 2
-//          in a context of up to 8 (one user, 901 tokens, 8 heads: 13.5 us, with 4
-//          pages 15.5); 8 of 64 dims (32 requests, window of 9 pages, 16 heads: 33 us whole, 39 in two);
+//   few    4 pages of 128 dims (64 ragged requests: 135 us, with 3, 6 and 8 pages
+//          136, 137 and 133; one request of 2001 tokens: 15 us, with 6 or 8 pages 19),
+//          but 2 in a context of up to 8 (one user, 901 tokens, 8 heads: 13.5 us,
+//          with 4 pages 15.5); 8 of 64 dims (32 requests, window of 9 pages, 16
+//          heads: 31.7 us whole, 36 in two);
 //   single 16 (32 requests of 20 rows: 144 us, with 8 tiles 166);
 //   paired 8, and only when the row tiles do not fill the SMs.
 __host__ __device__ constexpr int kv_units(int kind) { return kind == kKvPaired ? 148 : 296; }

@@ -50,11 +50,13 @@
 // exponentials (16 per clock and SM: 128 x 128 take 1024 clocks, the tile's
 // products 1024 too): 4096 tokens after 16384 (4 KV heads) take 1.09 ms, 1.13 PFLOP/s, 0.69
 // of what one large library product measures in a burst; at that length the
-// clock falls to about 1.4 GHz under the power limit.  2048 tokens alone: 59 us
-// (0.36; 64 row tiles of unequal length on 148 SMs).  One chunk of 17 to 128
-// rows is bound by its stream of K and V: 32 requests of 20 rows 138 us for
+// clock falls to about 1.4 GHz under the power limit.  2048 tokens alone: 57 us
+// (0.37; 256 items of 1 to 16 tiles on 148 SMs).  One chunk of 17 to 128
+// rows waits for its chain of S, softmax and P V: 32 requests of 20 rows 138 us for
 // 526 MB (3.8 TB/s), 4 requests of 64 rows on one KV head over 262144
-// tokens 154 us for 537 MB (3.5 TB/s).
+// tokens 150 us for 537 MB (3.6 TB/s); with the pages in L2 they take as long:
+// 2350 clocks per tile and some 12 000 per item, between its last product and
+// the next item's first.
 #include "kv.cuh"
 
 namespace csla {
