@@ -105,6 +105,23 @@ def test_chunks(D, HQ, HK, T, L):
     _run(DenseShape(D=D, HQ=HQ, HK=HK, d_rope=64, rope_pairs=HALF), T, L, seed=len(T))
 
 
+@pytest.mark.parametrize("D,HQ,HK,T", [(64, 3, 3, [7, 8, 9, 16, 17]), (128, 2, 2, [17, 9, 8, 1]), (128, 4, 2, [4, 5, 8, 9]),
+                                       (64, 8, 1, [1, 2, 3]), (128, 9, 1, [1, 2]), (64, 17, 1, [1, 8])])
+@pytest.mark.parametrize("window", [0, 70])
+def test_rows_around_the_kinds_of_requests(D, HQ, HK, T, window):
+    """8, 16 and 128 rows per KV head and one more, in one batch: each is taken by other code."""
+    L = [t + 200 + 331 * i for i, t in enumerate(T)]
+    lo = [max(0, n - t + 1 - window) if window else 0 for t, n in zip(T, L)]
+    b, out = _run(DenseShape(D=D, HQ=HQ, HK=HK, d_rope=32, window=window), T, L, lo=lo, seed=D + window, out_dtype=F32)
+    # an unmapped page (the first request's first) is masked whatever the kind, and touches nobody else's rows
+    if not window:
+        b.lb.block_table[b.slots_l[0], 0] = -1
+        got = b.attend(F32)
+        assert _bits() == C.CSLA_DEVERR_PAGE
+        assert torch.equal(got[T[0]:], out[T[0]:]) and bool(torch.isfinite(got).all())
+        assert not torch.equal(got[:T[0]], out[:T[0]])
+
+
 @pytest.mark.parametrize("window", [1, 2, 64, 127, 128, 129, 300])
 def test_windows(window):
     T, L = [1, 260, 7, 40], [900, 260, 131, 650]
