@@ -332,6 +332,8 @@ def csla_kv_attend(cfg, kv, slots, B, q_start, N, max_new, max_len, q, q_dtype, 
     """Attention of the N new tokens over a dense layer's pages (their K and V appended before)."""
     _kv_tensors("csla_kv_attend", q_dtype, q)
     _kv_tensors("csla_kv_attend", out_dtype, out)
+    if not (out is None or isinstance(out, int) or out.is_contiguous()):
+        raise ValueError("csla_kv_attend: out is not contiguous")
     return _check("csla_kv_attend", _lib.csla_kv_attend(
         _ref(cfg), _ref(kv), _ptr(slots), B, _ptr(q_start), N, max_new, max_len, _ptr(q), q_dtype, q_stride,
         _ptr(sink), _ptr(gamma_q), _ptr(out), out_dtype, _ptr(workspace), workspace_bytes, _stream(stream)))

@@ -492,6 +492,8 @@ def test_refusals_of_the_binding():
     b.fill()
     with pytest.raises(ValueError):
         b.attend(out=torch.empty((1, 2, 64), dtype=F32))   # a host tensor
+    with pytest.raises(ValueError):
+        b.attend(out=torch.empty((1, 64, 2), dtype=F32, device=DEV).transpose(1, 2))
     b.q = b.q.to(F32)
     with pytest.raises(ValueError):
         b.attend()
