@@ -4,8 +4,8 @@
 //   K row = bf16(R(p) (k / sqrt(mean(k^2) + eps) * gamma_k)),  V row = bf16(v)
 //
 // A block takes a few consecutive tokens of the ragged batch.  It finds their
-// requests by counting the request starts at or below each token, resolves
-// each token's page once, and evaluates the rotation's cosines and sines once
+// requests (a token's ends at the first start above it), resolves each
+// token's page once, and evaluates the rotation's cosines and sines once
 // per token and pair in shared memory; then D/8 lanes move one (token, head)
 // row, 16 or 32 bytes per lane: the K rows of its tokens, then the V rows (a
 // copy), two rows of a thread at a time and the next two in flight.
@@ -17,6 +17,8 @@
 // are not overlapped by another.  Short calls are bound by the
 // chain offsets -> slot -> length -> page, which runs while the first rows'
 // loads are in flight, and by the call itself on the host (about 7 us).
+#include <limits.h>
+
 #include "kv.cuh"
 
 namespace csla {
@@ -46,7 +48,7 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, kBlocks) kv_append_kernel(const __grid_constant__ KvAppendArgs a, int tok) {
     CSLA_TL_SCOPE(kTlKvAppend);
     constexpr int kLanes = D / 8, kRows = kThreads / kLanes;   // rows per pass
-    __shared__ int s_cnt[kMaxTok];
+    __shared__ int s_end[kMaxTok];         // first j with q_start[j] just above token i (the last token: any above it)
     __shared__ int s_pos[kMaxTok];
     __shared__ long long s_dst[kMaxTok];   // element of the token's row in head 0, -1: skipped
     __shared__ float2 s_cs[kMaxTok][D / 2];
@@ -56,7 +58,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) kv_append_kernel(const __gr
     const int n0 = blockIdx.x * tok, nt = min(tok, a.bt.N - n0);
     const int half = a.d_rope / 2;
     const RowLane rl = row_lane<D>(c, a.d_rope, a.pairs);
-    if (tid < kMaxTok) s_cnt[tid] = 0;
+    if (tid < kMaxTok) s_end[tid] = INT_MAX;
     if (tid < half) s_turn[tid] = a.freq.turn[tid];
     // (row / HK of the at most 32 rows of a pass, HK <= 1024: exact)
     const int dt = kRows * a.inv_hk >> 16, dh = kRows - dt * a.HK, row = tid / kLanes, t0 = row * a.inv_hk >> 16;
@@ -77,20 +79,32 @@ __global__ void __launch_bounds__(kThreads, kBlocks) kv_append_kernel(const __gr
     fetch(a.k_new, a.k_stride, load, raw);
 
     __syncthreads();
-    // the request of token n is the number of starts q_start[1..B] at or below n
+    // Token n is of the request that ends at the first start above n, if that one
+    // begins at or below n and no earlier request begins above it.
+    bool fell = false;   // some start is below the one before, or outside [0, N]
     if (a.bt.q_start) {
-        for (int j = tid + 1; j <= a.bt.B; j += kThreads) {
-            const int s = a.bt.q_start[j];
-            if (s < n0 + nt) atomicAdd(&s_cnt[max(s - n0, 0)], 1);
+        int beyond = INT_MAX;   // this thread's first start above all of the block's tokens
+        for (int j = tid; j <= a.bt.B; j += kThreads) {
+            const int s = a.bt.q_start[j], last = j > 0 ? a.bt.q_start[j - 1] : 0;
+            fell |= s < last || s > a.bt.N;
+            if (j == 0 || s <= n0) continue;
+            if (s >= n0 + nt)
+                beyond = min(beyond, j);
+            else
+                atomicMin(&s_end[s - n0 - 1], j);
         }
-        __syncthreads();
+        beyond = __reduce_min_sync(0xffffffffu, beyond);
+        if ((tid & 31) == 0 && beyond != INT_MAX) atomicMin(&s_end[nt - 1], beyond);
+        fell = __syncthreads_or(fell);
+        if (fell && blockIdx.x == 0 && tid == 0) set_dev_err(CSLA_DEVERR_INDEX);
     }
     if (tid < nt) {
         const int n = n0 + tid;
         int b = n / max(a.bt.T, 1);
         if (a.bt.q_start) {
-            b = 0;
-            for (int j = 0; j <= tid; ++j) b += s_cnt[j];
+            int end = INT_MAX;
+            for (int j = tid; j < nt; ++j) end = min(end, s_end[j]);
+            b = end - 1;
         }
         long long dst = -1;
         int pos = 0;
@@ -98,7 +112,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks) kv_append_kernel(const __gr
         if (b < a.bt.B) {
             const KvReq r = kv_request(a.bt, b, 0x7FFFFFFF, 0x7FFFFFFF);
             err = r.err;
-            if (r.ok && n >= r.n0 && n < r.n0 + r.T) {   // else: a row of no request
+            if (fell)
+                for (int j = 0; j < b; ++j)
+                    if (a.bt.q_start[j] > r.n0) err = CSLA_DEVERR_INDEX;
+            if (!err && r.ok && n >= r.n0 && n < r.n0 + r.T) {   // else: a row of no request
                 pos = r.L - r.T + (n - r.n0);
                 const int page = a.bt.block_table[(long long)r.slot * a.bt.bt_stride + pos / CSLA_PAGE_TOKENS];
                 if (page >= 0 && page < a.bt.n_pages)

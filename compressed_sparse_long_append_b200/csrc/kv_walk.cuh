@@ -11,7 +11,8 @@ namespace csla {
 
 // Request b of a dense call: rows n0 .. n0+T-1, context L (new tokens
 // included), state-cache slot.  ok == false: the request is skipped (`err`
-// says why, 0 for one without new tokens).
+// says why, 0 for one without new tokens).  Its two offsets are checked
+// against each other and N here, against the requests before it by the caller.
 struct KvReq {
     int n0, T, L, slot;
     unsigned err;
@@ -52,6 +53,8 @@ __device__ __forceinline__ KvReq kv_request(const KvBatch &a, int b, int max_new
 // of the largest chunks first.
 struct KvWalk {
     int first = -32, total = 0, before = 0, round = 0, incl = 0;
+    int top = 0;         // largest start so far, once one has fallen below another
+    bool fell = false;
     long long part_before = 0, part_total = 0, part_excl = 0;
     KvReq r{};
     KvPlan p{};
@@ -73,6 +76,29 @@ struct KvWalk {
             long long parts = 0;
             if (b < a.bt.B) {
                 r = kv_request(a.bt, b, a.max_new, a.max_len);
+            }
+            // Requests whose offsets are in order on their own may still overlap
+            // where a start falls below an earlier one, and the workspace is
+            // sized for N rows in all: those are refused.  (Nothing has fallen as
+            // long as no request's end lies below its start.)
+            if (a.bt.q_start && (fell || __any_sync(0xffffffffu, b < a.bt.B && r.err))) {
+                const int start0 = __shfl_sync(0xffffffffu, r.n0, 0);   // (of the group's first: none before is larger yet)
+                if (!fell) top = start0;
+                fell = true;
+                int hi = b < a.bt.B ? r.n0 : top;
+#pragma unroll 1
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, hi, o);
+                    if (lane >= o) hi = max(hi, v);
+                }
+                hi = max(hi, top);
+                if (b < a.bt.B && r.n0 < hi) {
+                    r.err = CSLA_DEVERR_INDEX;
+                    r.ok = false;
+                }
+                top = __shfl_sync(0xffffffffu, hi, 31);
+            }
+            if (b < a.bt.B) {
                 if (r.err && blockIdx.x == 0) set_dev_err(r.err);
                 if (r.ok) {
                     p = kv_plan(r.T, r.L, a.HQ / a.HK, a.HK, a.window, a.D);

@@ -511,8 +511,9 @@ int csla_cp_place(const csla_cfg *cfg, const csla_state *st, const csla_cache *c
  * p * rope_theta^(-2i/d_rope); CSLA_ROPE_ADJACENT pairs dims (2i, 2i+1),
  * CSLA_ROPE_HALVES dims (i, i + d_rope/2), counted from D - d_rope.
  *
- * Device-detected errors: a slot outside [0, n_slots), or q_start not
- * ascending within [0, N] (CSLA_DEVERR_INDEX), or len outside
+ * Device-detected errors: a slot outside [0, n_slots), or a request whose
+ * q_start[b] is below 0 or below the start of a request before it, or whose
+ * q_start[b+1] is below q_start[b] or above N (CSLA_DEVERR_INDEX), or len outside
  * [T_b, 128*bt_stride], or (attention) len above max_len or T_b above
  * max_new (CSLA_DEVERR_LEN): the request is skipped, its outputs untouched.
  * A page id outside the pool (CSLA_DEVERR_PAGE): the append skips the
