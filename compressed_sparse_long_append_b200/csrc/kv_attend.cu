@@ -169,23 +169,21 @@ __device__ __forceinline__ bool make_item(const KvAttendArgs &a, const KvReq &r,
 
 __device__ void sched_role(const KvAttendArgs &a, Misc *ms) {
     const int lane = threadIdx.x & 31;
-    KvWalk w;
-    for (int n = 0;;) {
-        int src = 0, local = 0;
-        const bool more = w.next(a, 1u << kKvSingle | 1u << kKvPaired, &src, &local);
+    int n = 0;
+    kv_walk(a, 1u << kKvSingle | 1u << kKvPaired, [&](const KvWalk &w, bool more, int src, int local) {
         Item it;
         it.end = 1;
         bool have = true;
         if (more && lane == src) have = make_item(a, w.r, w.p, local, w.part_before + w.part_excl, &it);
-        if (!__shfl_sync(0xffffffffu, (int)have, src)) continue;   // (a chunk behind a short row tile's keys)
+        if (!__shfl_sync(0xffffffffu, (int)have, src)) return true;   // (a chunk behind a short row tile's keys)
         const int slot = n % kItems;
-        if (n >= kItems && !warp_all(kv_wait(&ms->item_empty[slot], (n / kItems - 1) & 1, &ms->abort))) return;
+        if (n >= kItems && !warp_all(kv_wait(&ms->item_empty[slot], (n / kItems - 1) & 1, &ms->abort))) return false;
         if (lane == src) ms->item[slot] = it;
         if (n == 0 && lane == 0) CSLA_TL_MARK_ANY(0);
         mbar_arrive_warp(&ms->item_full[slot]);
-        if (!more) return;
         ++n;
-    }
+        return true;
+    });
 }
 
 // The next item for a role's warp; false when there is none (or on an abort).

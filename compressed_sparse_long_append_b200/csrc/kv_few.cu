@@ -131,12 +131,8 @@ template <int D>
 __device__ void producer(const KvAttendArgs &a, const CUtensorMap &km, const CUtensorMap &vm, uint8_t *smem, Misc *ms) {
     using C = Cfg<D>;
     const int lane = threadIdx.x & 31;
-    KvWalk w;
-    int st = 0, issued = 0;
-    bool ok = true;
-    for (int n = 0; ok; ++n) {
-        int src = 0, local = 0;
-        const bool more = w.next(a, 1u << kKvFew, &src, &local);
+    int st = 0, issued = 0, n = 0;
+    kv_walk(a, 1u << kKvFew, [&](const KvWalk &w, bool more, int src, int local) {
         Item it;
         it.end = !more;
         if (more && lane == src) {
@@ -156,19 +152,17 @@ __device__ void producer(const KvAttendArgs &a, const CUtensorMap &km, const CUt
             it.base = w.part_before + w.part_excl;
         }
         const int lo = __shfl_sync(0xffffffffu, it.lo, src), hi = __shfl_sync(0xffffffffu, it.hi, src);
-        if (more && lo >= hi) {
-            --n;
-            continue;
-        }
+        if (more && lo >= hi) return true;
         const int slot = n % kItems;
-        if (n >= kItems && !warp_all(kv_wait(&ms->item_empty[slot], (n / kItems - 1) & 1, &ms->abort))) break;
+        if (n >= kItems && !warp_all(kv_wait(&ms->item_empty[slot], (n / kItems - 1) & 1, &ms->abort))) return false;
         if (lane == src) ms->item[slot] = it;
         mbar_arrive_warp(&ms->item_full[slot]);
-        if (!more) break;
+        ++n;
+        if (!more) return true;
         const int req_slot = __shfl_sync(0xffffffffu, it.slot, src), hk = __shfl_sync(0xffffffffu, it.hk, src);
         const int32_t *table = a.bt.block_table + (long long)req_slot * a.bt.bt_stride;
         int pages = -1, ahead = lo + lane < hi ? table[lo + lane] : -1;
-        for (int p = lo; ok && p < hi; ++p) {
+        for (int p = lo; p < hi; ++p) {
             if (((p - lo) & 31) == 0) {
                 pages = ahead;
                 ahead = p + 32 + lane < hi ? table[p + 32 + lane] : -1;
@@ -178,9 +172,9 @@ __device__ void producer(const KvAttendArgs &a, const CUtensorMap &km, const CUt
             if (bad && lane == 0) set_dev_err(CSLA_DEVERR_PAGE);
             // (an unmapped page's tokens are page 0's, masked)
             const int row = ((bad ? 0 : pg) * a.HK + hk) * CSLA_PAGE_TOKENS;
-            for (int h = 0; ok && h < 2 * C::kPer; ++h) {   // K then V of each part of the page
-                if (issued >= C::kStages) ok = warp_all(kv_wait(&ms->empty[st], (issued / C::kStages - 1) & 1, &ms->abort));
-                if (!ok) break;
+            for (int h = 0; h < 2 * C::kPer; ++h) {   // K then V of each part of the page
+                if (issued >= C::kStages && !warp_all(kv_wait(&ms->empty[st], (issued / C::kStages - 1) & 1, &ms->abort)))
+                    return false;
                 if (lane == 0) {
                     ms->bad[st] = bad;
                     mbar_arrive_expect_tx(&ms->full[st], C::kStage);
@@ -194,7 +188,8 @@ __device__ void producer(const KvAttendArgs &a, const CUtensorMap &km, const CUt
                 st = st + 1 == C::kStages ? 0 : st + 1;
             }
         }
-    }
+        return true;
+    });
     // copies in flight land before the CTA exits (all have, unless a wait gave up)
     for (int i = max(0, issued - C::kStages); i < issued; ++i)
         kv_wait(&ms->full[i % C::kStages], (i / C::kStages) & 1, nullptr);

@@ -5,6 +5,8 @@
 // host code, one fiber per lane.
 #pragma once
 
+#include <limits.h>
+
 #include "kernels.h"
 
 namespace csla {
@@ -61,10 +63,12 @@ struct KvWalk {
 
     // The next item: true with *src = the lane that holds its request (its r, p
     // and the request's first partial row part_before + part_excl) and *local
-    // = its number in the request; false when there is none.  All lanes call it.
-    __device__ __forceinline__ bool next(const KvAttendArgs &a, unsigned kinds, int *src, int *local) {
+    // = its number in the request; false when there is none, or when the caller
+    // wants no more (`rest`: the batch is walked to its end).  All lanes call it.
+    __device__ __forceinline__ bool next(const KvAttendArgs &a, unsigned kinds, bool rest, int *src, int *local) {
         const int lane = threadIdx.x & 31, grid = gridDim.x;
-        const int u = (round & 1) ? (round + 1) * grid - 1 - (int)blockIdx.x : round * grid + (int)blockIdx.x;
+        const int u = rest ? INT_MAX
+                           : ((round & 1) ? (round + 1) * grid - 1 - (int)blockIdx.x : round * grid + (int)blockIdx.x);
         ++round;
         while (u >= before + total) {
             before += total;
@@ -151,6 +155,19 @@ struct KvWalk {
         return true;
     }
 };
+// The items of a CTA: take(w, true, src, local) for each, then take(w, false, 0,
+// 0).  When take gives up (returns false) it is not called again, but the walk
+// goes on to the end of the batch all the same: the join reads an entry of every
+// request, and CTA 0's walk writes them.
+template <typename Take>
+__device__ __forceinline__ void kv_walk(const KvAttendArgs &a, unsigned kinds, Take take) {
+    KvWalk w;
+    for (bool rest = false, more = true; more;) {
+        int src = 0, local = 0;
+        more = w.next(a, kinds, rest, &src, &local);
+        rest = rest || !take(w, more, src, local);
+    }
+}
 
 // Bounded wait of the attention kernels' roles: they hand tiles over every few
 // hundred nanoseconds, so they poll (each poll parks the warp for the

@@ -135,14 +135,11 @@ void walk(const int32_t *shape, const int32_t *slots, const int32_t *q_start, co
     g_err = 0;
     run_warp([&] {
         int n = 0;
-        KvWalk w;
-        int src, local;
-        while (w.next(a, kinds, &src, &local))
-            if (n++ == give_up) break;
-        if (threadIdx.x == 0) {
-            out[0] = n;
-            out[2] = w.part_before;   // (all of them, at the end)
-        }
+        kv_walk(a, kinds, [&](const KvWalk &w, bool more, int, int) {
+            if (threadIdx.x == 0 && !more) out[2] = w.part_before;   // (of all requests, at the end)
+            return !more || n++ != give_up;
+        });
+        if (threadIdx.x == 0) out[0] = n;
     });
     out[1] = g_err;
     for (int b = 0; b < B; ++b) {

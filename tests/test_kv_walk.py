@@ -111,3 +111,17 @@ def test_random_offsets(host, broken):
             assert w.part_rows <= w.room, (i, w.part_rows, w.room)
             most = max(most, w.part_rows / w.room)
     assert most > 0.3   # the bound is not out of all proportion, so the batches did reach for it
+
+
+@pytest.mark.parametrize("starts", [None, [3 * i for i in range(101)]])
+def test_a_role_that_gives_up_still_leaves_every_request_for_the_join(host, starts):
+    """After a wait that ran out no item is taken, but the join runs all the same and reads every request's entry."""
+    shape = DenseShape(D=128, HQ=16, HK=2)
+    args = (host, shape, starts, [9000 + i for i in range(100)], 300, 3, 10000)
+    whole = Walk(*args, B=100)
+    assert whole.items > 10 and whole.err == 0 and bool((whole.rows_s > 0).all())
+    for n in (0, 1, 10):
+        w = Walk(*args, B=100, give_up=n)
+        assert w.items == n + 1
+        assert np.array_equal(w.join, whole.join)
+        assert w.err == 0
