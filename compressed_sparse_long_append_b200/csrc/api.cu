@@ -738,8 +738,8 @@ int csla_kv_append(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
     return cuda_status(launch_kv_append(a, dtype == CSLA_BF16, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-// Longest context of an attention call: a row tile's keys (2^20 tiles of less
-// than a microsecond) have to end well inside the 2 s bound of the kernels' waits.
+// Longest context of an attention call: counts of key tiles and partial rows
+// stay far inside 32 and 64 bits (one KV head of 64 dims and so many tokens has 34 GB of pages).
 constexpr int32_t kKvMaxLen = 1 << 27;
 
 // Key tiles that a row tile may have, at most.

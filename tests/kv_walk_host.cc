@@ -149,4 +149,22 @@ void walk(const int32_t *shape, const int32_t *slots, const int32_t *q_start, co
     }
 }
 
+// kv_wait on a barrier that completes after ready_ms, of a role that sees the tile count move every beat_ms (0:
+// it never does; watch 0: it does not look).  Returns what it returned, *ms the time it took, *abort the flag it left.
+int wait(int64_t ready_ms, int64_t beat_ms, int watch, int64_t *ms, int *abort, unsigned *err) {
+    uint64_t bar = 0;
+    volatile int stop = 0;
+    g_now = 12345;
+    g_ready = g_now + ready_ms * 1000000;
+    g_beat_ns = beat_ms * 1000000;
+    g_err = 0;
+    const uint64_t t0 = g_now;
+    const bool ok = watch ? kv_wait(&bar, 0, &stop, &g_beat) : kv_wait(&bar, 0, &stop);
+    g_beat_ns = 0;
+    *ms = (int64_t)((g_now - t0) / 1000000);
+    *abort = stop;
+    *err = g_err;
+    return ok;
+}
+
 }  // extern "C"
