@@ -108,7 +108,6 @@ struct Misc {
     int bad[kFlags];     // tile's page is not mapped
     unsigned long long turn[64];   // rotation frequencies
     uint32_t tmem;
-    int beat;            // key tiles asked for: what a wait for an item's end watches
     int abort;
 };
 
@@ -178,7 +177,7 @@ __device__ void sched_role(const KvAttendArgs &a, Misc *ms) {
         if (more && lane == src) have = make_item(a, w.r, w.p, local, w.part_before + w.part_excl, &it);
         if (!__shfl_sync(0xffffffffu, (int)have, src)) return true;   // (a chunk behind a short row tile's keys)
         const int slot = n % kItems;
-        if (n >= kItems && !warp_all(kv_wait(&ms->item_empty[slot], (n / kItems - 1) & 1, &ms->abort, &ms->beat))) return false;
+        if (n >= kItems && !warp_all(kv_wait(&ms->item_empty[slot], (n / kItems - 1) & 1, &ms->abort, kItemLimitNs))) return false;
         if (lane == src) ms->item[slot] = it;
         if (n == 0 && lane == 0) CSLA_TL_MARK_ANY(0);
         mbar_arrive_warp(&ms->item_full[slot]);
@@ -261,7 +260,6 @@ struct Loader {
         const bool bad = pg < 0 || pg >= a.bt.n_pages;
         if (lane == 0) {
             ms->bad[ks % kFlags] = bad;
-            *(volatile int *)&ms->beat = ks;
             if (bad) set_dev_err(CSLA_DEVERR_PAGE);
         }
         // (an unmapped page's tile is page 0's, masked)
@@ -367,8 +365,8 @@ struct QRows {
             if (gr + 1 < groups) fetch(gr + 1);   // a group ahead
             // (the first rows' loads are in flight while the operand is still in use)
             if (!waited) {
-                if (!warp_all(kv_wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort, &ms->beat))) return false;
-                if (!it.paired && !warp_all(kv_wait(&ms->q_empty[1], (n - 1) & 1, &ms->abort, &ms->beat))) return false;
+                if (!warp_all(kv_wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort, kItemLimitNs))) return false;
+                if (!it.paired && !warp_all(kv_wait(&ms->q_empty[1], (n - 1) & 1, &ms->abort, kItemLimitNs))) return false;
                 waited = true;
             }
             float x[kGroup][8];
@@ -422,8 +420,8 @@ struct QRows {
             }
         }
         if (!waited) {   // (no row of this warp: the operand's phases are kept in step all the same)
-            if (!warp_all(kv_wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort, &ms->beat))) return false;
-            if (!it.paired && !warp_all(kv_wait(&ms->q_empty[1], (n - 1) & 1, &ms->abort, &ms->beat))) return false;
+            if (!warp_all(kv_wait(&ms->q_empty[s], (n - 1) & 1, &ms->abort, kItemLimitNs))) return false;
+            if (!it.paired && !warp_all(kv_wait(&ms->q_empty[1], (n - 1) & 1, &ms->abort, kItemLimitNs))) return false;
         }
         fence_proxy_async_smem();
         mbar_arrive_warp(&ms->q_full[s]);
@@ -889,7 +887,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
         }
         mbar_init(&ms->drain[0], 1);
         mbar_init(&ms->drain[1], 1);
-        ms->beat = -1;
         ms->abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&km);

@@ -172,24 +172,20 @@ __device__ __forceinline__ void kv_walk(const KvAttendArgs &a, unsigned kinds, T
 // Bounded wait of the attention kernels' roles: they hand tiles over every few
 // hundred nanoseconds, so they poll (each poll parks the warp for the
 // hardware's own short time) instead of asking to be put to sleep.  A wait for
-// a tile gives up after kWaitLimitNs; one for the end of an item, which may
-// take longer (2^20 tiles of 2 us), after as long without a change of *beat, the
-// CTA's count of tiles.
+// a tile gives up after kWaitLimitNs, one for the end of an item after
+// kItemLimitNs: an item is 2^20 key tiles at most, of 2.2 us each where every SM
+// is busy.  (A CTA that stands still ends by its waits for tiles all the same,
+// whose *abort the longer waits look at.)
+constexpr uint64_t kItemLimitNs = 8 * kWaitLimitNs;
 __device__ __forceinline__ bool kv_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
-                                        const volatile int *beat = nullptr) {
+                                        uint64_t limit_ns = kWaitLimitNs) {
     if (mbar_try_wait(bar, parity)) return true;
-    uint64_t t0 = globaltimer_ns();
-    int seen = beat ? *beat : 0;
+    const uint64_t t0 = globaltimer_ns();
     for (int i = 1;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
         if ((i & 15) == 0) {
             if (abort && *abort) return false;
-            const uint64_t t = globaltimer_ns();
-            if (beat && *beat != seen) {
-                seen = *beat;
-                t0 = t;
-            }
-            if (t - t0 > kWaitLimitNs) {
+            if (globaltimer_ns() - t0 > limit_ns) {
                 set_dev_err(CSLA_DEVERR_TIMEOUT);
                 if (abort) *abort = 1;
                 return false;

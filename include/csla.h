@@ -444,7 +444,8 @@ int csla_device_error(csla_stream_t stream, uint32_t *bits);
  * limit_us microseconds (1 .. 2000000); the wait gives up, sets
  * CSLA_DEVERR_TIMEOUT in the device error word and the kernel returns, so
  * csla_device_error() afterwards reports CSLA_ERR_DEVICE with that bit and
- * the context stays usable.  (The kernels' own waits give up after 2 s.)
+ * the context stays usable.  (The kernels' own waits give up after 2 s, the
+ * dense attention's for the end of a long row tile after 16 s.)
  * Errors: CSLA_ERR_ARG for a limit outside the range; CSLA_ERR_CUDA if the
  * launch fails.
  */

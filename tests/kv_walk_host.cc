@@ -97,13 +97,13 @@ static int __ffs(unsigned x) { return __builtin_ffs(x); }
 
 // ---- a clock, a barrier that completes at a time, the error word
 static unsigned g_err;
-static uint64_t g_now, g_ready, g_beat_ns;
-static volatile int g_beat;
+static uint64_t g_now, g_ready, g_stop_at;
+static volatile int g_stop;
 static void set_dev_err(unsigned bits) { g_err |= bits; }
 static uint64_t globaltimer_ns() { return g_now; }
 static bool mbar_try_wait(uint64_t *, uint32_t) {
     g_now += 1000;
-    if (g_beat_ns) g_beat = (int)(g_now / g_beat_ns);
+    if (g_now >= g_stop_at) g_stop = 1;
     return g_now >= g_ready;
 }
 namespace csla {
@@ -149,20 +149,18 @@ void walk(const int32_t *shape, const int32_t *slots, const int32_t *q_start, co
     }
 }
 
-// kv_wait on a barrier that completes after ready_ms, of a role that sees the tile count move every beat_ms (0:
-// it never does; watch 0: it does not look).  Returns what it returned, *ms the time it took, *abort the flag it left.
-int wait(int64_t ready_ms, int64_t beat_ms, int watch, int64_t *ms, int *abort, unsigned *err) {
+// kv_wait on a barrier that completes after ready_ms (item 1: a wait for the end of an item), of a CTA in which another
+// role gives up after abort_ms (0: never).  Returns what it returned, *ms the time it took, *abort the flag it left.
+int wait(int64_t ready_ms, int64_t abort_ms, int item, int64_t *ms, int *abort, unsigned *err) {
     uint64_t bar = 0;
-    volatile int stop = 0;
-    g_now = 12345;
+    const uint64_t t0 = g_now = 12345;
     g_ready = g_now + ready_ms * 1000000;
-    g_beat_ns = beat_ms * 1000000;
+    g_stop_at = abort_ms ? g_now + abort_ms * 1000000 : ~0ull;
+    g_stop = 0;
     g_err = 0;
-    const uint64_t t0 = g_now;
-    const bool ok = watch ? kv_wait(&bar, 0, &stop, &g_beat) : kv_wait(&bar, 0, &stop);
-    g_beat_ns = 0;
+    const bool ok = item ? kv_wait(&bar, 0, &g_stop, kItemLimitNs) : kv_wait(&bar, 0, &g_stop);
     *ms = (int64_t)((g_now - t0) / 1000000);
-    *abort = stop;
+    *abort = g_stop;
     *err = g_err;
     return ok;
 }

@@ -127,15 +127,14 @@ def test_a_role_that_gives_up_still_leaves_every_request_for_the_join(host, star
         assert w.err == 0
 
 
-@pytest.mark.parametrize("ready,beat,watch,ok,took", [
-    (1900, 0, 0, True, 1900), (2400, 0, 0, False, 2000), (2400, 2, 0, False, 2000),   # a tile that does not come within 2 s
-    (2400, 0, 1, False, 2000),        # an item whose tiles do not move
-    (2400, 2, 1, True, 2400),         # 2^20 tiles of 2 us and more: longer than 2 s, moving all the while
-    (9000, 1500, 1, True, 9000),      # slow, but moving
-    (9000, 2500, 1, False, 2000)])    # a stop of more than 2 s
-def test_waits_give_up_after_two_seconds_without_progress(host, ready, beat, watch, ok, took):
+@pytest.mark.parametrize("ready,stop,item,ok,took", [
+    (1900, 0, 0, True, 1900), (2400, 0, 0, False, 2000),   # a tile: 2 s
+    (2400, 0, 1, True, 2400),                              # 2^20 tiles of 2.3 us each, the longest item
+    (9000, 0, 1, True, 9000), (17000, 0, 1, False, 16000),
+    (9000, 2100, 1, False, 2100)])                         # another role of the CTA has given up
+def test_waits_are_bounded(host, ready, stop, item, ok, took):
     ms, abort, err = ctypes.c_int64(), ctypes.c_int(), ctypes.c_uint()
-    got = host.wait(ctypes.c_int64(ready), ctypes.c_int64(beat), watch, ctypes.byref(ms), ctypes.byref(abort), ctypes.byref(err))
+    got = host.wait(ctypes.c_int64(ready), ctypes.c_int64(stop), item, ctypes.byref(ms), ctypes.byref(abort), ctypes.byref(err))
     assert bool(got) == ok
     assert abs(ms.value - took) <= 10
-    assert (abort.value, err.value) == ((0, 0) if ok else (1, C.CSLA_DEVERR_TIMEOUT))
+    assert (abort.value, err.value) == ((0, 0) if ok else (1, 0 if stop else C.CSLA_DEVERR_TIMEOUT))
