@@ -536,7 +536,7 @@ int csla_hca_attend(const csla_cfg *cfg, const csla_state *st, const csla_cache 
 }
 
 // Side stream and fork/join events of the calling thread on each device
-// (created on the thread's first decode-step call on that device).
+// (created on the thread's first call that forks on that device).
 struct SideStream {
     cudaStream_t s = nullptr;
     cudaEvent_t fork = nullptr, join = nullptr;
@@ -555,6 +555,24 @@ static int side_stream(SideStream **out) {
     }
     *out = &x;
     return CSLA_OK;
+}
+
+// The same for work on `stream`, or null where the two cannot be forked and
+// joined: the side stream would have to be created inside a capture, or one of
+// the two belongs to a capture that the other is not in (a thread that calls
+// between the fork of one captured call and the end of its capture).
+static SideStream *side_stream_for(cudaStream_t stream) {
+    int dev = 0;
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone, side = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0, side_id = 0;
+    SideStream *x = nullptr;
+    if (cudaStreamGetCaptureInfo(stream, &cs, &id) == cudaSuccess && cudaGetDevice(&dev) == cudaSuccess && dev >= 0 &&
+        dev < 64 && (cs == cudaStreamCaptureStatusNone || tl_side[dev].s) && side_stream(&x) == CSLA_OK &&
+        cudaStreamGetCaptureInfo(x->s, &side, &side_id) == cudaSuccess &&
+        (side == cudaStreamCaptureStatusNone || (side == cs && side_id == id)))
+        return x;
+    cudaGetLastError();   // (nothing failed that the call needs)
+    return nullptr;
 }
 
 int csla_csa_decode_step(const csla_cfg *cfg, const csla_state *st, const csla_cache *cache, const int32_t *slots,
@@ -844,25 +862,39 @@ int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
     const uint64_t cache_rows = (uint64_t)kv->n_pages * cfg->HK * CSLA_PAGE_TOKENS;
     const long long nt = kv_most_tiles(cfg, max_new, max_len);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaSuccess;
-    if (least_rows <= kKvFewRows) {
-        CUtensorMap km, vm;
-        if (!encode_bf16_2d(&km, kv->k, cfg->D, cache_rows, kv_few_box(cfg->D)) ||
-            !encode_bf16_2d(&vm, kv->v, cfg->D, cache_rows, kv_few_box(cfg->D)))
-            return CSLA_ERR_CUDA;
-        const long long m = kv_min_tiles(kKvFew, cfg->D, 1);
-        e = launch_kv_few(a, q16, o16, km, vm, num_sms_current(),
-                          (long long)B * cfg->HK * ((nt + m - 1) / m), st);
+    const bool few = least_rows <= kKvFewRows, more = most_rows > kKvFewRows;
+    CUtensorMap few_k, few_v, more_k, more_v;
+    if (few && (!encode_bf16_2d(&few_k, kv->k, cfg->D, cache_rows, kv_few_box(cfg->D)) ||
+                !encode_bf16_2d(&few_v, kv->v, cfg->D, cache_rows, kv_few_box(cfg->D))))
+        return CSLA_ERR_CUDA;
+    if (more && (!encode_bf16_2d(&more_k, kv->k, cfg->D, cache_rows, CSLA_PAGE_TOKENS) ||
+                 !encode_bf16_2d(&more_v, kv->v, cfg->D, cache_rows, CSLA_PAGE_TOKENS)))
+        return CSLA_ERR_CUDA;
+    // Requests of both kinds: the two kernels write rows of their own (and the
+    // same entries for the join), so they run side by side on two streams: 12
+    // requests of 1 to 1500 tokens 67 us, one after the other 84; 64 decoding
+    // requests and a chunk of 512 tokens 409 us, with kv_attend_kernel first 413,
+    // one after the other 467.
+    SideStream *side = few && more ? side_stream_for(st) : nullptr;
+    cudaError_t e = cudaSuccess, ej = cudaSuccess;
+    if (side) {
+        e = cudaEventRecord(side->fork, st);
+        if (e == cudaSuccess) e = cudaStreamWaitEvent(side->s, side->fork, 0);
+        if (e != cudaSuccess) return cuda_status(e);
     }
-    if (e == cudaSuccess && most_rows > kKvFewRows) {
-        CUtensorMap km, vm;
-        if (!encode_bf16_2d(&km, kv->k, cfg->D, cache_rows, CSLA_PAGE_TOKENS) ||
-            !encode_bf16_2d(&vm, kv->v, cfg->D, cache_rows, CSLA_PAGE_TOKENS))
-            return CSLA_ERR_CUDA;
+    if (few) {
+        const long long m = kv_min_tiles(kKvFew, cfg->D, 1);
+        e = launch_kv_few(a, q16, o16, few_k, few_v, num_sms_current(), (long long)B * cfg->HK * ((nt + m - 1) / m), st);
+    }
+    if (e == cudaSuccess && more) {
         const long long m = kv_min_tiles(kKvSingle, cfg->D, 1);
-        a.beside = least_rows <= kKvFewRows;
-        e = launch_kv_attend(a, q16, o16, km, vm, num_sms_current(),
-                             ((long long)N * G / 256 + B) * cfg->HK * ((nt + m - 1) / m), st);
+        e = launch_kv_attend(a, q16, o16, more_k, more_v, num_sms_current(),
+                             ((long long)N * G / 256 + B) * cfg->HK * ((nt + m - 1) / m), side ? side->s : st);
+    }
+    if (side) {   // joined also when a launch failed: an unjoined fork would invalidate a capture
+        ej = cudaEventRecord(side->join, side->s);
+        if (ej == cudaSuccess) ej = cudaStreamWaitEvent(st, side->join, 0);
+        if (e == cudaSuccess) e = ej;
     }
     if (e == cudaSuccess && rows) e = launch_kv_join(a, o16, num_sms_current(), st);
     return cuda_status(e);

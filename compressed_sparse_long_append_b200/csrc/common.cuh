@@ -92,8 +92,8 @@ __device__ __forceinline__ int key_exp_e4m3(float amax) {
 // ------------------------------------------------------------ programmatic dependent launch
 // Every libcsla kernel is launched with programmatic stream serialization
 // (programmatic dependent launch) and calls pdl_trigger() first (kernels that
-// allocate TMEM: right after the allocation), so the next kernel on the
-// stream can be scheduled while it runs.  pdl_wait() blocks
+// allocate TMEM: right after the allocation; kv_few_kernel: after its wait), so
+// the next kernel on the stream can be scheduled while it runs.  pdl_wait() blocks
 // until the preceding kernel has completed and its writes are visible; a
 // kernel calls it before it reads anything produced on the stream or writes
 // global memory (the device error word aside).  Before the wait a kernel

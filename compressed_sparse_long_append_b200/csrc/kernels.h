@@ -341,7 +341,6 @@ struct KvAttendArgs {
     void *out;
     // workspace: first partial row of each request [B], (m, l) and O of the partial rows
     KvJoin *part_req;   // [B], what the join needs of a request
-    int beside;         // kv_attend_kernel is launched right behind kv_few_kernel of the same call
     float2 *part_ml;
     float *part_o;
 };

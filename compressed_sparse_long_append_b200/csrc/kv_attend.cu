@@ -896,10 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
     __syncthreads();
     tc_fence_after();
     pdl_trigger();
-    // (behind kv_few_kernel of the same call, which lets this kernel start only
-    // when all before it has ended, the two run side by side; the
-    // end of this one waits for the other)
-    if (!a.beside) pdl_wait();
+    pdl_wait();
     CSLA_TL_WAITED();
     // registers: 2 x 128 x 176 + 128 x 96 + 128 x 64 = 65536, the launch's 512 x 128
     if (warp < 8) {
@@ -926,7 +923,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
         tc_fence_after();
         tmem_dealloc(ms->tmem, 512);
     }
-    if (a.beside) pdl_wait();
 }
 
 // ---------------------------------------------------------------- join

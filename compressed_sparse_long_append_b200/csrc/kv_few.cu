@@ -771,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_few_kernel(const __grid_consta
     }
     __syncthreads();
     pdl_wait();
-    pdl_trigger();   // after the wait: what starts now finds everything before this kernel ended
+    pdl_trigger();   // (before the wait: one user's 901 tokens 11.0 us instead of 10.7 in a graph)
     CSLA_TL_WAITED();
     if (threadIdx.x >= 32 * kConsumers)
         producer<D>(a, km, vm, smem, ms);

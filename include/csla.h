@@ -583,6 +583,12 @@ int csla_kv_append(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
  * own T_b and len and of the layer's shape.
  * workspace: csla_kv_workspace_size(cfg, B, N, max_new, max_len) bytes,
  * 16-byte aligned, not shared with a call that may run at the same time.
+ * A call whose requests may have up to 16 rows (T_b * HQ / HK) as well as more
+ * runs two kernels side by side, one of them on the calling thread's side
+ * stream (see csla_csa_decode_step), forked from and joined back into `stream`.
+ * Where that cannot be (the thread's first such call on the device is inside a
+ * capture, or the side stream is part of another capture that has not ended) they
+ * run one after the other, with the same results.
  * Errors: CSLA_ERR_ARG, CSLA_ERR_UNSUPPORTED (shapes; n_pages*HK*128 or
  * N*HQ >= 2^31); device bits INDEX, LEN, PAGE.
  */
