@@ -300,43 +300,112 @@ def csla_version():
     return int(_lib.csla_version())
 
 
-_KV_DTYPES = {}
+# Tensors of the dense layers' calls, checked, as addresses (which pass unchecked).  This runs at every call of a decode
+# step, so what is right is found right in one line, and only the rest is looked at closely.
+_torch = None
+_KV_TYPES = {}   # dtype code -> torch dtype
 
 
-def _kv_tensors(fn, dtype, *tensors):
-    """Tensors of a dense layer's call (addresses pass unchecked): of the given dtype code, on the current device."""
-    import torch
-    if not _KV_DTYPES:
-        _KV_DTYPES.update({CSLA_F32: torch.float32, CSLA_BF16: torch.bfloat16})
-    want, dev = _KV_DTYPES.get(dtype), torch._C._cuda_getDevice()
-    for t in tensors:
-        if t is None or isinstance(t, int):
-            continue
-        if t.dtype is not want:
-            raise ValueError("%s: a %s tensor where dtype code %s was given" % (fn, t.dtype, dtype))
-        if t.get_device() != dev:
-            raise ValueError("%s: a tensor on %s, not on the current device" % (fn, t.device))
+def _kv_here():
+    """The current device's index (-2: none)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _KV_TYPES.update({CSLA_F32: torch.float32, CSLA_BF16: torch.bfloat16})
+        _torch = torch
+    try:
+        return _torch._C._cuda_getDevice()
+    except RuntimeError:   # no GPU: every tensor is on another device
+        return -2
+
+
+def _kv_stream(stream, dev):
+    if stream is None and dev >= 0:
+        return _torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
+
+
+def _kv_array(fn, name, t, dtype, n, dev):
+    """A contiguous tensor of at least n elements."""
+    if t is None or type(t) is int:
+        return t
+    if t.dtype is dtype and t.numel() >= n and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    if t.dtype is not dtype:
+        raise ValueError("%s: %s is %s, not %s" % (fn, name, t.dtype, dtype))
+    if t.numel() < n or not t.is_contiguous():
+        raise ValueError("%s: %s is not contiguous, or has fewer than %d elements" % (fn, name, n))
+    raise ValueError("%s: %s is on %s, not on the current device" % (fn, name, t.device))
+
+
+def _kv_rows(fn, name, t, dtype, n, width, stride, dev):
+    """A tensor whose memory is n rows of `width` elements, `stride` elements apart."""
+    if t is None or type(t) is int:
+        return t
+    fits = t.numel() >= (n - 1) * stride + width if t.is_contiguous() else _kv_strided(t, n, width, stride)
+    if fits and t.dtype is dtype and t.get_device() == dev:
+        return t.data_ptr()
+    if t.dtype is not dtype:
+        raise ValueError("%s: %s is %s where the dtype code says %s" % (fn, name, t.dtype, dtype))
+    if not fits:
+        raise ValueError("%s: %s of shape %s and strides %s is not %d rows of %d elements, %d apart"
+                         % (fn, name, tuple(t.shape), t.stride(), n, width, stride))
+    raise ValueError("%s: %s is on %s, not on the current device" % (fn, name, t.device))
+
+
+def _kv_strided(t, n, width, stride):
+    size, step = t.shape, t.stride()
+    i = len(size)
+    if i == 3 and step == (stride, size[2], 1):
+        return size[0] >= n and size[1] * size[2] >= width
+    if i == 2 and step == (stride, 1):
+        return size[0] >= n and size[1] >= width
+    # the dims that lie side by side, then those that step by `stride`
+    inner, rows, at = 1, 1, stride
+    while i and (step[i - 1] == inner or size[i - 1] == 1):
+        i -= 1
+        inner *= size[i]
+    while i and (step[i - 1] == at or size[i - 1] == 1):
+        i -= 1
+        rows *= size[i]
+        at *= size[i]
+    return inner >= (n - 1) * stride + width or (not i and inner >= width and rows >= n)
 
 
 def csla_kv_append(cfg, kv, slots, B, q_start, N, k_new, k_stride, v_new, v_stride, dtype, gamma_k=None, stream=None):
     """Keys (normed with gamma_k, rotated) and values of N new tokens into a dense layer's pages.  q_start: int32
-    [B+1] row offsets, or None when every request has N / B new tokens; strides in elements between tokens."""
-    _kv_tensors("csla_kv_append", dtype, k_new, v_new)
-    return _check("csla_kv_append", _lib.csla_kv_append(
-        _ref(cfg), _ref(kv), _ptr(slots), B, _ptr(q_start), N, _ptr(k_new), k_stride, _ptr(v_new), v_stride, dtype,
-        _ptr(gamma_k), _stream(stream)))
+    [B+1] row offsets, or None when every request has N / B new tokens; strides in elements between tokens.  Tensors are
+    checked (ValueError): int32 slots and q_start, f32 gamma_k, rows as the strides say, all on the current device."""
+    fn, dev = "csla_kv_append", _kv_here()
+    D, width = (cfg.D, cfg.HK * cfg.D) if cfg is not None else (0, 0)
+    new, i32 = _KV_TYPES.get(dtype), _torch.int32
+    return _check(fn, _lib.csla_kv_append(
+        _ref(cfg), _ref(kv), _kv_array(fn, "slots", slots, i32, B, dev), B,
+        _kv_array(fn, "q_start", q_start, i32, B + 1, dev), N,
+        _kv_rows(fn, "k_new", k_new, new, N, width, k_stride, dev), k_stride,
+        _kv_rows(fn, "v_new", v_new, new, N, width, v_stride, dev), v_stride, dtype,
+        _kv_array(fn, "gamma_k", gamma_k, _torch.float32, D, dev), _kv_stream(stream, dev)))
 
 
 def csla_kv_attend(cfg, kv, slots, B, q_start, N, max_new, max_len, q, q_dtype, q_stride, sink, gamma_q, out,
                    out_dtype, workspace, workspace_bytes, stream=None):
-    """Attention of the N new tokens over a dense layer's pages (their K and V appended before)."""
-    _kv_tensors("csla_kv_attend", q_dtype, q)
-    _kv_tensors("csla_kv_attend", out_dtype, out)
-    if not (out is None or isinstance(out, int) or out.is_contiguous()):
-        raise ValueError("csla_kv_attend: out is not contiguous")
-    return _check("csla_kv_attend", _lib.csla_kv_attend(
-        _ref(cfg), _ref(kv), _ptr(slots), B, _ptr(q_start), N, max_new, max_len, _ptr(q), q_dtype, q_stride,
-        _ptr(sink), _ptr(gamma_q), _ptr(out), out_dtype, _ptr(workspace), workspace_bytes, _stream(stream)))
+    """Attention of the N new tokens over a dense layer's pages (their K and V appended before).  Tensors are checked as in
+    csla_kv_append; out contiguous, workspace of workspace_bytes at least."""
+    fn, dev = "csla_kv_attend", _kv_here()
+    D, HQ = (cfg.D, cfg.HQ) if cfg is not None else (0, 0)
+    i32, f32 = _torch.int32, _torch.float32
+    if not (workspace is None or type(workspace) is int):
+        if workspace.nbytes < workspace_bytes or not workspace.is_contiguous() or workspace.get_device() != dev:
+            raise ValueError("%s: workspace is not contiguous, has fewer than %d bytes, or is not on the current device (%s)"
+                             % (fn, workspace_bytes, workspace.device))
+        workspace = workspace.data_ptr()
+    return _check(fn, _lib.csla_kv_attend(
+        _ref(cfg), _ref(kv), _kv_array(fn, "slots", slots, i32, B, dev), B,
+        _kv_array(fn, "q_start", q_start, i32, B + 1, dev), N, max_new, max_len,
+        _kv_rows(fn, "q", q, _KV_TYPES.get(q_dtype), N, HQ * D, q_stride, dev), q_dtype, q_stride,
+        _kv_array(fn, "sink", sink, f32, HQ, dev), _kv_array(fn, "gamma_q", gamma_q, f32, D, dev),
+        _kv_array(fn, "out", out, _KV_TYPES.get(out_dtype), N * HQ * D, dev), out_dtype, workspace, workspace_bytes,
+        _kv_stream(stream, dev)))
 
 
 def csla_kv_workspace_size(cfg, B, N, max_new, max_len):

@@ -69,3 +69,29 @@ def test_overlapping_requests_are_refused(T, order, kept):
         assert torch.equal(b.lb.v[page, :, (p % 128).to(DEV)], v)
     for pool in (b.lb.k, b.lb.v):
         assert bool(torch.isnan(pool[~hit]).all()) and bool(torch.isfinite(pool[hit]).all())
+
+
+def test_other_types_and_layouts_on_the_device():
+    """Tensors that would be read as something else, or past their end, are refused by the binding; the call is then made right."""
+    b = Batch(DenseShape(D=64, HQ=4, HK=2, d_rope=64), [3, 2], [300, 40], seed=71)
+    b.fill()
+    want = b.attend(F32)
+    for name, bad in (("gamma_q", b.gamma_q.bfloat16()), ("gamma_q", b.gamma_q[:-1].contiguous()), ("sink", b.sink.bfloat16()),
+                      ("sink", b.sink.double()), ("slots", b.slots.long()), ("slots", b.slots[:1]), ("start", b.start.long()),
+                      ("start", b.start[:-1]), ("q", b.q.reshape(5, 4, 64).transpose(0, 1)), ("q", b.q[:-1]), ("slots", b.slots.cpu())):
+        good = getattr(b, name)
+        setattr(b, name, bad)
+        with pytest.raises(ValueError):
+            b.attend(F32)
+        if name in ("slots", "start"):
+            with pytest.raises(ValueError):
+                b.append()
+        setattr(b, name, good)
+    with pytest.raises(ValueError):
+        b.gamma_k = b.gamma_k.bfloat16()
+        b.append()
+    need = C.csla_kv_workspace_size(b.lb.cfg(), b.B, b.N, b.max_new, b.max_len)
+    with pytest.raises(ValueError):
+        b.attend(F32, ws=torch.empty(need - 1, dtype=torch.uint8, device=DEV))
+    assert torch.equal(b.attend(F32), want)
+    assert _bits() == 0
