@@ -154,8 +154,11 @@ def _ptr(x):
 def _stream(stream):
     if stream is None:
         import torch
-        # the handle alone: the Stream object around it costs more than a launch
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        try:
+            # the handle alone: the Stream object around it costs more than a launch
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:   # names of torch's own, which another version may not have
+            return torch.cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -315,13 +318,18 @@ def _kv_here():
         _torch = torch
     try:
         return _torch._C._cuda_getDevice()
+    except AttributeError:
+        return _torch.cuda.current_device()
     except RuntimeError:   # no GPU: every tensor is on another device
         return -2
 
 
 def _kv_stream(stream, dev):
     if stream is None and dev >= 0:
-        return _torch._C._cuda_getCurrentRawStream(dev)
+        try:
+            return _torch._C._cuda_getCurrentRawStream(dev)
+        except AttributeError:
+            pass
     return _stream(stream)
 
 

@@ -91,3 +91,19 @@ def test_addresses_and_missing_structs_go_to_the_library():
         C.csla_kv_append(None, KV, ADDR, B, ADDR, N, ADDR, HK * D, ADDR, HK * D, C.CSLA_BF16, None, 1)
     with pytest.raises(C.CslaError):
         _append(dt=7)
+
+
+def test_the_stream_without_torchs_private_names(monkeypatch):
+    class Stream:
+        cuda_stream = 123
+
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    assert C._stream(None) == 123
+    assert C._stream(7) == 7 and C._stream(Stream) == 123
+    C._kv_here()
+    assert C._kv_stream(None, 0) == 123 and C._kv_stream(7, 0) == 7
+    monkeypatch.delattr(torch._C, "_cuda_getDevice")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    assert C._kv_here() == 3 and C._kv_stream(None, 3) == 123 and C._stream(None) == 123
