@@ -52,28 +52,34 @@ def _stale():
     return any(os.path.getmtime(p) > t for p in deps)
 
 
-def _link(out, extra=(), shared=()):
-    """Compile every source (in parallel) and link them into `out`; sources outside `shared` get a whole program each."""
+def _run(cmd, verbose):
+    if verbose:
+        print(" ".join(cmd))
+    subprocess.run(cmd, check=True)
+
+
+def _link(out, extra=(), shared=(), verbose=False):
+    """Compile every source (in parallel) and link them into `out`; those in ALONE and not in `shared` as whole programs."""
     with tempfile.TemporaryDirectory(dir=PKG, prefix="_build") as d:
         def one(src):
             name = os.path.basename(src)
             obj = os.path.join(d, name + ".o")
             alone = name in ALONE and name not in shared
             mode = ["-DCSLA_UNIT_ALONE"] if alone else ["-rdc=true"]
-            subprocess.run([NVCC, *FLAGS, *extra, *mode, "-c", "-o", obj, src], check=True)
+            _run([NVCC, *FLAGS, *extra, *mode, "-c", "-o", obj, src], verbose)
             return obj
         with ThreadPoolExecutor(max_workers=os.cpu_count() or 4) as pool:
             objs = list(pool.map(one, sources()))
         tmp = out + ".tmp%d" % os.getpid()
-        subprocess.run([NVCC, *FLAGS, "-rdc=true", "-shared", "-o", tmp, *objs], check=True)
+        _run([NVCC, *FLAGS, "-rdc=true", "-shared", "-o", tmp, *objs], verbose)
         os.replace(tmp, out)
     return out
 
 
-def build(force=False, extra=()):
+def build(force=False, verbose=False, extra=()):
     if not force and not _stale():
         return LIB
-    return _link(LIB, extra)
+    return _link(LIB, extra, verbose=verbose)
 
 
 def build_timeline(out):
@@ -85,4 +91,4 @@ if __name__ == "__main__":
         print(build_timeline(os.path.abspath(sys.argv[sys.argv.index("--timeline") + 1])))
         sys.exit(0)
     extra = ["-Xptxas", "-v"] if "--ptxas-v" in sys.argv else []
-    print(build(force="--force" in sys.argv or bool(extra), extra=extra))
+    print(build(force="--force" in sys.argv or bool(extra), verbose=True, extra=extra))
