@@ -11,6 +11,10 @@ namespace csla {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.0f;   // log2 growth of a row's maximum that its sums tolerate before they are rescaled
+// A row's running maximum from its first visible token on, at least: with -inf
+// left to rows that have seen no token, one whose visible scores are all -inf
+// ends as 0 / (0 + the sink), not as a row of no tokens.
+constexpr float kLeast = -3.0e38f;
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));

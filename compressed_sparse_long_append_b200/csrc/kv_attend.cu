@@ -722,7 +722,8 @@ __device__ void softmax_role(const KvAttendArgs &a, uint8_t *smem, Misc *ms, int
                     for (int i = 2; i < 32; i += 2)
                         mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(v[c][i])), __uint_as_float(v[c][i + 1]));
                 }
-                const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc);
+                const float least = last >= 0 && from < kTile ? fmaxf(m, kLeast) : m;   // (from <= last)
+                const float mn = fmaxf(least, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc);
                 const bool grow = mn > m + kGrow;   // (also from -inf)
                 if (any) {   // P and O of the tile before
                     if (!warp_all(kv_wait(&ms->pv_done[s], s_count & 1, &ms->abort))) return;

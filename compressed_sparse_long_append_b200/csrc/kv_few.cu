@@ -324,7 +324,8 @@ __device__ __forceinline__ bool narrow_item(const KvAttendArgs &a, const Item &i
         for (int j = 1; j < kNT; ++j) mn = fmaxf(mn, fmaxf(x[j][0], x[j][1]));
         mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 1));
         mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, 2));
-        mn = fmaxf(m, mn * sc);
+        const bool some = !bad && t0 <= pos && t0 + C::kWT > low;   // the row sees a token of the warp's
+        mn = fmaxf(some ? fmaxf(m, kLeast) : m, mn * sc);
         const bool grow = mn > m + kGrow;
         if (__any_sync(0xffffffffu, grow)) {
             const float f = !grow ? 1.f : (m == -INFINITY ? 0.f : ex2(m - mn));
@@ -589,7 +590,8 @@ __device__ void consumer(const KvAttendArgs &a, uint8_t *smem, Misc *ms) {
                 for (int j = 1; j < kNT; ++j) x = fmaxf(x, fmaxf(acc[j][2 * h], acc[j][2 * h + 1]));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                mn[h] = fmaxf(m[h], x * sc);
+                const bool some = !bad && t0 <= pos[h] && t0 + C::kWT > low[h];   // the row sees a token of the warp's
+                mn[h] = fmaxf(some ? fmaxf(m[h], kLeast) : m[h], x * sc);
                 grow |= mn[h] > m[h] + kGrow;
             }
             if (__any_sync(0xffffffffu, grow)) {

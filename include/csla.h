@@ -571,7 +571,10 @@ int csla_kv_append(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
  *   s_j = scale * <qh, K_j>,  j = max(0, p - window + 1) .. p
  *   o = sum_j e^{s_j} V_j / (e^{sink[h]} + sum_j e^{s_j})   (sink NULL: no sink term)
  * From one token per request (decode) to whole prompts, mixed in one call.
- * A row whose tokens all lie in unmapped pages is written as zeros.  Cache
+ * A row whose tokens all lie in unmapped pages is written as zeros; one whose
+ * visible tokens all score -inf is 0 / 0, NaN, without a sink and zeros with
+ * one.  (An infinite element of a visible K row or of q may give NaN where the
+ * formula has a score of +-inf.)  Cache
  * rows that no new token of the request sees (positions >= len, or before
  * every window) are never used, whatever they hold, and pages of such rows
  * need not be mapped.  V of a token that some new tokens see and others do
