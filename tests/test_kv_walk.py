@@ -138,3 +138,21 @@ def test_waits_are_bounded(host, ready, stop, item, ok, took):
     assert bool(got) == ok
     assert abs(ms.value - took) <= 10
     assert (abort.value, err.value) == ((0, 0) if ok else (1, 0 if stop else C.CSLA_DEVERR_TIMEOUT))
+
+
+@pytest.mark.parametrize("D,HQ,HK,T,L,rows,parts", [
+    (128, 8, 1, 1, 40000, 8, 63),          # 313 tiles in 313 / 4 = 78 chunks at most, so of 5 tiles: more parts than a warp joins
+    (64, 16, 1, 1, 100003, 16, 87),        # 782 in 782 / 8 = 97 at most, so of 9
+    (128, 32, 8, 5, 28500, 20, 36),        # one round over the SMs: 18 chunks of 12 to 16 tiles instead of 13
+    (128, 32, 8, 20, 33000, 80, 36),
+    (128, 64, 1, 1, 230001, 64, 278),      # chunks of 13 tiles, two streams
+    (128, 64, 1, 2, 3000, 128, 2),
+    (128, 4, 4, 300, 17000, 300, 0),       # row tiles too few for the SMs: all cut (parts by row tile)
+    (128, 16, 16, 2500, 7000, 256, 0),     # more row tiles than SMs: the first one of each head cut
+    (64, 32, 16, 1300, 9000, 512, 0),      # the first two
+    (128, 32, 8, 2048, 2048, 0, 0)])       # none
+def test_how_requests_are_cut(host, D, HQ, HK, T, L, rows, parts):
+    """The plan behind the cases that the GPU tests name."""
+    w = Walk(host, DenseShape(D=D, HQ=HQ, HK=HK), [0, T], [L], T, T, L)
+    assert (w.rows_s[0], w.join[0, 2]) == (rows, parts)
+    assert w.part_rows <= w.room
