@@ -5,6 +5,7 @@
 
 #include "../../include/csla.h"
 #include "common.cuh"
+#include "kv_walk.cuh"
 #include "kernels.h"
 
 namespace {
@@ -125,15 +126,16 @@ __device__ unsigned int g_timeline_n = 0;
 
 namespace csla {
 namespace {
-// One thread waits, with the library's bounded wait, on an mbarrier that
-// expects one arrival nobody makes; the wait gives up after limit_ns and
-// records CSLA_DEVERR_TIMEOUT.
+// One thread waits, with the library's bounded waits in turn, on an mbarrier
+// that expects one arrival nobody makes; each gives up after half of limit_ns
+// and records CSLA_DEVERR_TIMEOUT.
 __global__ void __launch_bounds__(32) wait_check_kernel(uint64_t limit_ns) {
     __shared__ uint64_t bar;
     if (threadIdx.x == 0) {
         mbar_init(&bar, 1);
         fence_mbar_init();
-        mbar_wait_limit(&bar, 0, nullptr, limit_ns);
+        mbar_wait_limit(&bar, 0, nullptr, limit_ns / 2);
+        kv_wait(&bar, 0, nullptr, limit_ns / 2);
     }
 }
 }  // namespace

@@ -437,14 +437,14 @@ size_t csla_workspace_size(const csla_cfg *cfg, int32_t op, int32_t B, int32_t m
 int csla_device_error(csla_stream_t stream, uint32_t *bits);
 
 /*
- * csla_check_wait_timeout -- exercise of the failure path every kernel's
- * bounded waits share (the pages have no counterpart: an operational check).
- * Launches one CTA on `stream` whose thread waits, with the library's own
- * bounded mbarrier wait, on a barrier that nobody arrives at, for at most
- * limit_us microseconds (1 .. 2000000); the wait gives up, sets
- * CSLA_DEVERR_TIMEOUT in the device error word and the kernel returns, so
- * csla_device_error() afterwards reports CSLA_ERR_DEVICE with that bit and
- * the context stays usable.  (The kernels' own waits give up after 2 s, the
+ * csla_check_wait_timeout -- exercise of the failure path of every kernel's
+ * bounded waits (the pages have no counterpart: an operational check).
+ * Launches one CTA on `stream` whose thread waits on a barrier that nobody
+ * arrives at, with the library's two bounded mbarrier waits in turn (the dense
+ * attention's polls), for at most limit_us microseconds (1 .. 2000000) in all;
+ * both give up and set CSLA_DEVERR_TIMEOUT in the device error word, and the
+ * kernel returns, so csla_device_error() afterwards reports CSLA_ERR_DEVICE
+ * with that bit and the context stays usable.  (The kernels' own waits give up after 2 s, the
  * dense attention's for the end of a long row tile after 16 s.)
  * Errors: CSLA_ERR_ARG for a limit outside the range; CSLA_ERR_CUDA if the
  * launch fails.

@@ -95,3 +95,18 @@ def test_other_types_and_layouts_on_the_device():
         b.attend(F32, ws=torch.empty(need - 1, dtype=torch.uint8, device=DEV))
     assert torch.equal(b.attend(F32), want)
     assert _bits() == 0
+
+
+def test_both_bounded_waits_run_out():
+    """100 ms, half for each of the library's two waits; the context stays usable."""
+    b = Batch(DenseShape(D=64, HQ=4, HK=2, d_rope=64), [1, 40], [300, 400], seed=72)
+    b.fill()
+    want = b.attend(F32)
+    assert _bits() == 0
+    a, z = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    a.record()
+    C.csla_check_wait_timeout(100000)
+    z.record()
+    assert C.csla_device_error() == (C.CSLA_ERR_DEVICE, C.CSLA_DEVERR_TIMEOUT)
+    assert 100 <= a.elapsed_time(z) < 1000
+    assert torch.equal(b.attend(F32), want) and _bits() == 0
