@@ -872,11 +872,11 @@ int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
     if (more && (!encode_bf16_2d(&more_k, kv->k, cfg->D, cache_rows, CSLA_PAGE_TOKENS) ||
                  !encode_bf16_2d(&more_v, kv->v, cfg->D, cache_rows, CSLA_PAGE_TOKENS)))
         return CSLA_ERR_CUDA;
-    // Requests of both kinds: the two kernels write rows of their own (and the
-    // same entries for the join), so they run side by side on two streams: 12
-    // requests of 1 to 1500 tokens 67 us, one after the other 84; 64 decoding
-    // requests and a chunk of 512 tokens 409 us, with kv_attend_kernel first 413,
-    // one after the other 467.
+    // Requests of both kinds: the two kernels write rows of their own (the join's
+    // entries are kv_attend_kernel's then), so they run side by side on two
+    // streams: 12 requests of 1 to 1500 tokens 67 us, one after the other 84; 64
+    // decoding requests and a chunk of 512 tokens 409 us, with kv_attend_kernel
+    // first 413, one after the other 467.
     SideStream *side = few && more ? side_stream_for(st) : nullptr;
     cudaError_t e = cudaSuccess, ej = cudaSuccess;
     if (side) {
@@ -886,7 +886,9 @@ int csla_kv_attend(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
     }
     if (few) {
         const long long m = kv_min_tiles(kKvFew, cfg->D, 1);
-        e = launch_kv_few(a, q16, o16, few_k, few_v, num_sms_current(), (long long)B * cfg->HK * ((nt + m - 1) / m), st);
+        KvAttendArgs f = a;
+        if (more) f.part_req = nullptr;
+        e = launch_kv_few(f, q16, o16, few_k, few_v, num_sms_current(), (long long)B * cfg->HK * ((nt + m - 1) / m), st);
     }
     if (e == cudaSuccess && more) {
         const long long m = kv_min_tiles(kKvSingle, cfg->D, 1);

@@ -143,7 +143,7 @@ struct KvWalk {
             part_excl = pincl - parts;
             total = __shfl_sync(0xffffffffu, incl, 31);
             part_total = __shfl_sync(0xffffffffu, pincl, 31);
-            // (every attention kernel of the call writes the same)
+            // the join's entries, whatever the requests' kinds
             if (a.part_req && blockIdx.x == 0 && b < a.bt.B) {
                 const int same = p.kind != kKvPaired && parts ? kv_parts(p, kv_range(p, r.L - r.T, 0, a.window), 0) : 0;
                 a.part_req[b] = KvJoin{r.n0, parts && same != 1 ? p.rows_s : 0, same, r.T, r.L, 0, part_before + part_excl};
