@@ -282,7 +282,8 @@ struct KvSmemOnce {
 // RoPE frequencies theta^(-2i/d_rope) of a dense layer (d_rope up to 128) as
 // turns per position, in units of 2^-64 turn: position times frequency
 // modulo one turn is then one 64-bit integer product, exact in the product and
-// off by less than pos * 2^-65 turns from the frequency's rounding.
+// off by less than pos * 2^-57 turns from the frequency's (64 products of
+// extended precision, then cut to a whole number of units).
 struct KvFreq {
     unsigned long long turn[64];
 };
@@ -339,8 +340,9 @@ struct KvAttendArgs {
     long long q_stride;
     const float *sink, *gamma_q;    // null: none
     void *out;
-    // workspace: first partial row of each request [B], (m, l) and O of the partial rows
-    KvJoin *part_req;   // [B], what the join needs of a request
+    // workspace: what the join needs of each request [B] (null: another kernel of
+    // the call writes it), (m, l) and O of the partial rows
+    KvJoin *part_req;
     float2 *part_ml;
     float *part_o;
 };
@@ -368,8 +370,12 @@ constexpr int kKvFewRows = 16;
 //          but 2 in a context of up to 8 (one user, 901 tokens, 8 heads: 13.5 us,
 //          with 4 pages 15.5); 8 of 64 dims (32 requests, window of 9 pages, 16
 //          heads: 31.7 us whole, 36 in two);
-//   single 16 (32 requests of 20 rows: 144 us, with 8 tiles 166);
-//   paired 8, and only when the row tiles do not fill the SMs.
+//   single 16 (32 requests of 20 rows: 144 us, with 8 tiles 166), or 12 where
+//          half of the items then have 12 to 16 tiles each (a lone request in one
+//          round over the SMs: 64 rows of one KV head over 262144 tokens, 147
+//          chunks of 14 tiles instead of 128 of 16);
+//   paired 8 where the row tiles do not fill the SMs; where they do, only those
+//          left over from full rounds are cut, in up to four (kv_plan).
 __host__ __device__ constexpr int kv_units(int kind) { return kind == kKvPaired ? 148 : 296; }
 __host__ __device__ constexpr int kv_min_tiles(int kind, int D, int nt) {
     return kind == kKvFew ? (D == 64 ? 8 : (nt <= 8 ? 2 : 4)) : (kind == kKvSingle ? 16 : 8);

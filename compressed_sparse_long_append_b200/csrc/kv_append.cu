@@ -12,11 +12,12 @@
 // The bytes bound a long call (each row read once and written once) and leave
 // about 170 instructions per warp for two rows, so a thread's (token, head) is
 // carried from row to row, not divided out: 8192 tokens of 8 heads x 128 take
-// 16.0 us for 67 MB, 4.2 TB/s or 0.64 of a plain copy's rate, with instruction issue
-// 64 % busy (norm and rotation) and one round of blocks, whose start and end
+// 15.9 us for 67 MB, 4.2 TB/s or 0.64 of a plain copy's rate, with instruction issue
+// 62 % busy (norm and rotation) and one round of blocks, whose start and end
 // are not overlapped by another.  Short calls are bound by the
 // chain offsets -> slot -> length -> page, which runs while the first rows'
-// loads are in flight, and by the call itself on the host (about 7 us).
+// loads are in flight (8 tokens: 2.9 us in a graph), and by the call itself on
+// the host (7.5 us).
 #include <limits.h>
 
 #include "kv.cuh"

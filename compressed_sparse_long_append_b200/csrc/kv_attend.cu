@@ -52,9 +52,9 @@
 // of what one large library product measures in a burst; at that length the
 // clock falls to about 1.4 GHz under the power limit.  2048 tokens alone: 57 us
 // (0.37; 256 items of 1 to 16 tiles on 148 SMs).  One chunk of 17 to 128
-// rows waits for its chain of S, softmax and P V: 32 requests of 20 rows 138 us for
-// 526 MB (3.8 TB/s), 4 requests of 64 rows on one KV head over 262144
-// tokens 150 us for 537 MB (3.6 TB/s); with the pages in L2 they take as long:
+// rows waits for its chain of S, softmax and P V: 32 requests of 20 rows 132 us for
+// 526 MB (4.0 TB/s), 4 requests of 64 rows on one KV head over 262144
+// tokens 149 us for 537 MB (3.6 TB/s); with the pages in L2 they take as long:
 // 2350 clocks per tile and some 12 000 per item, between its last product and
 // the next item's first.
 #include "kv.cuh"
@@ -936,9 +936,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attend_kernel(const __grid_con
 // requests of 16384 tokens and 32 heads, 10.0 us beside 94 us of attention.
 constexpr int kJoinWarps = 8, kJoinFew = 32;
 
-// o += sum of 2^(m_i - top) O_i over parts [i0, i1), (m, l) of part i0 + i in
-// lane i's ml (i1 - i0 <= 32).  The parts' loads are issued eight at a time,
-// ahead of their weights.
+// o += sum of w_i O_i over n <= 32 parts `step` rows apart from row pr on, with
+// w_i = 2^(m_i - top) in lane i's w.  The parts' loads are issued eight at a
+// time, ahead of their weights.
 template <int D>
 __device__ __forceinline__ void join_parts(const float *part_o, long long pr, long long step, int n, float w, float (&o)[D / 32]) {
     constexpr int kDims = D / 32;

@@ -22,12 +22,13 @@
 // when the request's keys were cut.
 //
 // Measured (8 KV heads of 128 dims, 4 or 8 query heads each, join included): 8
-// requests of 131072 tokens 636 us for 4.29 GB, 6.75 TB/s or 1.03 of a plain
-// copy's rate (which writes half of its bytes); 64 ragged requests of 1 to
+// requests of 131072 tokens 636 to 656 us for 4.29 GB (boxes differ), 6.75 to
+// 6.55 TB/s or 1.03 to 1.00 of a plain copy's rate (which writes half of its
+// bytes); 64 ragged requests of 1 to
 // 32768 tokens 134 us for 757 MB (5.6 TB/s: the last items' latency and the
 // join); a window of 1000 in 32 requests (64 dims, 16 KV heads) 31.6 us for
-// 131 MB.  One request of 901 tokens: 11.5 us, a chain of two launches and one
-// item's latency.  The same items in the tensor-memory kernel took 1.17 ms, 156
+// 131 MB.  One request of 901 tokens: 11.7 us, 10.6 in a graph, a chain of two
+// launches and one item's latency.  The same items in the tensor-memory kernel took 1.17 ms, 156
 // us and 47 us; with rows as rows only (no narrow_item) 657 us, 141 us and 36 us.
 #include "kv.cuh"
 

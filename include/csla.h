@@ -584,6 +584,12 @@ int csla_kv_append(const csla_kv_cfg *cfg, const csla_kv_cache *kv, const int32_
  *   max_new >= every T_b, max_len >= every len (host bounds; max_len <= 2^27).
  * Batch invariant: how a request is split and joined is a function of its
  * own T_b and len and of the layer's shape.
+ * Precision, also with q and out in f32: K and V are bf16 as they lie in the
+ * pages; norm, rotation (angles exact to 2^-32 turn, sine and cosine to 2^-20),
+ * scores, maxima, sums and partial results are f32; each weight e^{s_j} is
+ * rounded to bf16 where it multiplies V (the denominator sums the unrounded ones);
+ * the rotated qh enters its products as two bf16 terms (2^-16), but as one (2^-8)
+ * in requests of more than 128 rows (T_b * HQ / HK) with D = 128.
  * workspace: csla_kv_workspace_size(cfg, B, N, max_new, max_len) bytes,
  * 16-byte aligned, not shared with a call that may run at the same time.
  * A call whose requests may have up to 16 rows (T_b * HQ / HK) as well as more
