@@ -549,9 +549,9 @@ static int side_stream(SideStream **out) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CSLA_ERR_CUDA;
     SideStream &x = tl_side[dev];
-    if (!x.s) {
-        if (cudaStreamCreateWithFlags(&x.s, cudaStreamNonBlocking) != cudaSuccess ||
-            cudaEventCreateWithFlags(&x.fork, cudaEventDisableTiming) != cudaSuccess ||
+    if (!x.join) {   // (the last of the three: a call that failed half way is made up for)
+        if ((!x.s && cudaStreamCreateWithFlags(&x.s, cudaStreamNonBlocking) != cudaSuccess) ||
+            (!x.fork && cudaEventCreateWithFlags(&x.fork, cudaEventDisableTiming) != cudaSuccess) ||
             cudaEventCreateWithFlags(&x.join, cudaEventDisableTiming) != cudaSuccess)
             return CSLA_ERR_CUDA;
     }
@@ -568,13 +568,17 @@ static SideStream *side_stream_for(cudaStream_t stream) {
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone, side = cudaStreamCaptureStatusNone;
     unsigned long long id = 0, side_id = 0;
     SideStream *x = nullptr;
-    if (cudaStreamGetCaptureInfo(stream, &cs, &id) == cudaSuccess && cudaGetDevice(&dev) == cudaSuccess && dev >= 0 &&
-        dev < 64 && (cs == cudaStreamCaptureStatusNone || tl_side[dev].s) && side_stream(&x) == CSLA_OK &&
-        cudaStreamGetCaptureInfo(x->s, &side, &side_id) == cudaSuccess &&
-        (side == cudaStreamCaptureStatusNone || (side == cs && side_id == id)))
-        return x;
-    cudaGetLastError();   // (nothing failed that the call needs)
-    return nullptr;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+    if (cudaStreamGetCaptureInfo(stream, &cs, &id) != cudaSuccess) {
+        cudaGetLastError();   // (nothing failed that the call needs)
+        return nullptr;
+    }
+    if (cs != cudaStreamCaptureStatusNone && !tl_side[dev].join) return nullptr;
+    if (side_stream(&x) != CSLA_OK || cudaStreamGetCaptureInfo(x->s, &side, &side_id) != cudaSuccess) {
+        cudaGetLastError();
+        return nullptr;
+    }
+    return side == cudaStreamCaptureStatusNone || (side == cs && side_id == id) ? x : nullptr;
 }
 
 int csla_csa_decode_step(const csla_cfg *cfg, const csla_state *st, const csla_cache *cache, const int32_t *slots,
